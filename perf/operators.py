@@ -626,8 +626,6 @@ def _prepare_logprobs(case, seed):
     if own:
         import ragged_mixed_paged_gb300 as rb
 
-        s["workspace"] = torch.empty(rb.logprobs_workspace_size(rows, vocab, case["top"]),
-                                     dtype=torch.uint8, device="cuda")
         s["out"] = rb.TokenLogprobs.allocate(rows, case["top"], "cuda")
         s["error"] = torch.zeros(1, dtype=torch.int32, device="cuda")
     return s
@@ -639,7 +637,7 @@ def _run_logprobs(s):
         import ragged_mixed_paged_gb300 as rb
 
         o = rb.token_logprobs(s["logits"], s["tokens"], top, out=s["out"],
-                              workspace=s["workspace"], error_word=s["error"])
+                              error_word=s["error"])
         return o.logprobs, o.ranks, o.entropy, o.top_ids, o.top_logprobs
     vocab = s["case"]["vocab"]
     step = max(1, (1 << 28) // vocab)
