@@ -17,6 +17,13 @@
  *
  *   rb_batch_apply_update  remove, append, install and condense rows on the device
  *
+ * Beside the step:
+ *
+ *   rb_pages_*         reference counts of the cache's pages; copying pages, forking rows of the
+ *                      page table (shared full pages, the partial page copied), freeing rows and
+ *                      compacting the live pages
+ *   rb_token_logprobs  log probability and rank of given tokens, entropy, top alternatives
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - Every pointer named d_* is DEVICE memory on the current CUDA device; the caller owns it,
@@ -76,6 +83,17 @@ typedef enum rb_status {
                                        entry != num_tokens, seq_len < query length, or seq_len
                                        beyond max_blocks_per_req pages */
 #define RB_EBIT_TIMEOUT 0x100       /* a bounded wait on an asynchronous copy gave up */
+#define RB_EBIT_ROW 0x800           /* rb_pages_*: a row outside the table, a row's page count
+                                       outside [0, max_blocks_per_req], a fork into a row that
+                                       holds pages, is named twice or is its own source, or from
+                                       a row that holds fewer pages than its cached tokens need */
+#define RB_EBIT_PAGE_PAIR 0x1000    /* rb_pages_copy: a page is the destination of two pairs, or
+                                       both a source and a destination */
+#define RB_EBIT_PAGE_REF 0x2000     /* rb_pages_*: a freed page whose reference count is below
+                                       one, or a negative count */
+#define RB_EBIT_NO_PAGE 0x4000      /* rb_pages_fork: too few free pages */
+#define RB_EBIT_TOKEN_ID 0x8000     /* rb_token_logprobs: token id below -1 or >= vocab_size */
+#define RB_EBIT_LOGITS 0x10000      /* rb_token_logprobs: a row holds NaN or +inf */
 
 /* Static sizes of the persistent batch and of one layer's paged KV pool. */
 typedef struct rb_dims {
@@ -544,6 +562,128 @@ rb_status rb_batch_apply_update(const rb_batch* batch, const rb_batch_update* up
                                 int32_t* d_num_scheduled, int32_t* d_row_of_sched,
                                 void* d_workspace, size_t workspace_bytes,
                                 int32_t* d_error_word, void* stream);
+
+/*
+ * Page tables with reference counts — the page columns of a persistent batch (rb_batch's
+ * d_block_table and d_num_blocks, or any table of that layout) and, for every page-table entry
+ * id, how many rows hold that page (0: free).  A "page" of the rb_pages_* calls is what one
+ * entry names: a kernel page of block_size tokens, or a manager block of r * block_size
+ * (kernel_blocks_per_manager_block); E = num_blocks / r of them, the reserved one (that holds
+ * null_block) neither live nor free.  Rows outside [0, num_rows) and entries past a row's count
+ * are not read or written.  The caches are those of rb_kv_write; a token's row
+ * (2 * nkv * head_dim bytes) must be a multiple of 16 bytes and the bases 16-byte aligned.
+ */
+typedef struct rb_page_tables {
+  int32_t num_rows;        /* rows of the tables (<= max_num_reqs) */
+  int32_t reserved;        /* 0 */
+  int32_t* d_block_table;  /* [num_rows, max_blocks_per_req] page ids of each row */
+  int32_t* d_num_blocks;   /* [num_rows] valid entries of each row */
+  int32_t* d_ref_count;    /* [E] rows that hold each page */
+} rb_page_tables;
+
+/* Workspace bytes of the rb_pages_* calls (0 for invalid dims): caller-owned device memory, 256-
+   byte aligned, scratch without initialisation; calls that may overlap need one each. */
+size_t rb_pages_workspace_size(const rb_dims* dims);
+
+/*
+ * rb_pages_count — d_ref_count from the tables: the number of rows [0, num_rows) that hold each
+ * page (a page twice in one row counts twice).  Enqueues one memset and one launch.
+ * Errors: host -> RB_ERR_INVALID_ARG, RB_ERR_CAPACITY (num_rows > max_num_reqs); device -> bits
+ * ROW (the row is skipped), BLOCK_ID (the entry is skipped).
+ */
+rb_status rb_pages_count(const rb_dims* dims, const rb_page_tables* tables,
+                         int32_t* d_error_word, void* stream);
+
+/*
+ * rb_pages_copy — K and V of page d_src[i] to page d_dst[i], i < num_pairs, whole pages.  A
+ * source may be named many times; a pair with a negative id is skipped.  One launch; CTA 0 checks the
+ * pairs meanwhile.
+ * Errors: host -> RB_ERR_INVALID_ARG, RB_ERR_CAPACITY (num_pairs > E, small workspace),
+ * RB_ERR_UNSUPPORTED (token row not a multiple of 16 bytes); device -> BLOCK_ID (id outside the
+ * pool or the reserved page: the pair is skipped), PAGE_PAIR (a page is the destination of two pairs
+ * or source and destination: the contents of those destinations are unspecified).
+ */
+rb_status rb_pages_copy(const rb_dims* dims, int32_t num_pairs, const int32_t* d_src,
+                        const int32_t* d_dst, void* d_k_cache, void* d_v_cache,
+                        void* d_workspace, size_t workspace_bytes, int32_t* d_error_word,
+                        void* stream);
+
+/*
+ * rb_pages_fork — row d_dst_rows[i] becomes a copy of row d_src_rows[i] of the page table, i <
+ * num_forks (<= num_rows), with c = d_num_cached[d_src_rows[i]] cached tokens ([num_rows], for
+ * example rb_batch's d_num_computed): the c / page full pages are shared (their counts rise by
+ * one); if c ends inside a page, the row gets the lowest free page for it (forks in list
+ * order, free pages in ascending order) and the c % page tokens' K and V are copied there.
+ * d_num_blocks of the new row is ceil(c / page).  Pages the source holds beyond its cached
+ * tokens are not shared.  A source may be forked many times; a destination must hold no page.
+ * Errors: host -> RB_ERR_INVALID_ARG, RB_ERR_CAPACITY, RB_ERR_UNSUPPORTED; device -> ROW and
+ * NO_PAGE, and then nothing is changed; BLOCK_ID (an entry outside the pool or the reserved
+ * page: not counted or copied).
+ */
+rb_status rb_pages_fork(const rb_dims* dims, const rb_page_tables* tables, int32_t num_forks,
+                        const int32_t* d_src_rows, const int32_t* d_dst_rows,
+                        const int32_t* d_num_cached, void* d_k_cache, void* d_v_cache,
+                        void* d_workspace, size_t workspace_bytes, int32_t* d_error_word,
+                        void* stream);
+
+/*
+ * rb_pages_free — the pages of rows d_rows[i], i < num_free, lose one holder each; the rows'
+ * valid entries become -1 and their counts 0.  A row that holds nothing (or is named again)
+ * frees nothing.  d_num_freed (or NULL) receives the number of pages that became free.
+ * The contents of the pages are left as they are.
+ * Errors: host -> RB_ERR_INVALID_ARG, RB_ERR_CAPACITY; device -> ROW (the row is skipped),
+ * BLOCK_ID (the entry is skipped), PAGE_REF (a page nobody held: its count stays).
+ */
+rb_status rb_pages_free(const rb_dims* dims, const rb_page_tables* tables, int32_t num_free,
+                        const int32_t* d_rows, int32_t* d_num_freed, int32_t* d_error_word,
+                        void* stream);
+
+/*
+ * rb_pages_compact — moves the L live pages (count > 0) into the L lowest ids other than the
+ * reserved page: pages already there stay, the others, in ascending order, go to the free ids there,
+ * in ascending order.  K and V of the moved pages are copied, d_ref_count and every row's
+ * valid entries follow.
+ * Outputs: d_page_map [E] (or NULL): the new id of each live page, -1 for a free one, the
+ * reserved page's own id; d_num_live [1] (or NULL): L.
+ * Errors: host -> RB_ERR_INVALID_ARG, RB_ERR_CAPACITY, RB_ERR_UNSUPPORTED; device -> ROW (the
+ * row is skipped), BLOCK_ID (an entry outside the pool, the reserved page or a page with count
+ * 0: left as it is), PAGE_REF (a negative count: taken as free).
+ */
+rb_status rb_pages_compact(const rb_dims* dims, const rb_page_tables* tables,
+                           int32_t* d_page_map, int32_t* d_num_live, void* d_k_cache,
+                           void* d_v_cache, void* d_workspace, size_t workspace_bytes,
+                           int32_t* d_error_word, void* stream);
+
+/* Element types of rb_token_logprobs's logits. */
+typedef enum rb_dtype { RB_BF16 = 0, RB_FP16 = 1, RB_FP32 = 2 } rb_dtype;
+
+/*
+ * rb_token_logprobs — for each of num_rows rows of logits: the log probability and the rank of
+ * one token, the entropy of the row's distribution and its top_k most likely tokens.  The rows
+ * are those the LM head computes from rb_gather_rows's output (or of every prompt token).
+ *   log p_i = x_i - ln sum_j exp(x_j);  rank(t) = 1 + #{i : x_i > x_t};  H = -sum p_i ln p_i
+ * (natural logarithms).
+ *
+ *   d_logits       [num_rows, vocab_size] of logits_dtype (rb_dtype), element-aligned; row r
+ *                  starts row_stride elements after row r - 1 (row_stride >= vocab_size)
+ *   d_token_ids    [num_rows] int32, or NULL (then d_logprobs and d_ranks are NULL); -1: no
+ *                  token is asked for (log probability 0, rank 0)
+ *   top_k          0 .. 32; the tokens with the largest logits, equal logits by ascending id;
+ *                  entries past vocab_size get id -1 and -inf
+ *   d_logprobs, d_ranks, d_entropy  [num_rows] or NULL
+ *   d_top_ids, d_top_logprobs       [num_rows, top_k] (ignored for top_k = 0)
+ * A logit of -inf has probability 0 (log probability -inf); a row of nothing but -inf gives
+ * log probabilities of -inf and entropy 0.  A row with NaN or +inf has no distribution: bit
+ * LOGITS, floating outputs NaN, rank 0 and ids -1.  Sums are fp32 around a running reference.
+ * Errors: host -> RB_ERR_INVALID_ARG, RB_ERR_UNSUPPORTED (top_k > 32, another type, vocab_size
+ * > 2^30), RB_ERR_CAPACITY (num_rows > 2^28 - 1); device -> LOGITS, and TOKEN_ID (an id below
+ * -1 or >= vocab_size: as -1).
+ */
+rb_status rb_token_logprobs(int32_t num_rows, int32_t vocab_size, int64_t row_stride,
+                            int32_t logits_dtype, const void* d_logits,
+                            const int32_t* d_token_ids, int32_t top_k, float* d_logprobs,
+                            int32_t* d_ranks, float* d_entropy, int32_t* d_top_ids,
+                            float* d_top_logprobs, int32_t* d_error_word, void* stream);
 
 #ifdef __cplusplus
 }

@@ -9,6 +9,8 @@
     gather_rows      hidden rows at logits_indices
     PersistentBatch  device-resident rows of the resident requests; ``apply`` merges one
                      step's scheduler output (remove, append, install, condense) on the GPU
+    PagePool         reference counts of the cache's pages: copy, fork, free, compact
+    token_logprobs   log probability and rank of given tokens, entropy, top alternatives
     pad_for_graph    smallest captured graph size >= the token count
 
 All compute runs in the library's sm_103a kernels; tensors are caller-owned CUDA tensors.
@@ -19,11 +21,15 @@ from ._binding import (Dims, RbError, EBIT_ATTN_META, EBIT_BLOCK_ID, EBIT_NUM_CO
                        pad_for_graph, paged_attention, prepare_inputs, status_string,
                        workspace_size, cascade_prefix_len, cascade_workspace_size,
                        paged_attention_cascade)
-from ._binding import EBIT_BATCH_ID, EBIT_BATCH_SIZE
+from ._binding import (EBIT_BATCH_ID, EBIT_BATCH_SIZE, EBIT_LOGITS, EBIT_NO_PAGE,
+                       EBIT_PAGE_PAIR, EBIT_PAGE_REF, EBIT_ROW, EBIT_TOKEN_ID)
+from .logprobs import MAX_TOP_LOGPROBS, TokenLogprobs, token_logprobs
+from .pages import PagePool, pages_workspace_size
 from .persistent_batch import PersistentBatch, batch_workspace_size
 from .step import StepBuffers, run_step, run_step_fused, run_step_host, run_step_host_async
 
 __all__ = ["Dims", "RbError", "gather_rows", "kv_write", "launch_count", "lib", "pad_for_graph",
            "paged_attention", "prepare_inputs", "status_string", "workspace_size", "StepBuffers",
            "run_step", "run_step_fused", "run_step_host", "run_step_host_async", "LIB_PATH", "PersistentBatch", "batch_workspace_size",
-           "cascade_prefix_len", "cascade_workspace_size", "paged_attention_cascade"]
+           "cascade_prefix_len", "cascade_workspace_size", "paged_attention_cascade", "PagePool",
+           "pages_workspace_size", "TokenLogprobs", "token_logprobs", "MAX_TOP_LOGPROBS"]

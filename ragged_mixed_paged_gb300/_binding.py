@@ -32,6 +32,12 @@ EBIT_ATTN_META = 0x080
 EBIT_TIMEOUT = 0x100
 EBIT_BATCH_ID = 0x200
 EBIT_BATCH_SIZE = 0x400
+EBIT_ROW = 0x800
+EBIT_PAGE_PAIR = 0x1000
+EBIT_PAGE_REF = 0x2000
+EBIT_NO_PAGE = 0x4000
+EBIT_TOKEN_ID = 0x8000
+EBIT_LOGITS = 0x10000
 
 
 class RbError(RuntimeError):
@@ -65,6 +71,11 @@ class rb_batch_update(ctypes.Structure):
             "d_cached_blocks")]
 
 
+class rb_page_tables(ctypes.Structure):
+    _fields_ = [("num_rows", ctypes.c_int32), ("reserved", ctypes.c_int32)] + [
+        (n, ctypes.c_void_p) for n in ("d_block_table", "d_num_blocks", "d_ref_count")]
+
+
 class rb_host_copy(ctypes.Structure):
     _fields_ = [("dst", ctypes.c_void_p), ("src", ctypes.c_void_p), ("bytes", ctypes.c_size_t)]
 
@@ -93,6 +104,7 @@ def _load():
     P = ctypes.c_void_p
     I32 = ctypes.c_int32
     PD = ctypes.POINTER(rb_dims)
+    PT = ctypes.POINTER(rb_page_tables)
     sig = {
         "rb_status_string": (ctypes.c_char_p, [I32]),
         "rb_kernel_launch_count": (ctypes.c_uint64, []),
@@ -122,6 +134,14 @@ def _load():
                                              ctypes.c_float, P, P, ctypes.c_size_t, P, P]),
         "rb_batch_apply_update": (I32, [ctypes.POINTER(rb_batch), ctypes.POINTER(rb_batch_update),
                                         P, P, P, ctypes.c_size_t, P, P]),
+        "rb_pages_workspace_size": (ctypes.c_size_t, [PD]),
+        "rb_pages_count": (I32, [PD, PT, P, P]),
+        "rb_pages_copy": (I32, [PD, I32, P, P, P, P, P, ctypes.c_size_t, P, P]),
+        "rb_pages_fork": (I32, [PD, PT, I32, P, P, P, P, P, P, ctypes.c_size_t, P, P]),
+        "rb_pages_free": (I32, [PD, PT, I32, P, P, P, P]),
+        "rb_pages_compact": (I32, [PD, PT, P, P, P, P, P, ctypes.c_size_t, P, P]),
+        "rb_token_logprobs": (I32, [I32, I32, ctypes.c_int64, I32, P, P, I32, P, P, P, P, P, P,
+                                    P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -183,6 +203,20 @@ def _stream(stream) -> ctypes.c_void_p:
 
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _stream_on(device, stream) -> ctypes.c_void_p:
+    """The stream to launch on for tensors of ``device``, which must be the current one."""
+    import torch
+
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    elif stream.device != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors are on {device}")
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def launch_count() -> int:
