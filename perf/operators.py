@@ -236,7 +236,7 @@ def _prepare_attention(case, seed):
                             max_blocks_per_req=width, num_blocks=num_pages)
         s["rules"] = rb.ScoreRules(softcap=case["softcap"], head_slopes=s["slopes"],
                                    key_start=s["starts"], prefix_lens=s["prefix"])
-        s["workspace"] = torch.empty(rb.scored_workspace_size(s["dims"], len(reqs), tokens),
+        s["workspace"] = torch.empty(rb.workspace_size(s["dims"], len(reqs), tokens),
                                      dtype=torch.uint8, device="cuda")
         s["out"] = torch.empty_like(s["q"])
         s["error"] = torch.zeros(1, dtype=torch.int32, device="cuda")
