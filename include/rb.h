@@ -19,6 +19,8 @@
  *
  * Beside the step:
  *
+ *   rb_paged_attention_scored  attention with capped scores, a distance bias, packed documents,
+ *                      windows and bidirectional prefixes
  *   rb_pages_*         reference counts of the cache's pages; copying pages, forking rows of the
  *                      page table (shared full pages, the partial page copied), freeing rows and
  *                      compacting the live pages
@@ -246,6 +248,45 @@ rb_status rb_paged_attention(const rb_dims* dims, int32_t num_reqs, int32_t num_
                              const int32_t* d_query_start_loc, const int32_t* d_seq_lens,
                              float softmax_scale, void* d_out, void* d_workspace,
                              size_t workspace_bytes, int32_t* d_error_word, void* stream);
+
+/*
+ * Score rules of rb_paged_attention_scored, all optional, applied in this order to the score of
+ * query head h at position p and key k of the same request:
+ *   s = softmax_scale * q . k
+ *   softcap > 0:           s = softcap * tanh(s / softcap)
+ *   d_head_slopes [nh]:    s = s - slope_h * |p - k|   (fp32, in score units; any sign)
+ *   visible keys:          key_start <= k < min(seq_len, max(p + 1, prefix_len))
+ * d_key_start [num_tokens] is the first key each query token may see (its document's first
+ * position for packed documents, p - w + 1 for a window of w keys; negative: 0; NULL: 0);
+ * d_prefix_lens [num_reqs] is how many of a request's first keys all its queries see, also
+ * those before them (a bidirectional prefix; negative: 0; beyond seq_len: seq_len; NULL: 0).
+ */
+typedef struct rb_score_rules {
+  float softcap;     /* 0: none; finite and >= 0 */
+  int32_t reserved;  /* 0 */
+  const float* d_head_slopes;
+  const int32_t* d_key_start;
+  const int32_t* d_prefix_lens;
+} rb_score_rules;
+
+/*
+ * rb_paged_attention_scored — rb_paged_attention with score rules: softmax over each query's
+ * visible keys of the ruled scores.  A query that sees no key gets a row of zeros.
+ * Arguments, layouts, workspace (rb_paged_attention_workspace_size), supported shapes and
+ * errors are those of rb_paged_attention; RB_ERR_INVALID_ARG also for NULL rules, a nonzero
+ * `reserved`, and a softcap that is negative, not finite, or so small that softmax_scale /
+ * softcap overflows.
+ * Pages that no query of the request sees are not read and their page-table entries are not
+ * checked (a window's old pages may be gone), and the rows of such keys may hold anything.
+ */
+rb_status rb_paged_attention_scored(const rb_dims* dims, int32_t num_reqs, int32_t num_tokens,
+                                    int32_t num_tokens_padded, const void* d_q,
+                                    const void* d_k_cache, const void* d_v_cache,
+                                    const int32_t* d_block_table,
+                                    const int32_t* d_query_start_loc, const int32_t* d_seq_lens,
+                                    float softmax_scale, const rb_score_rules* rules,
+                                    void* d_out, void* d_workspace, size_t workspace_bytes,
+                                    int32_t* d_error_word, void* stream);
 
 /*
  * rb_paged_attention_profiled — rb_paged_attention that also records caller-created CUDA events

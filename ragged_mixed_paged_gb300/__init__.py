@@ -6,6 +6,8 @@
     paged_attention  varlen causal GQA attention through the page table
     paged_attention_cascade  the same when all requests share a prefix (read once), with
                      cascade_prefix_len giving the usable prefix length
+    paged_attention_scored  the same with score rules (ScoreRules): capped scores, a distance
+                     bias, packed documents and windows, bidirectional prefixes
     gather_rows      hidden rows at logits_indices
     PersistentBatch  device-resident rows of the resident requests; ``apply`` merges one
                      step's scheduler output (remove, append, install, condense) on the GPU
@@ -20,7 +22,7 @@ from ._binding import (Dims, RbError, EBIT_ATTN_META, EBIT_BLOCK_ID, EBIT_NUM_CO
                        EBIT_TOKEN_SUM, LIB_PATH, gather_rows, kv_write, launch_count, lib,
                        pad_for_graph, paged_attention, prepare_inputs, status_string,
                        workspace_size, cascade_prefix_len, cascade_workspace_size,
-                       paged_attention_cascade)
+                       paged_attention_cascade, ScoreRules, paged_attention_scored)
 from ._binding import (EBIT_BATCH_ID, EBIT_BATCH_SIZE, EBIT_LOGITS, EBIT_NO_PAGE,
                        EBIT_PAGE_PAIR, EBIT_PAGE_REF, EBIT_ROW, EBIT_TOKEN_ID)
 from .logprobs import MAX_TOP_LOGPROBS, TokenLogprobs, token_logprobs
@@ -31,5 +33,6 @@ from .step import StepBuffers, run_step, run_step_fused, run_step_host, run_step
 __all__ = ["Dims", "RbError", "gather_rows", "kv_write", "launch_count", "lib", "pad_for_graph",
            "paged_attention", "prepare_inputs", "status_string", "workspace_size", "StepBuffers",
            "run_step", "run_step_fused", "run_step_host", "run_step_host_async", "LIB_PATH", "PersistentBatch", "batch_workspace_size",
-           "cascade_prefix_len", "cascade_workspace_size", "paged_attention_cascade", "PagePool",
+           "cascade_prefix_len", "cascade_workspace_size", "paged_attention_cascade", "ScoreRules",
+           "paged_attention_scored", "PagePool",
            "pages_workspace_size", "TokenLogprobs", "token_logprobs", "MAX_TOP_LOGPROBS"]

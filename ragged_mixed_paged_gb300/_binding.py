@@ -11,7 +11,7 @@ import ctypes
 import math
 import os
 from dataclasses import dataclass
-from typing import Optional, Sequence
+from typing import Any, Optional, Sequence
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "librb.so")
@@ -69,6 +69,11 @@ class rb_batch_update(ctypes.Structure):
             "d_new_blocks", "d_cached_req_id", "d_cached_num_computed", "d_cached_replace",
             "d_cached_token_start", "d_cached_tokens", "d_cached_block_start",
             "d_cached_blocks")]
+
+
+class rb_score_rules(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("reserved", ctypes.c_int32)] + [
+        (n, ctypes.c_void_p) for n in ("d_head_slopes", "d_key_start", "d_prefix_lens")]
 
 
 class rb_page_tables(ctypes.Structure):
@@ -134,6 +139,9 @@ def _load():
                                              ctypes.c_float, P, P, ctypes.c_size_t, P, P]),
         "rb_batch_apply_update": (I32, [ctypes.POINTER(rb_batch), ctypes.POINTER(rb_batch_update),
                                         P, P, P, ctypes.c_size_t, P, P]),
+        "rb_paged_attention_scored": (I32, [PD, I32, I32, I32, P, P, P, P, P, P, ctypes.c_float,
+                                            ctypes.POINTER(rb_score_rules), P, P,
+                                            ctypes.c_size_t, P, P]),
         "rb_pages_workspace_size": (ctypes.c_size_t, [PD]),
         "rb_pages_count": (I32, [PD, PT, P, P]),
         "rb_pages_copy": (I32, [PD, I32, P, P, P, P, P, ctypes.c_size_t, P, P]),
@@ -325,6 +333,63 @@ def paged_attention(dims: Dims, num_reqs: int, num_tokens: int, q, k_cache, v_ca
         arr = (ctypes.c_void_p * len(handles))(*handles)
         _check("rb_paged_attention_profiled",
                lib.rb_paged_attention_profiled(*args, arr, len(handles)))
+    return out
+
+
+@dataclass(frozen=True)
+class ScoreRules:
+    """How ``paged_attention_scored`` changes the scores (each rule optional): ``softcap`` caps
+    them, softcap * tanh(s / softcap); ``head_slopes`` [nh] fp32 subtracts slope * |p - k|;
+    query token t sees keys from ``key_start[t]`` (int32, flat order: documents, windows) and
+    all of its request's first ``prefix_lens[i]`` keys (int32)."""
+
+    softcap: float = 0.0
+    head_slopes: Any = None
+    key_start: Any = None
+    prefix_lens: Any = None
+
+
+def paged_attention_scored(dims: Dims, num_reqs: int, num_tokens: int, q, k_cache, v_cache,
+                           block_table, query_start_loc, seq_lens, rules: ScoreRules, out=None,
+                           workspace=None, softmax_scale: Optional[float] = None,
+                           error_word=None, stream=None):
+    """``paged_attention`` with score rules; a query that sees no key gets zeros."""
+    import torch
+
+    bf, i32 = torch.bfloat16, torch.int32
+    for name, t, n in (("head_slopes", rules.head_slopes, dims.num_q_heads),
+                       ("key_start", rules.key_start, num_tokens),
+                       ("prefix_lens", rules.prefix_lens, num_reqs)):
+        if t is not None and t.numel() < n:
+            raise ValueError(f"{name} must have {n} entries")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("block_table", block_table),
+                    ("query_start_loc", query_start_loc), ("seq_lens", seq_lens), ("out", out),
+                    ("workspace", workspace), ("error_word", error_word),
+                    ("head_slopes", rules.head_slopes), ("key_start", rules.key_start),
+                    ("prefix_lens", rules.prefix_lens)):
+        if t is not None and t.device != q.device:
+            raise ValueError(f"{name} is on {t.device}, q is on {q.device}")
+    on = _stream_on(q.device, stream)
+    if out is None or workspace is None:
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+            if out is None:
+                out = torch.empty_like(q)
+            if workspace is None:
+                workspace = torch.empty(workspace_size(dims, num_reqs, num_tokens),
+                                        dtype=torch.uint8, device=q.device)
+    scale = 1.0 / math.sqrt(dims.head_dim) if softmax_scale is None else softmax_scale
+    d = dims.c()
+    c = rb_score_rules(rules.softcap, 0, _ptr(rules.head_slopes, torch.float32, "head_slopes"),
+                       _ptr(rules.key_start, i32, "key_start"),
+                       _ptr(rules.prefix_lens, i32, "prefix_lens"))
+    st = lib.rb_paged_attention_scored(
+        ctypes.byref(d), num_reqs, num_tokens, q.shape[0], _ptr(q, bf, "q"),
+        _ptr(k_cache, bf, "k_cache"), _ptr(v_cache, bf, "v_cache"),
+        _ptr(block_table, i32, "block_table"), _ptr(query_start_loc, i32, "query_start_loc"),
+        _ptr(seq_lens, i32, "seq_lens"), ctypes.c_float(scale), ctypes.byref(c),
+        _ptr(out, bf, "out"), _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
+        _ptr(error_word, i32, "error_word"), on)
+    _check("rb_paged_attention_scored", st)
     return out
 
 

@@ -23,8 +23,9 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 
+template <bool kScored>
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnArgs a, int head_dim) {
-  plan_body(a, head_dim, ReqSrc{a.qsl, a.seq_lens, nullptr});
+  plan_body<kScored>(a, head_dim, ReqSrc{a.qsl, a.seq_lens, nullptr});
 }
 
 // Cascade: checks the shared prefix, writes the suffix pass's sequence lengths (seq_len - P)
@@ -149,6 +150,24 @@ rb_status attn_setup(const rb_dims* dims, int32_t num_reqs, int32_t num_tokens,
   return RB_OK;
 }
 
+rb_status attn_set_rules(AttnSetup* su, const rb_score_rules* rules, float softmax_scale) {
+  if (rules == nullptr || rules->reserved != 0 || !std::isfinite(rules->softcap) ||
+      rules->softcap < 0.f)
+    return RB_ERR_INVALID_ARG;
+  AttnArgs& a = su->a;
+  a.scored = 1;
+  if (rules->softcap > 0.f) {
+    a.cap_in = softmax_scale / rules->softcap;
+    a.cap_log2 = rules->softcap * 1.4426950408889634f;
+    if (!std::isfinite(a.cap_in) || !std::isfinite(a.cap_log2)) return RB_ERR_INVALID_ARG;
+    for (int k = 0; k < 6; ++k) a.cap_poly[k] = kTanhPoly[k] * a.cap_log2;
+  }
+  a.slopes = rules->d_head_slopes;
+  a.key_start = rules->d_key_start;
+  a.prefix = rules->d_prefix_lens;
+  return RB_OK;
+}
+
 rb_status attn_encode_maps(AttnSetup* su) {
   const AttnArgs& a = su->a;
   if (!encode_kv_tensor_map(&su->kmap, su->k_cache, su->head_dim, su->num_kv_heads,
@@ -204,7 +223,7 @@ rb_status paged_attention_impl(const rb_dims* dims, int32_t num_reqs, int32_t nu
                                float softmax_scale, void* d_out, void* d_workspace,
                                size_t workspace_bytes, int32_t* d_error_word, void* stream,
                                void* const* events, int32_t num_events,
-                               int32_t prefix_len = 0) {
+                               int32_t prefix_len = 0, const rb_score_rules* rules = nullptr) {
   using namespace rb;
   using namespace rb::attn;
   AttnSetup su;
@@ -213,6 +232,10 @@ rb_status paged_attention_impl(const rb_dims* dims, int32_t num_reqs, int32_t nu
                             softmax_scale, d_out, d_workspace, workspace_bytes, d_error_word,
                             &su);
   if (st != RB_OK) return st;
+  if (rules != nullptr) {
+    st = attn_set_rules(&su, rules, softmax_scale);
+    if (st != RB_OK) return st;
+  }
   const rb_dims& d = *dims;
   const PageGeom& g = su.g;
   AttnArgs& a = su.a;
@@ -264,7 +287,8 @@ rb_status paged_attention_impl(const rb_dims* dims, int32_t num_reqs, int32_t nu
   cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
   if (num_events > 0 && cudaStreamIsCapturing(s, &capturing) != cudaSuccess) return RB_ERR_CUDA;
   const Marks mark{events, num_events, s, capturing == cudaStreamCaptureStatusActive};
-  attn_plan_kernel<<<1, kPlanThreads, 0, s>>>(a, d.head_dim);
+  if (a.scored) attn_plan_kernel<true><<<1, kPlanThreads, 0, s>>>(a, d.head_dim);
+  else attn_plan_kernel<false><<<1, kPlanThreads, 0, s>>>(a, d.head_dim);
   if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
   note_launches(1);
   if (!mark(0)) return RB_ERR_CUDA;
@@ -286,6 +310,20 @@ extern "C" rb_status rb_paged_attention(const rb_dims* dims, int32_t num_reqs, i
                               d_v_cache, d_block_table, d_query_start_loc, d_seq_lens,
                               softmax_scale, d_out, d_workspace, workspace_bytes, d_error_word,
                               stream, nullptr, 0);
+}
+
+extern "C" rb_status rb_paged_attention_scored(
+    const rb_dims* dims, int32_t num_reqs, int32_t num_tokens, int32_t num_tokens_padded,
+    const void* d_q, const void* d_k_cache, const void* d_v_cache, const int32_t* d_block_table,
+    const int32_t* d_query_start_loc, const int32_t* d_seq_lens, float softmax_scale,
+    const rb_score_rules* rules, void* d_out, void* d_workspace, size_t workspace_bytes,
+    int32_t* d_error_word, void* stream) {
+  rb::CallRange range_("rb_paged_attention_scored");
+  if (rules == nullptr) return RB_ERR_INVALID_ARG;
+  return paged_attention_impl(dims, num_reqs, num_tokens, num_tokens_padded, d_q, d_k_cache,
+                              d_v_cache, d_block_table, d_query_start_loc, d_seq_lens,
+                              softmax_scale, d_out, d_workspace, workspace_bytes, d_error_word,
+                              stream, nullptr, 0, 0, rules);
 }
 
 extern "C" rb_status rb_paged_attention_profiled(

@@ -120,7 +120,78 @@ struct AttnArgs {
   // the arrival of its first prefill unit so that the waits for it run out
   unsigned long long wait_limit_ns;
   int withhold_first_unit;
+  // score rules (rb_paged_attention_scored); the ordinary kernels do not read them
+  int scored;
+  float cap_in, cap_log2;    // softcap: score = cap_log2 * tanh(cap_in * q.k) in log2 units
+  float cap_poly[6];         // cap_log2 * (coefficients of tanh(u) / u in u^2, |u| <= 1)
+  const float* slopes;       // [nh] distance bias -slope * |p - k|, or null
+  const int32_t* key_start;  // [N] first visible key of each query token, or null
+  const int32_t* prefix;     // [R] keys every query of the request sees, or null
 };
+
+// The keys a query token at position p of a request of length L may see are [lo, hi):
+// lo = key_start (0 without one), hi = min(L, max(p + 1, prefix)); none when lo >= hi.
+__device__ __forceinline__ int key_lo(const AttnArgs& a, int token) {
+  return a.key_start != nullptr ? max(0, __ldg(a.key_start + token)) : 0;
+}
+__device__ __forceinline__ int key_prefix(const AttnArgs& a, int r, int L) {
+  return a.prefix != nullptr ? min(L, max(0, __ldg(a.prefix + r))) : 0;
+}
+
+// First page a scored decode request (q query tokens from flat token t0, length L) reads: its
+// tokens' smallest key_start's, but always a page of the request, so that a request whose
+// tokens see nothing still has a unit that writes its zero rows.
+__device__ __forceinline__ int scored_first_page(const AttnArgs& a, int t0, int q, int L) {
+  if (a.key_start == nullptr) return 0;
+  int lo = 0x7fffffff;
+#pragma unroll 1
+  for (int j = 0; j < q; ++j) lo = min(lo, key_lo(a, t0 + j));
+  return min(lo / kPage, (L + kPage - 1) / kPage - 1);
+}
+
+// Capped scores (log2 units) of kCount raw products, in place: cap_log2 * tanh(u), u = cap_in *
+// s.  For |u| <= 1 tanh(u) = u P(u^2) with P of degree 5 (least maximum relative error on
+// [0, 1], 6.1e-7 with the coefficients rounded to fp32): multiply-adds two at a time and no
+// trip to the SFU, and exact in the limit of a cap far above the scores.  If some |u| is larger
+// anywhere in the warp, tanh(u) = 1 - 2 / (1 + e^2u), two SFU operations per score (e^2u = inf
+// or 0 gives +-1).
+constexpr float kTanhPoly[6] = {0.9999994039535522f,   -0.3332904279232025f,
+                                0.13281433284282684f,  -0.051605671644210815f,
+                                0.016743114218115807f, -0.0030670601408928633f};
+template <int kCount>
+__device__ __forceinline__ void cap_scores(const AttnArgs& a, float (&s)[kCount]) {
+  static_assert(kCount % 4 == 0, "scores are taken in pairs of pairs");
+  const float2 in = make_float2(a.cap_in, a.cap_in);
+  float2 y[kCount / 2];
+  float top[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kCount / 2; ++i) {
+    const float2 u = __fmul2_rn(make_float2(s[2 * i], s[2 * i + 1]), in);
+    const float2 z = __fmul2_rn(u, u);
+    top[i & 1] = fmax3(top[i & 1], z.x, z.y);
+    float2 p = make_float2(a.cap_poly[5], a.cap_poly[5]);
+#pragma unroll
+    for (int k = 4; k >= 0; --k) p = __ffma2_rn(p, z, make_float2(a.cap_poly[k], a.cap_poly[k]));
+    y[i] = __fmul2_rn(u, p);
+  }
+  if (__any_sync(0xffffffffu, fmaxf(top[0], top[1]) > 1.f)) {
+    const float in2 = a.cap_in * (2.f * 1.4426950408889634f);
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+      float r;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fast_exp2(s[i] * in2) + 1.f));
+      const float far = fmaf(-2.f * a.cap_log2, r, a.cap_log2);
+      const float u = s[i] * a.cap_in, near = i & 1 ? y[i / 2].y : y[i / 2].x;
+      s[i] = u * u > 1.f ? far : near;  // (a NaN stays one)
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kCount / 2; ++i) {
+      s[2 * i] = y[i].x;
+      s[2 * i + 1] = y[i].y;
+    }
+  }
+}
 
 // Test hook behind rb_debug_attention_wait_limit: the wait limit and withhold flag of every
 // later attention call (process-wide).
@@ -190,6 +261,9 @@ rb_status attn_setup(const rb_dims* dims, int32_t num_reqs, int32_t num_tokens,
 rb_status attn_encode_maps(AttnSetup* su);
 // Enqueues what follows the planner: the fused decode + prefill launch.
 rb_status attn_main(const AttnSetup& su, cudaStream_t s);
+
+// Adds rb_paged_attention_scored's rules to a set-up call.
+rb_status attn_set_rules(AttnSetup* su, const rb_score_rules* rules, float softmax_scale);
 
 rb_status launch_prefill_tc(const AttnArgs& a, int head_dim, const CUtensorMap& qmap,
                             const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s);

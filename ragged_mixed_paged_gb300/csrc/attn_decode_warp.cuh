@@ -115,7 +115,10 @@ __device__ void combine_splits(const AttnArgs& a, int h, int first, int nsplit, 
 // `wbase_ptr` the shared-memory address / pointer of its kStages stages (1024-byte aligned).
 // `first_unit` >= 0: the warp's first unit, handed out statically (the counter then starts
 // past every statically handed unit), which saves the first atomic's round trip.
-template <int HD>
+// `kScored`: with the call's score rules; pages are then taken last to first, because a bias
+// that falls with distance has its largest scores there (the reference maximum settles at
+// once), and pages before the first visible one are not read.
+template <int HD, bool kScored = false>
 __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p,
                             const AttnArgs& a, uint64_t* bars, uint32_t wbase,
                             uint8_t* wbase_ptr, int first_unit) {
@@ -141,7 +144,8 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
     const int split = local / a.nkv, h = local - split * a.nkv;
     const int t0 = a.qsl[r], q = a.qsl[r + 1] - t0, L = a.seq_lens[r];
     const int c = L - q, cols = q * a.group, pages = (L + kPage - 1) / kPage;
-    const int p_begin = split * sp, p_end = min(p_begin + sp, pages);
+    const int p_first = kScored ? scored_first_page(a, t0, q, L) : 0;
+    const int p_begin = p_first + split * sp, p_end = min(p_begin + sp, pages);
     const int n_pages = p_end - p_begin;
 
     // Q^T fragments (B operand: k = head dim, n = column)
@@ -163,6 +167,27 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
     const int c0 = 2 * (lane & 3), c1 = c0 + 1;
     const int lim0 = c0 < cols ? c + c0 / a.group : c;
     const int lim1 = c1 < cols ? c + c1 / a.group : c;
+    // scored: first visible key, past the last and slope of the lane's two columns, and the
+    // first key any column sees
+    int lo0 = 0, lo1 = 0, hi0 = 0, hi1 = 0, lo_all = 0;
+    float slope0 = 0.f, slope1 = 0.f;
+    if constexpr (kScored) {
+      const int j0 = c0 < cols ? c0 / a.group : 0, j1 = c1 < cols ? c1 / a.group : 0;
+      const int prefix = key_prefix(a, r, L);
+      lo0 = key_lo(a, t0 + j0);
+      lo1 = key_lo(a, t0 + j1);
+      hi0 = max(c + j0 + 1, prefix);
+      hi1 = max(c + j1 + 1, prefix);
+      if (a.slopes != nullptr) {
+        constexpr float kLog2e = 1.4426950408889634f;
+        const int h0 = c0 < cols ? c0 - j0 * a.group : 0, h1 = c1 < cols ? c1 - j1 * a.group : 0;
+        slope0 = __ldg(a.slopes + h * a.group + h0) * kLog2e;
+        slope1 = __ldg(a.slopes + h * a.group + h1) * kLog2e;
+      }
+      lo_all = min(lo0, lo1);
+      lo_all = min(lo_all, __shfl_xor_sync(0xffffffffu, lo_all, 1));
+      lo_all = min(lo_all, __shfl_xor_sync(0xffffffffu, lo_all, 2));
+    }
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     float acc[C::kKS][4];
 #pragma unroll
@@ -171,24 +196,26 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
 
     // page ids of pages [win, win + 32) held one per lane, the next window prefetched
     const int32_t* bt_row = a.block_table + static_cast<size_t>(r) * a.MB;
-    int win = p_begin;
-    auto page = [&](int pg) {
-      return pg < p_end ? kernel_page(bt_row, pg, a.ratio, a.num_blocks, a.null_block)
-                        : a.null_block;
+    int win = 0;  // pages are counted in the order they are taken: page_of(i), i = 0, 1, ...
+    auto page_of = [&](int i) { return kScored ? p_end - 1 - i : p_begin + i; };
+    auto page = [&](int i) {
+      return i < n_pages ? kernel_page(bt_row, page_of(i), a.ratio, a.num_blocks, a.null_block)
+                         : a.null_block;
     };
     int bid = page(win + lane);
     int bid_next = page(win + 32 + lane);
 
-    auto issue = [&](int pg, uint32_t stage) {  // called by the whole warp
-      if (pg - win >= 32) {
+    auto issue = [&](int i, uint32_t stage) {  // called by the whole warp
+      if (i - win >= 32) {
         win += 32;
         bid = bid_next;
         bid_next = page(win + 32 + lane);
       }
-      int id = __shfl_sync(0xffffffffu, bid, pg - win);
+      int id = __shfl_sync(0xffffffffu, bid, i - win);
       if (lane == 0) {
         if (id < 0 || id >= a.num_blocks || id == a.null_block) {
-          raise_error(a.err, RB_EBIT_BLOCK_ID);
+          // (a page no column sees may hold any id: the request's tokens see nothing)
+          if (!kScored || page_of(i) >= lo_all / kPage) raise_error(a.err, RB_EBIT_BLOCK_ID);
           id = a.null_block;
         }
         uint64_t* bar = &bars[stage];
@@ -205,11 +232,11 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
     };
 
     for (int i = 0; i < C::kStages && i < n_pages; ++i)
-      issue(p_begin + i, (it + i) % C::kStages);
+      issue(i, (it + i) % C::kStages);
 
     bool dead = false;
     for (int i = 0; i < n_pages; ++i) {
-      const int pg = p_begin + i;
+      const int pg = page_of(i);
       const uint32_t stage = it % C::kStages, phase = (it / C::kStages) & 1u;
       const bool ok = mbar_wait_bounded(&bars[stage], phase);
       if (__any_sync(0xffffffffu, !ok)) {
@@ -245,10 +272,35 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
       }
       // causal mask per column, then the softmax per column (log2 domain)
       const int key0 = pg * kPage + (lane >> 2), key1 = key0 + 8;
-      const float x0 = key0 <= lim0 ? s[0] * a.scale_log2 : -INFINITY;
-      const float x1 = key0 <= lim1 ? s[1] * a.scale_log2 : -INFINITY;
-      const float x2 = key1 <= lim0 ? s[2] * a.scale_log2 : -INFINITY;
-      const float x3 = key1 <= lim1 ? s[3] * a.scale_log2 : -INFINITY;
+      float x0, x1, x2, x3;
+      if constexpr (kScored) {
+        if (a.cap_log2 > 0.f) {
+          cap_scores(a, s);
+          x0 = s[0];
+          x1 = s[1];
+          x2 = s[2];
+          x3 = s[3];
+        } else {
+          x0 = s[0] * a.scale_log2;
+          x1 = s[1] * a.scale_log2;
+          x2 = s[2] * a.scale_log2;
+          x3 = s[3] * a.scale_log2;
+        }
+        const int pos0 = lim0, pos1 = lim1;  // the columns' own positions
+        x0 = fmaf(-slope0, fabsf(static_cast<float>(key0 - pos0)), x0);
+        x1 = fmaf(-slope1, fabsf(static_cast<float>(key0 - pos1)), x1);
+        x2 = fmaf(-slope0, fabsf(static_cast<float>(key1 - pos0)), x2);
+        x3 = fmaf(-slope1, fabsf(static_cast<float>(key1 - pos1)), x3);
+        x0 = key0 >= lo0 && key0 < hi0 ? x0 : -INFINITY;
+        x1 = key0 >= lo1 && key0 < hi1 ? x1 : -INFINITY;
+        x2 = key1 >= lo0 && key1 < hi0 ? x2 : -INFINITY;
+        x3 = key1 >= lo1 && key1 < hi1 ? x3 : -INFINITY;
+      } else {
+        x0 = key0 <= lim0 ? s[0] * a.scale_log2 : -INFINITY;
+        x1 = key0 <= lim1 ? s[1] * a.scale_log2 : -INFINITY;
+        x2 = key1 <= lim0 ? s[2] * a.scale_log2 : -INFINITY;
+        x3 = key1 <= lim1 ? s[3] * a.scale_log2 : -INFINITY;
+      }
       // The exponents are taken against a reference m per column that moves only when a score
       // exceeds it by more than kGrowth (log2 units): then the column maxima are reduced and
       // O and l rescaled, as an online softmax does on every page.  Otherwise the page costs
@@ -293,6 +345,20 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
         fence_proxy_async_smem();
         __syncwarp();
       }
+      if constexpr (kScored) {  // nor do keys before the first visible one hold anything known
+        if (pg * kPage < lo_all) {
+          const int kmax = min(lo_all - pg * kPage, kPage);
+          uint8_t* vptr = wbase_ptr + stage * C::kStageBytes + C::kPageBytes;
+          const int per_row = C::kBoxes * 8;
+          for (int x = lane; x < kmax * per_row; x += 32) {
+            const int row = x / per_row, rest = x % per_row;
+            *reinterpret_cast<uint4*>(vptr + (rest >> 3) * C::kBoxBytes + row * 128 +
+                                      (rest & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+      }
       // P^T fragments from S^T's by a register transpose
       const uint32_t pb0 = movmatrix_trans(pack_bf16x2(p0, p1));
       const uint32_t pb1 = movmatrix_trans(pack_bf16x2(p2, p3));
@@ -308,7 +374,7 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
         }
       }
       __syncwarp();
-      if (i + C::kStages < n_pages) issue(pg + C::kStages, stage);
+      if (i + C::kStages < n_pages) issue(i + C::kStages, stage);
       ++it;
     }
     if (dead) return;

@@ -53,6 +53,7 @@ struct ReqSrc {
   const int32_t* computed;
 };
 
+template <bool kScored>
 __device__ __forceinline__ ReqInfo req_info(const AttnArgs& a, const ReqSrc& src, int r) {
   ReqInfo x;
   const int s = src.qsl[r], e = src.qsl[r + 1];
@@ -62,6 +63,8 @@ __device__ __forceinline__ ReqInfo req_info(const AttnArgs& a, const ReqSrc& src
             : src.seq_lens[r];
   x.pages = (x.L + kPage - 1) / kPage;
   x.ok = s >= 0 && x.q >= 0 && e <= a.N && x.L >= x.q && x.pages <= a.kp_cap;
+  if constexpr (kScored)  // pages a decode request reads
+    if (x.ok && is_decode_class(x.q, a.group)) x.pages -= scored_first_page(a, s, x.q, x.L);
   return x;
 }
 
@@ -77,6 +80,17 @@ __device__ __forceinline__ int prefill_pairs(int q, int tile_tokens) {
 __device__ __forceinline__ int pair_key_tiles(int c, int q, int tile_tokens, int pair) {
   const int last_tok = min((pair + 1) * 2 * tile_tokens, q) - 1;
   return (c + last_tok + 1 + 127) / 128;
+}
+
+// The same of a scored unit, from its first and last tokens' key_start: an estimate, which only
+// orders and balances the units (the exact range is taken where the unit is read).
+__device__ __forceinline__ int scored_pair_tiles(const AttnArgs& a, int t0, int r, int c, int q,
+                                                 int tile_tokens, int pair) {
+  const int first = pair * 2 * tile_tokens, last = min(first + 2 * tile_tokens, q) - 1;
+  const int hi = max(c + last + 1, key_prefix(a, r, c + q));
+  const int lo = min(key_lo(a, t0 + first), key_lo(a, t0 + last));
+  const int n = (hi + 127) / 128;
+  return n - min(lo / 128, n - 1);
 }
 
 // Finish-time model of the fused launch (microseconds, this GPU, cold caches; fitted to per-unit
@@ -95,6 +109,7 @@ constexpr int kTileBins = 512;  // histogram bins of prefill units by key tiles 
 // `src`: defaults to the call's query_start_loc and seq_lens in global memory; the fused step
 // passes its shared-memory scan and num_computed, so the planner need not wait for (and read
 // back) the request outputs the same launch writes.
+template <bool kScored = false>
 __device__ __forceinline__ void plan_body(const AttnArgs& a, int head_dim, ReqSrc src) {
   __shared__ unsigned long long s_pages;
   const int tid = threadIdx.x, nthreads = blockDim.x, lane = tid & 31;
@@ -108,8 +123,8 @@ __device__ __forceinline__ void plan_body(const AttnArgs& a, int head_dim, ReqSr
   ReqInfo cache[kCache];
 #pragma unroll 1
   for (int k = 0; k < kCache; ++k)
-    cache[k] = lo + k < hi ? req_info(a, src, lo + k) : ReqInfo{false, 0, 0, 0};
-  auto get = [&](int k) { return k < kCache ? cache[k] : req_info(a, src, lo + k); };
+    cache[k] = lo + k < hi ? req_info<kScored>(a, src, lo + k) : ReqInfo{false, 0, 0, 0};
+  auto get = [&](int k) { return k < kCache ? cache[k] : req_info<kScored>(a, src, lo + k); };
   auto each = [&](auto&& fn) {  // fn(r, info) over this thread's requests, in order
 #pragma unroll 1
     for (int k = 0; lo + k < hi; ++k) fn(lo + k, get(k));
@@ -159,6 +174,10 @@ __device__ __forceinline__ void plan_body(const AttnArgs& a, int head_dim, ReqSr
   __shared__ float s_pre_us;
   __shared__ int s_pre_max;
   const bool fused = a.fused_ctas > 0;
+  auto key_tiles = [&](int r, int c, int q, int p) {
+    if constexpr (kScored) return scored_pair_tiles(a, src.qsl[r], r, c, q, a.tile_tokens, p);
+    else return pair_key_tiles(c, q, a.tile_tokens, p);
+  };
   auto warp_pairs = [&](auto&& body) {  // body(r, c, q, pair) for every pair, warp-cooperative
     auto one = [&](int r, const ReqInfo& x, bool has) {
       const bool pre = has && x.ok && x.q > 0 && !is_decode_class(x.q, a.group);
@@ -189,8 +208,8 @@ __device__ __forceinline__ void plan_body(const AttnArgs& a, int head_dim, ReqSr
     __syncthreads();
     float my_us = 0.f;
     int my_max = 0;
-    warp_pairs([&](int, int c, int q, int p) {
-      const int n = pair_key_tiles(c, q, a.tile_tokens, p);
+    warp_pairs([&](int r, int c, int q, int p) {
+      const int n = key_tiles(r, c, q, p);
       atomicAdd(&s_bin[min(n, kTileBins - 1)], 1);
       my_us += kPreUnitUs + kPreTileUs * n;
       my_max = max(my_max, n);
@@ -221,7 +240,7 @@ __device__ __forceinline__ void plan_body(const AttnArgs& a, int head_dim, ReqSr
     }
     __syncthreads();
     warp_pairs([&](int r, int c, int q, int p) {
-      const int n = pair_key_tiles(c, q, a.tile_tokens, p);
+      const int n = key_tiles(r, c, q, p);
       a.pre_list[atomicAdd(&s_bin[min(n, kTileBins - 1)], 1)] = r * 65536 + p;
     });
   }

@@ -89,6 +89,26 @@ struct TcUnit {
   int r, h, tok0, t0, q, L, c, n[2], n_kt, pages, valid;
 };
 
+// A unit of a scored call.  Its key tiles are [j0, j0 + n_kt) and both query tiles take all of
+// them, last to first: with a bias that falls with distance, or with packed documents, a row's
+// largest scores are in its last tiles, so its reference settles there, whereas first to last
+// it would climb tile by tile (O rescaled each time).  Tile A takes at most one tile that only
+// B's rows see.
+struct ScoredUnit : TcUnit {
+  int j0;         // first key tile
+  int lo;         // first key any row sees
+  int prefix;     // keys every row sees (from its own lo on)
+  int lo_max[2];  // largest first key of each tile's rows
+};
+template <bool kScored>
+struct UnitOf {
+  using type = TcUnit;
+};
+template <>
+struct UnitOf<true> {
+  using type = ScoredUnit;
+};
+
 // First page of a unit's keys and the page-table row they are read from.
 __device__ __forceinline__ int unit_first_page(const AttnArgs& a, const TcUnit& un) {
   return a.cascade == kPrefixPass ? un.r * (a.prefix_split_keys / kPage) : 0;
@@ -97,6 +117,7 @@ __device__ __forceinline__ int unit_table_row(const AttnArgs& a, const TcUnit& u
   return a.cascade == kPrefixPass ? 0 : un.r;
 }
 
+template <bool kScored>
 struct TcShared {
   uint64_t unit_full[4], unit_empty[4];
   uint64_t q_full, q_empty;
@@ -105,7 +126,7 @@ struct TcShared {
   uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
   uint64_t drain;
   uint64_t dec_bars[8][DecCfg<128>::kStages];  // decode phase: one ring per warp 0..7
-  TcUnit units[4];
+  typename UnitOf<kScored>::type units[4];
   uint32_t tmem_base;
   int abort;
   int decode_first;
@@ -227,11 +248,90 @@ struct PageWindow {
   }
 };
 
+// A scored unit, by a whole warp: the ordinary unit's rows, and its tokens' key ranges.
+__device__ __forceinline__ ScoredUnit scored_unit(const AttnArgs& a, int u, int lane) {
+  ScoredUnit un{};
+  static_cast<TcUnit&>(un) = decode_unit(a, u);
+  const int T = a.tile_tokens;
+  un.prefix = key_prefix(a, un.r, un.L);
+  int lo = un.L;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    int mn = 0x7fffffff, mx = 0;
+    if (a.key_start == nullptr) {
+      mn = 0;
+    } else {
+      const int end = min(un.tok0 + (x + 1) * T, un.q);
+      for (int j = un.tok0 + x * T + lane; j < end; j += 32) {
+        const int k = key_lo(a, un.t0 + j);
+        mn = min(mn, k);
+        mx = max(mx, k);
+      }
+      mn = __reduce_min_sync(0xffffffffu, mn);
+      mx = __reduce_max_sync(0xffffffffu, mx);
+    }
+    un.lo_max[x] = mx;
+    lo = min(lo, mn);
+  }
+  un.lo = lo;
+  const int last_tok = min(un.tok0 + 2 * T, un.q) - 1;
+  const int n = (max(un.c + last_tok + 1, un.prefix) + kKeysPerTile - 1) / kKeysPerTile;
+  un.j0 = min(lo / kKeysPerTile, n - 1);  // at least one tile, also when no row sees a key
+  un.n_kt = n - un.j0;
+  un.n[0] = un.n_kt;
+  un.n[1] = un.tok0 + T < un.q ? un.n_kt : 0;
+  return un;
+}
+
+// Page ids of a scored unit's K/V tiles for one warp, last tile first: lane l & 7 holds page
+// l & 7 of the next two tiles.  Pages before the first visible key (which may be gone from the
+// page table) and past the sequence are the null page; their V rows are zeroed.
+struct ScoredPages {
+  const AttnArgs& a;
+  const int32_t* bt_row;
+  int first, pages, j0, last, lane, next0, next1;
+  __device__ ScoredPages(const AttnArgs& a_, const ScoredUnit& un, int lane_)
+      : a(a_),
+        bt_row(a_.block_table + static_cast<size_t>(un.r) * a_.MB),
+        first(un.lo / kPage),
+        pages(un.pages),
+        j0(un.j0),
+        last(un.j0 + un.n_kt - 1),
+        lane(lane_) {
+    next0 = page(last);
+    next1 = page(last - 1);
+  }
+  __device__ int page(int tile) const {
+    const int pg = tile * (kKeysPerTile / kPage) + (lane & 7);
+    return tile >= j0 && pg >= first && pg < pages
+               ? kernel_page(bt_row, pg, a.ratio, a.num_blocks, a.null_block)
+               : a.null_block;
+  }
+  __device__ int tile_page(int j, bool report) {  // j-th tile taken
+    int id = next0;
+    next0 = next1;
+    next1 = page(last - j - 2);
+    if (id < 0) {
+      if (report && lane < kKeysPerTile / kPage) raise_error(a.err, RB_EBIT_BLOCK_ID);
+      id = a.null_block;
+    }
+    return id;
+  }
+};
+template <bool kScored>
+struct PagesOf {
+  using type = PageWindow;
+};
+template <>
+struct PagesOf<true> {
+  using type = ScoredPages;
+};
+
 // Producer of units, Q and K (warp 1, whole warp).  It takes units from the global counter
 // into the 4-entry unit ring, loads Q_A and Q_B once per unit and each K tile into the K
 // ring; lanes 0..7 each issue the boxes of one page of a tile.
-template <int HD>
-__device__ void producer_qk(const AttnArgs& a, TcShared& sh, uint32_t smem_base,
+template <int HD, bool kScored>
+__device__ void producer_qk(const AttnArgs& a, TcShared<kScored>& sh, uint32_t smem_base,
                             const CUtensorMap* qmap, const CUtensorMap* kmap) {
   using C = TcCfg<HD>;
   volatile int* abort = &sh.abort;
@@ -256,10 +356,19 @@ __device__ void producer_qk(const AttnArgs& a, TcShared& sh, uint32_t smem_base,
     const int slot = k % C::kRing;
     if (!lane0_wait(&sh.unit_empty[slot], ((k / C::kRing) & 1) ^ 1)) break;
     int withhold = 0;
+    typename UnitOf<kScored>::type fetched{};
+    if constexpr (kScored) {
+      int u = 0;
+      if (lane == 0) u = atomicAdd(a.header + kHPrefillNext, 1);
+      u = __shfl_sync(0xffffffffu, u, 0);
+      if (u < n_units) fetched = scored_unit(a, u, lane);
+    }
     if (lane == 0) {
-      const int u = atomicAdd(a.header + kHPrefillNext, 1);
-      TcUnit un{};
-      if (u < n_units) un = decode_unit(a, u);
+      if constexpr (!kScored) {
+        const int u = atomicAdd(a.header + kHPrefillNext, 1);
+        if (u < n_units) fetched = decode_unit(a, u);
+      }
+      const auto& un = fetched;
       sh.units[slot] = un;
       // test hook: CTA 0 stops before its first unit reaches the other roles, so their waits
       // for it run out while nothing of that unit has been issued
@@ -268,7 +377,7 @@ __device__ void producer_qk(const AttnArgs& a, TcShared& sh, uint32_t smem_base,
     }
     if (__shfl_sync(0xffffffffu, withhold, 0)) break;
     __syncwarp();
-    const TcUnit un = sh.units[slot];
+    const typename UnitOf<kScored>::type un = sh.units[slot];
     if (!un.valid) break;
     if (!slot_wait(&sh.q_empty, (k & 1) ^ 1)) break;
     if (lane == 0) {
@@ -282,7 +391,7 @@ __device__ void producer_qk(const AttnArgs& a, TcShared& sh, uint32_t smem_base,
           tma_load_3d(smem_base + C::kQOffset + x * C::kQBytes + hf * C::kQHalfBytes, qmap,
                       &sh.q_full, hf * 64, un.h * a.group, un.t0 + un.tok0 + a.tile_tokens * x);
     }
-    PageWindow pw(a, un, lane);
+    typename PagesOf<kScored>::type pw(a, un, lane);
     bool ok = true;
     for (int j = 0; j < un.n_kt; ++j) {
       const int id = pw.tile_page(j, true);
@@ -314,8 +423,8 @@ __device__ void producer_qk(const AttnArgs& a, TcShared& sh, uint32_t smem_base,
 // each V tile into the V ring.  A warp of its own, so that V tiles are issued as soon as their
 // slot frees, not after the next K tile (one warp issuing both took about a whole key-tile step
 // for the TMA issue and waits alone, and left V late).
-template <int HD>
-__device__ void producer_v(const AttnArgs& a, TcShared& sh, uint32_t smem_base,
+template <int HD, bool kScored>
+__device__ void producer_v(const AttnArgs& a, TcShared<kScored>& sh, uint32_t smem_base,
                            const CUtensorMap* vmap) {
   using C = TcCfg<HD>;
   volatile int* abort = &sh.abort;
@@ -335,11 +444,11 @@ __device__ void producer_v(const AttnArgs& a, TcShared& sh, uint32_t smem_base,
   for (int k = 0;; ++k) {
     const int slot = k % C::kRing;
     if (!lane0_wait(&sh.unit_full[slot], (k / C::kRing) & 1)) break;
-    const TcUnit un = sh.units[slot];
+    const typename UnitOf<kScored>::type un = sh.units[slot];
     if (!un.valid) break;
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&sh.unit_empty[slot]);  // the descriptor is in registers
-    PageWindow pw(a, un, lane);
+    typename PagesOf<kScored>::type pw(a, un, lane);
     bool ok = true;
     for (int j = 0; j < un.n_kt; ++j) {
       const int id = pw.tile_page(j, false);
@@ -367,8 +476,9 @@ __device__ void producer_v(const AttnArgs& a, TcShared& sh, uint32_t smem_base,
   }
 }
 
-template <int HD>
-__device__ void mma_issuer(const AttnArgs& a, TcShared& sh, uint32_t tmem, uint32_t smem_base) {
+template <int HD, bool kScored>
+__device__ void mma_issuer(const AttnArgs& a, TcShared<kScored>& sh, uint32_t tmem,
+                           uint32_t smem_base) {
   using C = TcCfg<HD>;
   volatile int* abort = &sh.abort;
   constexpr uint32_t idesc_s = tc::make_idesc(128, 128, false);
@@ -430,7 +540,7 @@ __device__ void mma_issuer(const AttnArgs& a, TcShared& sh, uint32_t tmem, uint3
   for (int k = 0;; ++k) {
     const int slot = k % C::kRing;
     if (!tc_wait(&sh.unit_full[slot], (k / C::kRing) & 1, abort, a)) break;
-    const TcUnit un = sh.units[slot];
+    const typename UnitOf<kScored>::type un = sh.units[slot];
     if (!un.valid) break;
     const bool q_k = test(&sh.q_full, k & 1) & test(&sh.k_full[itk % C::kStagesK], (itk / C::kStagesK) & 1);
     if (!q_k && (!wait(&sh.q_full, k & 1) ||
@@ -484,9 +594,9 @@ __device__ void mma_issuer(const AttnArgs& a, TcShared& sh, uint32_t tmem, uint3
 }
 
 // Softmax and epilogue of tile x (0 = A, 1 = B); thread t = row t of the tile = TMEM lane t.
-template <int HD>
-__device__ void softmax_wg(const AttnArgs& a, TcShared& sh, uint32_t tmem, uint8_t* smem_ptr,
-                           int x) {
+template <int HD, bool kScored>
+__device__ void softmax_wg(const AttnArgs& a, TcShared<kScored>& sh, uint32_t tmem,
+                           uint8_t* smem_ptr, int x) {
   using C = TcCfg<HD>;
   volatile int* abort = &sh.abort;
   const int t = threadIdx.x & 127;
@@ -509,7 +619,7 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared& sh, uint32_t tmem, uint8
   for (int k = 0;; ++k) {
     const int slot = k % C::kRing;
     if (!wait_all(&sh.unit_full[slot], (k / C::kRing) & 1)) break;
-    const TcUnit un = sh.units[slot];
+    const typename UnitOf<kScored>::type un = sh.units[slot];
     if (!un.valid) break;
     const int n = un.n[x];
     // row t of this tile: token tok_base + t / group, head t % group of the kv head's group;
@@ -525,15 +635,30 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared& sh, uint32_t tmem, uint8
     const int lim = !valid ? -1 : (causal ? un.c + jt : un.c);
     const int lim_min = causal ? un.c + tok_base : un.c;
     const bool partial = rows_used < C::kM || tok_base + a.tile_tokens > un.q;
+    // scored: the row's keys [lo, hi), its slope, and the smallest hi of the tile's rows
+    int lo = 0, hi = 0, hi_min = 0;
+    float slope = 0.f;
+    if constexpr (kScored) {
+      if (valid) {
+        lo = key_lo(a, un.t0 + jt);
+        hi = max(max(un.c + jt + 1, un.prefix), lo);
+        if (a.slopes != nullptr)
+          slope = __ldg(a.slopes + un.h * a.group + hh) * 1.4426950408889634f;
+      }
+      hi_min = max(un.c + tok_base + 1, un.prefix);
+    }
+    // scores are scaled inside the exponent unless a rule already took them to log2 units
+    const bool ruled = kScored && (a.cap_log2 > 0.f || a.slopes != nullptr);
+    const float score_scale = ruled ? 1.f : a.scale_log2;
     // The side that reads every K/V tile of the unit (B, or A when B is empty: B's rows come
     // later, so it sees at least A's keys) hands the Q, K and V slots back to the producers:
     // its S of tile j landing means every MMA issued before that S has completed, S_A of tile
     // j and both P V of tile j - 1 among them; its last P V landing (o_done) frees the last V.
     // This keeps those arrivals off the MMA issuer, whose commits are its critical path.
     const bool releases = x == (un.n[1] > 0 ? 1 : 0);
-    // running reference (log2 domain) and sum; a row without a query starts at 0, so that only
-    // rows with visible keys take the first tile's maximum
-    float m_ref = valid ? -INFINITY : 0.f, l = 0.f;
+    // running reference (log2 domain) and sum; a row without a query (or, scored, without a
+    // visible key) starts at 0, so that only rows with visible keys take a first tile's maximum
+    float m_ref = (kScored ? hi > lo : valid) ? -INFINITY : 0.f, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const uint32_t tj = tc_x + j;
@@ -561,8 +686,28 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared& sh, uint32_t tmem, uint8
           s[96 + i] = __uint_as_float(r3[i]);
         }
       }
-      const int kv_base = j * C::kN;
-      if (partial || kv_base + C::kN - 1 > lim_min) {
+      int kv_base = j * C::kN;
+      if constexpr (kScored) {
+        kv_base = (un.j0 + n - 1 - j) * C::kN;
+        if (a.cap_log2 > 0.f) {
+#pragma unroll
+          for (int c = 0; c < 128; c += 16) cap_scores(a, *reinterpret_cast<float(*)[16]>(s + c));
+        } else if (ruled) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) s[i] *= a.scale_log2;
+        }
+        if (a.slopes != nullptr) {
+          const float d0 = static_cast<float>(kv_base - (un.c + jt));
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            s[i] = fmaf(-slope, fabsf(d0 + static_cast<float>(i)), s[i]);
+        }
+        if (partial || kv_base < un.lo_max[x] || kv_base + C::kN > hi_min) {
+          const unsigned first = static_cast<unsigned>(kv_base - lo), len = hi - lo;
+#pragma unroll
+          for (int i = 0; i < 128; ++i) s[i] = first + i < len ? s[i] : -INFINITY;
+        }
+      } else if (partial || kv_base + C::kN - 1 > lim_min) {
 #pragma unroll
         for (int i = 0; i < 128; ++i) s[i] = (kv_base + i <= lim) ? s[i] : -INFINITY;
       }
@@ -587,11 +732,12 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared& sh, uint32_t tmem, uint8
         // scores are scaled inside the exponent: max and mask commute with a positive scale
         const float m_tile = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
                                    fmaxf(mx[6], mx[7])) *
-                             a.scale_log2;
+                             score_scale;
         const bool need = m_tile > m_ref;
         if (__any_sync(0xffffffffu, need)) {
           const float m_new = need ? m_tile : m_ref;
-          const float alpha = fast_exp2(m_ref - m_new);
+          // (a scored row that has not seen a key yet keeps its reference of -inf)
+          const float alpha = !kScored || need ? fast_exp2(m_ref - m_new) : 1.f;
           if (j > 0) {  // O holds P_{j-1} V_{j-1}: S_j, issued after it, has landed
             uint32_t r[32];
 #pragma unroll
@@ -611,11 +757,16 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared& sh, uint32_t tmem, uint8
       if (__any_sync(0xffffffffu, m_ref == -INFINITY)) take_tile_max();
       // keys at or past the end of the sequence may hold anything: zero their V rows (only the
       // unit's last K/V tile can reach them; tile A zeroes it when it uses that tile)
-      if (kv_base + C::kN > un.L && (x == 0 || j >= un.n[0])) {
+      // (scored: nor are keys before the first visible one known, in the unit's first tile)
+      bool unknown = kv_base + C::kN > un.L;
+      if constexpr (kScored) unknown = unknown || kv_base < un.lo;
+      if (unknown && (x == 0 || j >= un.n[0])) {
         const uint32_t kt = itk + j, sv = kt % C::kStagesV;
         if (!wait_all(&sh.v_full[sv], (kt / C::kStagesV) & 1)) { ok = false; break; }
         const int kmin = max(un.L - kv_base, 0);
-        if (t >= kmin) {
+        bool zero = t >= kmin;
+        if constexpr (kScored) zero = zero || t < un.lo - kv_base;
+        if (zero) {
           uint8_t* vrow = smem_ptr + C::kVOffset + sv * C::kTileBytes + t * 128;
 #pragma unroll
           for (int hf = 0; hf < C::kHalves; ++hf)
@@ -630,7 +781,7 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared& sh, uint32_t tmem, uint8
       // instructions; P (bf16) goes over the S columns
       auto exponents = [&]() -> float {
         const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nmu2 = make_float2(-mu, -mu);
+        const float2 sc2 = make_float2(score_scale, score_scale), nmu2 = make_float2(-mu, -mu);
         float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                         make_float2(0.f, 0.f)};
 #pragma unroll
@@ -749,14 +900,14 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared& sh, uint32_t tmem, uint8
   }
 }
 
-template <int HD>
+template <int HD, bool kScored>
 __global__ void __launch_bounds__(TcCfg<HD>::kThreads, 1)
     attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap qmap,
                            const __grid_constant__ CUtensorMap kmap,
                            const __grid_constant__ CUtensorMap vmap, const AttnArgs a) {
   using C = TcCfg<HD>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ TcShared sh;
+  __shared__ TcShared<kScored> sh;
   const int tid = threadIdx.x, warp = tid >> 5;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -821,11 +972,11 @@ __global__ void __launch_bounds__(TcCfg<HD>::kThreads, 1)
     for (int phase = 0; phase < 2; ++phase) {
       if ((phase == 0) != decode_first) {
         if (warp == C::kProducerWarp) {
-          producer_qk<HD>(a, sh, base, &qmap, &kmap);
+          producer_qk<HD, kScored>(a, sh, base, &qmap, &kmap);
         } else if (warp == C::kProducerVWarp) {
-          producer_v<HD>(a, sh, base, &vmap);
+          producer_v<HD, kScored>(a, sh, base, &vmap);
         } else if (warp == C::kMmaWarp) {
-          if ((tid & 31) == 0) mma_issuer<HD>(a, sh, tmem, base);
+          if ((tid & 31) == 0) mma_issuer<HD, kScored>(a, sh, tmem, base);
         }
       }
       phase_end();
@@ -837,11 +988,12 @@ __global__ void __launch_bounds__(TcCfg<HD>::kThreads, 1)
         using D = DecCfg<HD>;
         const int w = warp - 4;
         // a decode-first CTA's warps start on units rank x 8 + w without the counter
-        decode_warp<HD>(&kmap, &vmap, a, sh.dec_bars[w], base + w * D::kStages * D::kStageBytes,
-                        base_ptr + w * D::kStages * D::kStageBytes,
-                        decode_first ? sh.role_rank * a.decode_warps_per_cta + w : -1);
+        decode_warp<HD, kScored>(&kmap, &vmap, a, sh.dec_bars[w],
+                                 base + w * D::kStages * D::kStageBytes,
+                                 base_ptr + w * D::kStages * D::kStageBytes,
+                                 decode_first ? sh.role_rank * a.decode_warps_per_cta + w : -1);
       } else {
-        softmax_wg<HD>(a, sh, tmem, base_ptr, (warp >> 2) - 1);
+        softmax_wg<HD, kScored>(a, sh, tmem, base_ptr, (warp >> 2) - 1);
       }
       phase_end();
     }
@@ -852,7 +1004,7 @@ __global__ void __launch_bounds__(TcCfg<HD>::kThreads, 1)
   }
 }
 
-template <int HD>
+template <int HD, bool kScored>
 rb_status launch_hd(const AttnArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                     const CUtensorMap& vmap, cudaStream_t s) {
   using C = TcCfg<HD>;
@@ -860,14 +1012,14 @@ rb_status launch_hd(const AttnArgs& a, const CUtensorMap& qmap, const CUtensorMa
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return RB_ERR_CUDA;
   if (!configured[dev]) {
-    if (cudaFuncSetAttribute(attn_prefill_tc_kernel<HD>,
+    if (cudaFuncSetAttribute(attn_prefill_tc_kernel<HD, kScored>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::kSmemBytes) != cudaSuccess)
       return RB_ERR_CUDA;
     configured[dev] = true;
   }
   const int grid = max(1, device_sm_count());
-  attn_prefill_tc_kernel<HD><<<grid, C::kThreads, C::kSmemBytes, s>>>(qmap, kmap, vmap, a);
+  attn_prefill_tc_kernel<HD, kScored><<<grid, C::kThreads, C::kSmemBytes, s>>>(qmap, kmap, vmap, a);
   if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
   note_launches(1);
   return RB_OK;
@@ -877,8 +1029,11 @@ rb_status launch_hd(const AttnArgs& a, const CUtensorMap& qmap, const CUtensorMa
 
 rb_status launch_prefill_tc(const AttnArgs& a, int head_dim, const CUtensorMap& qmap,
                             const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
-  return head_dim == 128 ? launch_hd<128>(a, qmap, kmap, vmap, s)
-                         : launch_hd<64>(a, qmap, kmap, vmap, s);
+  if (a.scored)
+    return head_dim == 128 ? launch_hd<128, true>(a, qmap, kmap, vmap, s)
+                           : launch_hd<64, true>(a, qmap, kmap, vmap, s);
+  return head_dim == 128 ? launch_hd<128, false>(a, qmap, kmap, vmap, s)
+                         : launch_hd<64, false>(a, qmap, kmap, vmap, s);
 }
 
 }  // namespace attn
