@@ -155,14 +155,28 @@ rb_status attn_set_rules(AttnSetup* su, const rb_score_rules* rules, float softm
       rules->softcap < 0.f)
     return RB_ERR_INVALID_ARG;
   AttnArgs& a = su->a;
-  a.scored = 1;
+  a.rules = kMasked;
   if (rules->softcap > 0.f) {
+    a.rules |= kCapped;
     a.cap_in = softmax_scale / rules->softcap;
     a.cap_log2 = rules->softcap * 1.4426950408889634f;
     if (!std::isfinite(a.cap_in) || !std::isfinite(a.cap_log2)) return RB_ERR_INVALID_ARG;
-    for (int k = 0; k < 6; ++k) a.cap_poly[k] = kTanhPoly[k] * a.cap_log2;
+    // A coefficient that falls below fp32's range (a cap far above any score) is dropped, and
+    // the polynomial kept to arguments where its term is below 1e-7.
+    double f = static_cast<double>(a.cap_log2) * a.cap_in, z = kTanhZ;
+    const double z_without[4] = {0.0, 1e-7, 1e-4, 1e-2};
+    for (int k = 0; k < 4; ++k) {
+      const double c = kTanhPoly[k] * f;
+      const bool fits = std::fabs(c) >= 1e-37 && std::fabs(c) <= 3e38;
+      a.cap_poly[k] = fits ? static_cast<float>(c) : 0.f;
+      if (!fits) z = std::fmin(z, z_without[k]);
+      f *= static_cast<double>(a.cap_in) * a.cap_in;
+    }
+    a.cap_z = static_cast<float>(
+        std::fmin(3e38, z / (static_cast<double>(a.cap_in) * a.cap_in)));
   }
   a.slopes = rules->d_head_slopes;
+  if (a.slopes != nullptr) a.rules |= kBiased;
   a.key_start = rules->d_key_start;
   a.prefix = rules->d_prefix_lens;
   return RB_OK;
@@ -287,7 +301,7 @@ rb_status paged_attention_impl(const rb_dims* dims, int32_t num_reqs, int32_t nu
   cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
   if (num_events > 0 && cudaStreamIsCapturing(s, &capturing) != cudaSuccess) return RB_ERR_CUDA;
   const Marks mark{events, num_events, s, capturing == cudaStreamCaptureStatusActive};
-  if (a.scored) attn_plan_kernel<true><<<1, kPlanThreads, 0, s>>>(a, d.head_dim);
+  if (is_scored(a.rules)) attn_plan_kernel<true><<<1, kPlanThreads, 0, s>>>(a, d.head_dim);
   else attn_plan_kernel<false><<<1, kPlanThreads, 0, s>>>(a, d.head_dim);
   if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
   note_launches(1);

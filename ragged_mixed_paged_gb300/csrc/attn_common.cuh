@@ -121,13 +121,20 @@ struct AttnArgs {
   unsigned long long wait_limit_ns;
   int withhold_first_unit;
   // score rules (rb_paged_attention_scored); the ordinary kernels do not read them
-  int scored;
+  int rules;                 // Rules the kernel applies
   float cap_in, cap_log2;    // softcap: score = cap_log2 * tanh(cap_in * q.k) in log2 units
-  float cap_poly[6];         // cap_log2 * (coefficients of tanh(u) / u in u^2, |u| <= 1)
+  float cap_poly[4];         // the same as s * (cap_poly[0] + s^2 (cap_poly[1] + ...)), s = q.k
+  float cap_z;               // for s^2 up to cap_z
   const float* slopes;       // [nh] distance bias -slope * |p - k|, or null
   const int32_t* key_start;  // [N] first visible key of each query token, or null
   const int32_t* prefix;     // [R] keys every query of the request sees, or null
 };
+
+// What a kernel instance applies, so that each rule's code (and its registers) is only in the
+// kernels of the calls that ask for it: kOrdinary is rb_paged_attention, kMasked adds the key
+// ranges, and the other two the soft cap and the distance bias on top of them.
+enum Rules : int { kOrdinary = 0, kMasked = 1, kCapped = 2, kBiased = 4 };
+__host__ __device__ constexpr bool is_scored(int rules) { return rules != kOrdinary; }
 
 // The keys a query token at position p of a request of length L may see are [lo, hi):
 // lo = key_start (0 without one), hi = min(L, max(p + 1, prefix)); none when lo >= hi.
@@ -149,40 +156,39 @@ __device__ __forceinline__ int scored_first_page(const AttnArgs& a, int t0, int 
   return min(lo / kPage, (L + kPage - 1) / kPage - 1);
 }
 
-// Capped scores (log2 units) of kCount raw products, in place: cap_log2 * tanh(u), u = cap_in *
-// s.  For |u| <= 1 tanh(u) = u P(u^2) with P of degree 5 (least maximum relative error on
-// [0, 1], 6.1e-7 with the coefficients rounded to fp32): multiply-adds two at a time and no
-// trip to the SFU, and exact in the limit of a cap far above the scores.  If some |u| is larger
-// anywhere in the warp, tanh(u) = 1 - 2 / (1 + e^2u), two SFU operations per score (e^2u = inf
-// or 0 gives +-1).
-constexpr float kTanhPoly[6] = {0.9999994039535522f,   -0.3332904279232025f,
-                                0.13281433284282684f,  -0.051605671644210815f,
-                                0.016743114218115807f, -0.0030670601408928633f};
+// Capped scores (log2 units): cap_log2 * tanh(u), u = cap_in * s.  For u^2 <= kTanhZ tanh(u) =
+// u P(u^2) with P(0) = 1 of degree 3, the least maximum relative error of that form (8.5e-6,
+// vanishing with u: 4e-4 log2 units for a cap of 50 at u = 0.7, a sixteenth of what rounding P
+// to bf16 costs): multiply-adds two at a time and no trip to the SFU, which the exponents keep
+// busy.  Larger |u|: tanh(u) = 1 - 2 / (1 + e^2u), two SFU operations (e^2u = inf or 0 gives
+// +-1).
+constexpr float kTanhPoly[4] = {1.0f, -0.3329871892929077f, 0.12897320091724396f, -0.03759901970624924f};
+constexpr float kTanhZ = 0.5f;
+
+// kCount raw products, in place.
 template <int kCount>
 __device__ __forceinline__ void cap_scores(const AttnArgs& a, float (&s)[kCount]) {
   static_assert(kCount % 4 == 0, "scores are taken in pairs of pairs");
-  const float2 in = make_float2(a.cap_in, a.cap_in);
   float2 y[kCount / 2];
   float top[2] = {0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < kCount / 2; ++i) {
-    const float2 u = __fmul2_rn(make_float2(s[2 * i], s[2 * i + 1]), in);
-    const float2 z = __fmul2_rn(u, u);
+    const float2 x = make_float2(s[2 * i], s[2 * i + 1]), z = __fmul2_rn(x, x);
     top[i & 1] = fmax3(top[i & 1], z.x, z.y);
-    float2 p = make_float2(a.cap_poly[5], a.cap_poly[5]);
+    float2 p = make_float2(a.cap_poly[3], a.cap_poly[3]);
 #pragma unroll
-    for (int k = 4; k >= 0; --k) p = __ffma2_rn(p, z, make_float2(a.cap_poly[k], a.cap_poly[k]));
-    y[i] = __fmul2_rn(u, p);
+    for (int k = 2; k >= 0; --k) p = __ffma2_rn(p, z, make_float2(a.cap_poly[k], a.cap_poly[k]));
+    y[i] = __fmul2_rn(x, p);
   }
-  if (__any_sync(0xffffffffu, fmaxf(top[0], top[1]) > 1.f)) {
+  if (__any_sync(0xffffffffu, fmaxf(top[0], top[1]) > a.cap_z)) {
     const float in2 = a.cap_in * (2.f * 1.4426950408889634f);
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
       float r;
       asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fast_exp2(s[i] * in2) + 1.f));
       const float far = fmaf(-2.f * a.cap_log2, r, a.cap_log2);
-      const float u = s[i] * a.cap_in, near = i & 1 ? y[i / 2].y : y[i / 2].x;
-      s[i] = u * u > 1.f ? far : near;  // (a NaN stays one)
+      const float near = i & 1 ? y[i / 2].y : y[i / 2].x;
+      s[i] = s[i] * s[i] > a.cap_z ? far : near;  // (a NaN stays one)
     }
   } else {
 #pragma unroll

@@ -115,14 +115,15 @@ __device__ void combine_splits(const AttnArgs& a, int h, int first, int nsplit, 
 // `wbase_ptr` the shared-memory address / pointer of its kStages stages (1024-byte aligned).
 // `first_unit` >= 0: the warp's first unit, handed out statically (the counter then starts
 // past every statically handed unit), which saves the first atomic's round trip.
-// `kScored`: with the call's score rules; pages are then taken last to first, because a bias
+// `kRules` (Rules): with the call's score rules; pages are then taken last to first, because a bias
 // that falls with distance has its largest scores there (the reference maximum settles at
 // once), and pages before the first visible one are not read.
-template <int HD, bool kScored = false>
+template <int HD, int kRules = kOrdinary>
 __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p,
                             const AttnArgs& a, uint64_t* bars, uint32_t wbase,
                             uint8_t* wbase_ptr, int first_unit) {
   using C = DecCfg<HD>;
+  constexpr bool kScored = is_scored(kRules);
   const int lane = threadIdx.x & 31;
   const int n_units = a.header[kHNumDecodeUnits];
   const int sp = a.header[kHSplitPages];
@@ -178,7 +179,7 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
       lo1 = key_lo(a, t0 + j1);
       hi0 = max(c + j0 + 1, prefix);
       hi1 = max(c + j1 + 1, prefix);
-      if (a.slopes != nullptr) {
+      if constexpr ((kRules & kBiased) != 0) {
         constexpr float kLog2e = 1.4426950408889634f;
         const int h0 = c0 < cols ? c0 - j0 * a.group : 0, h1 = c1 < cols ? c1 - j1 * a.group : 0;
         slope0 = __ldg(a.slopes + h * a.group + h0) * kLog2e;
@@ -274,7 +275,7 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
       const int key0 = pg * kPage + (lane >> 2), key1 = key0 + 8;
       float x0, x1, x2, x3;
       if constexpr (kScored) {
-        if (a.cap_log2 > 0.f) {
+        if constexpr ((kRules & kCapped) != 0) {
           cap_scores(a, s);
           x0 = s[0];
           x1 = s[1];
@@ -286,11 +287,13 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
           x2 = s[2] * a.scale_log2;
           x3 = s[3] * a.scale_log2;
         }
-        const int pos0 = lim0, pos1 = lim1;  // the columns' own positions
-        x0 = fmaf(-slope0, fabsf(static_cast<float>(key0 - pos0)), x0);
-        x1 = fmaf(-slope1, fabsf(static_cast<float>(key0 - pos1)), x1);
-        x2 = fmaf(-slope0, fabsf(static_cast<float>(key1 - pos0)), x2);
-        x3 = fmaf(-slope1, fabsf(static_cast<float>(key1 - pos1)), x3);
+        if constexpr ((kRules & kBiased) != 0) {
+          const int pos0 = lim0, pos1 = lim1;  // the columns' own positions
+          x0 = fmaf(-slope0, fabsf(static_cast<float>(key0 - pos0)), x0);
+          x1 = fmaf(-slope1, fabsf(static_cast<float>(key0 - pos1)), x1);
+          x2 = fmaf(-slope0, fabsf(static_cast<float>(key1 - pos0)), x2);
+          x3 = fmaf(-slope1, fabsf(static_cast<float>(key1 - pos1)), x3);
+        }
         x0 = key0 >= lo0 && key0 < hi0 ? x0 : -INFINITY;
         x1 = key0 >= lo1 && key0 < hi1 ? x1 : -INFINITY;
         x2 = key1 >= lo0 && key1 < hi0 ? x2 : -INFINITY;

@@ -32,6 +32,8 @@
 //              producers as its S tiles land, so the issuer commits only S, O and its drain.
 // All mbarrier waits are bounded; a timeout sets RB_EBIT_TIMEOUT, every role stops, in-flight
 // copies and MMAs are drained with bounded waits and TMEM is freed before the CTA exits.
+#include <type_traits>
+
 #include "attn_common.cuh"
 #include "attn_decode_warp.cuh"
 #include "tc_ptx.cuh"
@@ -98,7 +100,7 @@ struct ScoredUnit : TcUnit {
   int j0;         // first key tile
   int lo;         // first key any row sees
   int prefix;     // keys every row sees (from its own lo on)
-  int lo_max[2];  // largest first key of each tile's rows
+  int lo_max[2];  // largest first key of each tile's rows (rows that see no key left out)
 };
 template <bool kScored>
 struct UnitOf {
@@ -265,7 +267,7 @@ __device__ __forceinline__ ScoredUnit scored_unit(const AttnArgs& a, int u, int 
       for (int j = un.tok0 + x * T + lane; j < end; j += 32) {
         const int k = key_lo(a, un.t0 + j);
         mn = min(mn, k);
-        mx = max(mx, k);
+        if (k < max(un.c + j + 1, un.prefix)) mx = max(mx, k);
       }
       mn = __reduce_min_sync(0xffffffffu, mn);
       mx = __reduce_max_sync(0xffffffffu, mx);
@@ -594,10 +596,11 @@ __device__ void mma_issuer(const AttnArgs& a, TcShared<kScored>& sh, uint32_t tm
 }
 
 // Softmax and epilogue of tile x (0 = A, 1 = B); thread t = row t of the tile = TMEM lane t.
-template <int HD, bool kScored>
-__device__ void softmax_wg(const AttnArgs& a, TcShared<kScored>& sh, uint32_t tmem,
+template <int HD, int kRules>
+__device__ void softmax_wg(const AttnArgs& a, TcShared<is_scored(kRules)>& sh, uint32_t tmem,
                            uint8_t* smem_ptr, int x) {
   using C = TcCfg<HD>;
+  constexpr bool kScored = is_scored(kRules);
   volatile int* abort = &sh.abort;
   const int t = threadIdx.x & 127;
   const uint32_t lane_off = static_cast<uint32_t>((t >> 5) * 32) << 16;
@@ -637,29 +640,51 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<kScored>& sh, uint32_t tm
     const bool partial = rows_used < C::kM || tok_base + a.tile_tokens > un.q;
     // scored: the row's keys [lo, hi), its slope, and the smallest hi of the tile's rows
     int lo = 0, hi = 0, hi_min = 0;
+    bool blind = false;
     float slope = 0.f;
     if constexpr (kScored) {
       if (valid) {
         lo = key_lo(a, un.t0 + jt);
-        hi = max(max(un.c + jt + 1, un.prefix), lo);
-        if (a.slopes != nullptr)
+        hi = max(un.c + jt + 1, un.prefix);
+        // A row that sees no key takes the unit's keys as its own, so that it does not make
+        // every tile a masked one, and writes zeros in the end.
+        if (lo >= hi) {
+          blind = true;
+          lo = 0;
+        }
+        if constexpr ((kRules & kBiased) != 0)
           slope = __ldg(a.slopes + un.h * a.group + hh) * 1.4426950408889634f;
       }
       hi_min = max(un.c + tok_base + 1, un.prefix);
     }
     // scores are scaled inside the exponent unless a rule already took them to log2 units
-    const bool ruled = kScored && (a.cap_log2 > 0.f || a.slopes != nullptr);
+    constexpr bool ruled = (kRules & (kCapped | kBiased)) != 0;
     const float score_scale = ruled ? 1.f : a.scale_log2;
+    // factors of the ruled exponents as register pairs (two-at-a-time instructions take no
+    // operand from constant memory; the empty asm keeps them from being fetched again per use)
+    auto pair_of = [](float v) {
+      float2 p = make_float2(v, v);
+      asm volatile("" : "+f"(p.x), "+f"(p.y));
+      return p;
+    };
+    float2 scale2 = make_float2(0.f, 0.f), cap2[4];
+    if constexpr ((kRules & kCapped) != 0) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) cap2[k] = pair_of(a.cap_poly[k]);
+    } else if constexpr (ruled) {
+      scale2 = pair_of(a.scale_log2);
+    }
     // The side that reads every K/V tile of the unit (B, or A when B is empty: B's rows come
     // later, so it sees at least A's keys) hands the Q, K and V slots back to the producers:
     // its S of tile j landing means every MMA issued before that S has completed, S_A of tile
     // j and both P V of tile j - 1 among them; its last P V landing (o_done) frees the last V.
     // This keeps those arrivals off the MMA issuer, whose commits are its critical path.
     const bool releases = x == (un.n[1] > 0 ? 1 : 0);
-    // running reference (log2 domain) and sum; a row without a query (or, scored, without a
-    // visible key) starts at 0, so that only rows with visible keys take a first tile's maximum
-    float m_ref = (kScored ? hi > lo : valid) ? -INFINITY : 0.f, l = 0.f;
+    // running reference (log2 domain) and sum; a row without a query starts at 0, so that only
+    // rows with visible keys take the first tile's maximum
+    float m_ref = valid ? -INFINITY : 0.f, l = 0.f;
     bool ok = true;
+    bool far = false;  // a score of this unit lay outside the capping polynomial's range
     for (int j = 0; j < n; ++j) {
       const uint32_t tj = tc_x + j;
       if (!wait_all(&sh.s_full[x], tj & 1)) { ok = false; break; }
@@ -687,22 +712,37 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<kScored>& sh, uint32_t tm
         }
       }
       int kv_base = j * C::kN;
-      if constexpr (kScored) {
-        kv_base = (un.j0 + n - 1 - j) * C::kN;
-        if (a.cap_log2 > 0.f) {
+      // the rules applied to the tile's scores, in log2 units, in place
+      auto rule_scores = [&](int base) {
+        if constexpr ((kRules & kCapped) != 0) {
 #pragma unroll
           for (int c = 0; c < 128; c += 16) cap_scores(a, *reinterpret_cast<float(*)[16]>(s + c));
-        } else if (ruled) {
+        } else if constexpr (ruled) {
 #pragma unroll
           for (int i = 0; i < 128; ++i) s[i] *= a.scale_log2;
         }
-        if (a.slopes != nullptr) {
-          const float d0 = static_cast<float>(kv_base - (un.c + jt));
+        if constexpr ((kRules & kBiased) != 0) {
+          const float d0 = static_cast<float>(base - (un.c + jt));
 #pragma unroll
           for (int i = 0; i < 128; ++i)
             s[i] = fmaf(-slope, fabsf(d0 + static_cast<float>(i)), s[i]);
         }
-        if (partial || kv_base < un.lo_max[x] || kv_base + C::kN > hi_min) {
+      };
+      const bool fresh = __any_sync(0xffffffffu, m_ref == -INFINITY);
+      // Ruled scores are taken from the raw ones inside the exponents (`fused`), where a cap
+      // costs four multiply-adds and a bias one on top of the scaling; tiles that need their
+      // values before (a mask, a first maximum) are ruled in place first.
+      bool masked = false, fused = false;
+      if constexpr (kScored) {
+        kv_base = (un.j0 + n - 1 - j) * C::kN;
+        masked = partial || kv_base < un.lo_max[x] || kv_base + C::kN > hi_min;
+        if constexpr (ruled) {
+          // a key past its query, where the distance changes sign, needs |p - k| taken
+          const bool past = (kRules & kBiased) != 0 && kv_base + C::kN > un.c + tok_base + 1;
+          fused = !(masked || past || far || fresh);
+          if (!fused) rule_scores(kv_base);
+        }
+        if (masked) {
           const unsigned first = static_cast<unsigned>(kv_base - lo), len = hi - lo;
 #pragma unroll
           for (int i = 0; i < 128; ++i) s[i] = first + i < len ? s[i] : -INFINITY;
@@ -754,7 +794,7 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<kScored>& sh, uint32_t tm
           m_ref = m_new;
         }
       };
-      if (__any_sync(0xffffffffu, m_ref == -INFINITY)) take_tile_max();
+      if (fresh) take_tile_max();
       // keys at or past the end of the sequence may hold anything: zero their V rows (only the
       // unit's last K/V tile can reach them; tile A zeroes it when it uses that tile)
       // (scored: nor are keys before the first visible one known, in the unit's first tile)
@@ -801,9 +841,64 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<kScored>& sh, uint32_t tm
         const float2 rsum = __fadd2_rn(rs01, rs23);
         return rsum.x + rsum.y;
       };
-      float rsum = exponents();
-      if (__any_sync(0xffffffffu, !(rsum <= kSumLimit))) {  // rare: re-reference this tile
+      // the same from raw scores, none of them masked and no key past its query
+      float z_max = 0.f;
+      auto ruled_exponents = [&]() -> float {
+        float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                        make_float2(0.f, 0.f)};
+        float zm[2] = {0.f, 0.f};
+        // bias slope * (k - p) less the reference: slope * i + base
+        const float base = (kRules & kBiased) != 0
+                               ? fmaf(slope, static_cast<float>(kv_base - (un.c + jt)), -m_ref)
+                               : -m_ref;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int at = c * 32 + 2 * i;
+            const float2 y = make_float2(s[at], s[at + 1]);
+            float2 t = make_float2(base, base), f = scale2;
+            if constexpr ((kRules & kBiased) != 0)
+              t = make_float2(fmaf(slope, static_cast<float>(at), base),
+                              fmaf(slope, static_cast<float>(at + 1), base));
+            if constexpr ((kRules & kCapped) != 0) {
+              const float2 z = __fmul2_rn(y, y);
+              zm[i & 1] = fmax3(zm[i & 1], z.x, z.y);
+              f = __ffma2_rn(cap2[3], z, cap2[2]);
+              f = __ffma2_rn(f, z, cap2[1]);
+              f = __ffma2_rn(f, z, cap2[0]);
+            }
+            const float2 e = __ffma2_rn(y, f, t);
+            const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+            rs[i & 3] = __fadd2_rn(rs[i & 3], p);
+            pk[i] = pack_bf16x2(p.x, p.y);
+          }
+          tc::st16(col_s + c * 16, pk);
+        }
+        z_max = fmaxf(zm[0], zm[1]);
+        const float2 rs01 = __fadd2_rn(rs[0], rs[1]), rs23 = __fadd2_rn(rs[2], rs[3]);
+        const float2 rsum = __fadd2_rn(rs01, rs23);
+        return rsum.x + rsum.y;
+      };
+      float rsum;
+      if constexpr (ruled) rsum = fused ? ruled_exponents() : exponents();
+      else rsum = exponents();
+      bool again = !(rsum <= kSumLimit);
+      if constexpr ((kRules & kCapped) != 0) again = again || z_max > a.cap_z;
+      if (__any_sync(0xffffffffu, again)) {  // rare: re-reference this tile
         tc::wait_st();
+        if constexpr (ruled) {
+          if (fused) {
+            // (the empty asm keeps the squares and polynomials of the pass before, 128 of each,
+            // from being carried in registers to here)
+#pragma unroll
+            for (int i = 0; i < 128; ++i) asm volatile("" : "+f"(s[i]));
+            rule_scores(kv_base);
+          }
+          if constexpr ((kRules & kCapped) != 0)
+            far = far || __any_sync(0xffffffffu, z_max > a.cap_z);
+        }
         take_tile_max();
         rsum = exponents();
       }
@@ -864,6 +959,12 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<kScored>& sh, uint32_t tm
         else if (!(l > 0.f)) wa = 0.f;
 #pragma unroll
         for (int i = 0; i < HD; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * wa);
+        if constexpr (kScored) {
+          if (blind) {
+#pragma unroll
+            for (int i = 0; i < HD; ++i) o[i] = 0;
+          }
+        }
         if (cas) {
 #pragma unroll
           for (int ps = 0; ps < kMaxPrefixSplits; ++ps) {
@@ -900,12 +1001,13 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<kScored>& sh, uint32_t tm
   }
 }
 
-template <int HD, bool kScored>
+template <int HD, int kRules>
 __global__ void __launch_bounds__(TcCfg<HD>::kThreads, 1)
     attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap qmap,
                            const __grid_constant__ CUtensorMap kmap,
                            const __grid_constant__ CUtensorMap vmap, const AttnArgs a) {
   using C = TcCfg<HD>;
+  constexpr bool kScored = is_scored(kRules);
   extern __shared__ uint8_t smem_raw[];
   __shared__ TcShared<kScored> sh;
   const int tid = threadIdx.x, warp = tid >> 5;
@@ -988,12 +1090,12 @@ __global__ void __launch_bounds__(TcCfg<HD>::kThreads, 1)
         using D = DecCfg<HD>;
         const int w = warp - 4;
         // a decode-first CTA's warps start on units rank x 8 + w without the counter
-        decode_warp<HD, kScored>(&kmap, &vmap, a, sh.dec_bars[w],
+        decode_warp<HD, kRules>(&kmap, &vmap, a, sh.dec_bars[w],
                                  base + w * D::kStages * D::kStageBytes,
                                  base_ptr + w * D::kStages * D::kStageBytes,
                                  decode_first ? sh.role_rank * a.decode_warps_per_cta + w : -1);
       } else {
-        softmax_wg<HD, kScored>(a, sh, tmem, base_ptr, (warp >> 2) - 1);
+        softmax_wg<HD, kRules>(a, sh, tmem, base_ptr, (warp >> 2) - 1);
       }
       phase_end();
     }
@@ -1004,7 +1106,7 @@ __global__ void __launch_bounds__(TcCfg<HD>::kThreads, 1)
   }
 }
 
-template <int HD, bool kScored>
+template <int HD, int kRules>
 rb_status launch_hd(const AttnArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                     const CUtensorMap& vmap, cudaStream_t s) {
   using C = TcCfg<HD>;
@@ -1012,14 +1114,14 @@ rb_status launch_hd(const AttnArgs& a, const CUtensorMap& qmap, const CUtensorMa
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return RB_ERR_CUDA;
   if (!configured[dev]) {
-    if (cudaFuncSetAttribute(attn_prefill_tc_kernel<HD, kScored>,
+    if (cudaFuncSetAttribute(attn_prefill_tc_kernel<HD, kRules>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::kSmemBytes) != cudaSuccess)
       return RB_ERR_CUDA;
     configured[dev] = true;
   }
   const int grid = max(1, device_sm_count());
-  attn_prefill_tc_kernel<HD, kScored><<<grid, C::kThreads, C::kSmemBytes, s>>>(qmap, kmap, vmap, a);
+  attn_prefill_tc_kernel<HD, kRules><<<grid, C::kThreads, C::kSmemBytes, s>>>(qmap, kmap, vmap, a);
   if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
   note_launches(1);
   return RB_OK;
@@ -1029,11 +1131,18 @@ rb_status launch_hd(const AttnArgs& a, const CUtensorMap& qmap, const CUtensorMa
 
 rb_status launch_prefill_tc(const AttnArgs& a, int head_dim, const CUtensorMap& qmap,
                             const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
-  if (a.scored)
-    return head_dim == 128 ? launch_hd<128, true>(a, qmap, kmap, vmap, s)
-                           : launch_hd<64, true>(a, qmap, kmap, vmap, s);
-  return head_dim == 128 ? launch_hd<128, false>(a, qmap, kmap, vmap, s)
-                         : launch_hd<64, false>(a, qmap, kmap, vmap, s);
+  auto launch = [&](auto rules) {
+    constexpr int kRules = decltype(rules)::value;
+    return head_dim == 128 ? launch_hd<128, kRules>(a, qmap, kmap, vmap, s)
+                           : launch_hd<64, kRules>(a, qmap, kmap, vmap, s);
+  };
+  switch (a.rules) {
+    case kOrdinary: return launch(std::integral_constant<int, kOrdinary>{});
+    case kMasked: return launch(std::integral_constant<int, kMasked>{});
+    case kMasked | kCapped: return launch(std::integral_constant<int, kMasked | kCapped>{});
+    case kMasked | kBiased: return launch(std::integral_constant<int, kMasked | kBiased>{});
+    default: return launch(std::integral_constant<int, kMasked | kCapped | kBiased>{});
+  }
 }
 
 }  // namespace attn
