@@ -213,18 +213,18 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _stream_on(device, stream) -> ctypes.c_void_p:
+def _stream_on(device, stream) -> int:
     """The stream to launch on for tensors of ``device``, which must be the current one."""
     import torch
 
     if device.index != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    elif stream.device != device:
+    if stream is None:  # (a Stream object for it costs 3 us of host time, a third of a call)
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream.device != device:
         raise ValueError(f"the stream belongs to {stream.device}, the tensors are on {device}")
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def launch_count() -> int:

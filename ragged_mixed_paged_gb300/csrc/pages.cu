@@ -13,15 +13,22 @@
 //            free page number j below, and the table entries follow
 //
 // Copies move whole 16-byte chunks and are bound by HBM (2 x page bytes); everything else is a
-// few dependent passes over the counts and is bound by latency.
+// few dependent passes over the counts and is bound by latency, so each call is few launches: one
+// for copy and free, two (a plan by one CTA or one cluster, then the grid that copies) for fork
+// and compact.
+#include <cooperative_groups.h>
+
 #include "rb_internal.cuh"
 
 namespace rb {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kCopyThreads = 256;
 constexpr int kCheckThreads = 1024;
-constexpr int kScan = 2048;  // reference counts per CTA of a compaction's passes
+constexpr int kClusterCtas = 8;     // free and compact's plan: one cluster
+constexpr int kCopyPerSm = 32;      // CTAs of a copy per SM, most of them queued
 
 struct PageArgs {
   int rows, MB, entries, null_entry, page_tokens;
@@ -35,30 +42,27 @@ struct PageArgs {
   int32_t* err;
 };
 
-// Workspace: [mark / code: entries][list a: entries][list b: entries][chunk counts][header]
+// Workspace: [mark / code: entries][list a: entries][list b: entries][header]
 struct PagesWs {
-  int32_t *code, *movers, *holes, *counts, *header;
+  int32_t *code, *movers, *holes, *header;
 };
-enum HeaderInt : int { kHOk = 0, kHMoves = 1, kHLive = 2, kHInts = 16 };
+constexpr int kHeaderInts = 16;  // [0]: the fork plan holds; [1]: pages compact moves
 
 __host__ __device__ inline size_t up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 inline size_t ws_bytes(int entries, int rows) {
   const size_t list = up(sizeof(int32_t) * static_cast<size_t>(entries > rows ? entries : rows));
-  const size_t counts = up(sizeof(int32_t) * (static_cast<size_t>(entries) / kScan + 2));
-  return 3 * list + counts + up(kHInts * sizeof(int32_t));
+  return 3 * list + up(kHeaderInts * sizeof(int32_t));
 }
 
 inline PagesWs ws_of(void* p, int entries, int rows) {
   const size_t list = up(sizeof(int32_t) * static_cast<size_t>(entries > rows ? entries : rows));
-  const size_t counts = up(sizeof(int32_t) * (static_cast<size_t>(entries) / kScan + 2));
   unsigned char* b = static_cast<unsigned char*>(p);
   PagesWs w;
   w.code = reinterpret_cast<int32_t*>(b);
   w.movers = reinterpret_cast<int32_t*>(b + list);
   w.holes = reinterpret_cast<int32_t*>(b + 2 * list);
-  w.counts = reinterpret_cast<int32_t*>(b + 3 * list);
-  w.header = reinterpret_cast<int32_t*>(b + 3 * list + counts);
+  w.header = reinterpret_cast<int32_t*>(b + 3 * list);
   return w;
 }
 
@@ -66,19 +70,54 @@ __device__ __forceinline__ bool valid_page(const PageArgs& a, int id) {
   return id >= 0 && id < a.entries && id != a.null_entry;
 }
 
-// One page-sized run of 16-byte chunks, by one CTA's threads.
+// 16-byte chunks [first, last) of a page by one CTA's threads, kUnroll loads in flight each.
+template <int kUnroll>
 __device__ __forceinline__ void copy_chunks(int4* dst, const int4* src, long long first,
                                             long long last, int tid, int threads) {
-  constexpr int kUnroll = 4;
-  long long i = first + tid;
-  for (; i + (kUnroll - 1) * threads < last; i += kUnroll * threads) {
+  for (long long i = first + tid; i < last; i += kUnroll * threads) {
     int4 x[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) x[u] = src[i + u * threads];
+    for (int u = 0; u < kUnroll; ++u)
+      if (i + u * threads < last) x[u] = src[i + u * threads];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) dst[i + u * threads] = x[u];
+    for (int u = 0; u < kUnroll; ++u)
+      if (i + u * threads < last) dst[i + u * threads] = x[u];
   }
-  for (; i < last; i += threads) dst[i] = src[i];
+}
+
+// K and V of n pages, page src(i) to page dst(i) (negative: skipped), by CTAs `cta` of `ctas`.  A
+// unit of work is kUnroll chunks per thread of one page; `once(i)` runs in one thread for each i.
+template <int kUnroll, class Src, class Dst, class Once>
+__device__ __forceinline__ void copy_units(const PageArgs& a, long long n, int cta, int ctas,
+                                           Src&& src, Dst&& dst, Once&& once) {
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const long long chunk = static_cast<long long>(kUnroll) * threads;
+  const long long parts = (a.page_chunks + chunk - 1) / chunk, units = 2 * n * parts;
+  for (long long u = cta; u < units; u += ctas) {
+    const long long i = u / (2 * parts), rest = u - i * 2 * parts;
+    const int s = src(i), d = dst(i);
+    if (s < 0 || d < 0) continue;
+    if (rest == 0 && tid == 0) once(i);
+    int4* base = rest >= parts ? a.v : a.k;
+    const long long c0 = (rest >= parts ? rest - parts : rest) * chunk;
+    copy_chunks<kUnroll>(base + d * a.page_chunks, base + s * a.page_chunks, c0,
+                         min(a.page_chunks, c0 + chunk), tid, threads);
+  }
+}
+
+// Few pages are cut into many small units, so that every CTA has one; many pages are copied with
+// four 16-byte loads in flight per thread.  Measured on 8191 pairs of 2 x 32 KiB pages with
+// 256-thread CTAs: 178 us (6.0 TB/s) with 8 CTAs per SM, each taking many units, 164 us (6.5
+// TB/s) with 32 per SM, most of them queued; 16-byte loads eight at a time 170 and 164 us; bulk
+// copies through shared memory 166 us at their best shape, up to 237 us at others.
+template <class Src, class Dst, class Once>
+__device__ __forceinline__ void copy_pages(const PageArgs& a, long long n, int cta, int ctas,
+                                           Src&& src, Dst&& dst, Once&& once) {
+  const long long wide = 4LL * blockDim.x;
+  if (2 * n * ((a.page_chunks + wide - 1) / wide) >= ctas)
+    copy_units<4>(a, n, cta, ctas, src, dst, once);
+  else
+    copy_units<1>(a, n, cta, ctas, src, dst, once);
 }
 
 // ------------------------------------------------------------------------------------- count
@@ -131,22 +170,16 @@ __global__ void __launch_bounds__(kCopyThreads)
     if (bits) raise_error(a.err, bits);
     return;
   }
-  const int first = blockIdx.x - 1, step = gridDim.x - 1;
-  const long long chunk = 4 * kCopyThreads;
-  const long long parts = (a.page_chunks + chunk - 1) / chunk;
-  const long long units = 2LL * n * parts;
-  for (long long u = first; u < units; u += step) {
-    const long long i = u / (2 * parts), rest = u - i * 2 * parts;
-    const int s = __ldg(src + i), d = __ldg(dst + i);
-    if (!valid_page(a, s) || !valid_page(a, d)) continue;
-    int4* base = rest >= parts ? a.v : a.k;
-    const long long c0 = (rest >= parts ? rest - parts : rest) * chunk;
-    copy_chunks(base + d * a.page_chunks, base + s * a.page_chunks, c0,
-                min(a.page_chunks, c0 + chunk), tid, kCopyThreads);
-  }
+  auto page = [&](const int32_t* list, long long i) {
+    const int id = __ldg(list + i);
+    return valid_page(a, id) ? id : -1;
+  };
+  copy_pages(
+      a, n, blockIdx.x - 1, gridDim.x - 1, [&](long long i) { return page(src, i); },
+      [&](long long i) { return page(dst, i); }, [](long long) {});
 }
 
-// Exclusive prefix sum over a block of kCheckThreads threads; *total gets the block's sum.
+// Exclusive prefix sum over the block; *total gets the block's sum.
 __device__ int block_prefix(int v, int* tmp, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   int x = v;
@@ -209,20 +242,28 @@ __global__ void __launch_bounds__(kCheckThreads)
   }
   // the need lowest free pages
   __syncthreads();
+  constexpr int kPer = 16;  // counts per thread and round: 16 loads in flight, one block scan
   int found = 0;
-  for (int base = 0; base < a.entries && found < need; base += kCheckThreads) {
-    const int id = base + tid;
-    const int is_free = id < a.entries && id != a.null_entry && a.ref[id] == 0;
+  for (int base = 0; base < a.entries && found < need; base += kPer * kCheckThreads) {
+    const int id0 = base + kPer * tid;
+    unsigned free_bits = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int id = id0 + k;
+      if (id < a.entries && id != a.null_entry && a.ref[id] == 0) free_bits |= 1u << k;
+    }
     int total;
-    const int at = found + block_prefix(is_free, tmp, &total);
-    if (is_free && at < need) free_list[at] = id;
+    int at = found + block_prefix(__popc(free_bits), tmp, &total);
+    for (; free_bits != 0 && at < need; free_bits &= free_bits - 1)
+      free_list[at++] = id0 + __ffs(free_bits) - 1;
     found += total;
   }
+  found = min(found, need);
   if (found < need) bits |= RB_EBIT_NO_PAGE;
   if (bits) atomicOr(&s_bits, bits);
   __syncthreads();
   if (tid == 0) {
-    header[kHOk] = s_bits == 0;
+    header[0] = s_bits == 0;
     if (s_bits) raise_error(a.err, s_bits);
   }
   for (int i = tid; i < n; i += kCheckThreads)
@@ -232,7 +273,7 @@ __global__ void __launch_bounds__(kCheckThreads)
 __global__ void __launch_bounds__(kCopyThreads)
     fork_apply_kernel(PageArgs a, int n, const int32_t* src, const int32_t* dst,
                       const int32_t* cached, const int32_t* fresh, const int32_t* header) {
-  if (!header[kHOk]) return;
+  if (!header[0]) return;
   const int i = blockIdx.x, tid = threadIdx.x;
   const int s = src[i], d = dst[i], c = cached[s];
   const int full = c / a.page_tokens, tail = c - full * a.page_tokens;
@@ -253,52 +294,79 @@ __global__ void __launch_bounds__(kCopyThreads)
     }
     if (valid_page(a, old)) {
       const long long count = static_cast<long long>(tail) * a.token_chunks;
-      copy_chunks(a.k + page * a.page_chunks, a.k + old * a.page_chunks, 0, count, tid,
-                  kCopyThreads);
-      copy_chunks(a.v + page * a.page_chunks, a.v + old * a.page_chunks, 0, count, tid,
-                  kCopyThreads);
+      copy_chunks<4>(a.k + page * a.page_chunks, a.k + old * a.page_chunks, 0, count, tid,
+                     kCopyThreads);
+      copy_chunks<4>(a.v + page * a.page_chunks, a.v + old * a.page_chunks, 0, count, tid,
+                     kCopyThreads);
     }
   }
   if (tid == 0) a.num_blocks[d] = full + (tail > 0);
 }
 
 // -------------------------------------------------------------------------------------- free
-__global__ void __launch_bounds__(256)
-    pages_free_kernel(PageArgs a, const int32_t* list, int32_t* num_freed) {
-  __shared__ int s_n;
-  const int r = list[blockIdx.x];
-  if (r < 0 || r >= a.rows) {
-    if (threadIdx.x == 0) raise_error(a.err, RB_EBIT_ROW);
-    return;
-  }
-  // the first CTA to take the row's count frees it; a row named twice is then empty
-  if (threadIdx.x == 0) s_n = atomicExch(a.num_blocks + r, 0);
+// One cluster of 8 CTAs, a warp per row: the CTAs' numbers of freed pages meet in shared memory,
+// so the total needs no cleared counter (a memset before the launch cost more than the launch).
+__global__ void __launch_bounds__(kCheckThreads) __cluster_dims__(kClusterCtas, 1, 1)
+    pages_free_kernel(PageArgs a, int n, const int32_t* list, int32_t* num_freed) {
+  __shared__ int s_freed;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) s_freed = 0;
   __syncthreads();
-  const int n = s_n;
-  if (n < 0 || n > a.MB) {
-    if (threadIdx.x == 0) raise_error(a.err, RB_EBIT_ROW);
-    return;
-  }
-  int freed = 0;
-  for (int j = threadIdx.x; j < n; j += blockDim.x) {
-    int32_t* e = a.table + static_cast<size_t>(r) * a.MB + j;
-    const int id = *e;
-    *e = -1;
-    if (!valid_page(a, id)) {
-      raise_error(a.err, RB_EBIT_BLOCK_ID);
+  int freed = 0, bits = 0;
+  constexpr int kWarps = kCheckThreads / 32;
+  for (int i = (threadIdx.x >> 5) * kClusterCtas + blockIdx.x; i < n; i += kWarps * kClusterCtas) {
+    const int r = __ldg(list + i);
+    if (r < 0 || r >= a.rows) {
+      bits |= RB_EBIT_ROW;
       continue;
     }
-    const int was = atomicSub(a.ref + id, 1);
-    if (was < 1) {
-      atomicAdd(a.ref + id, 1);
-      raise_error(a.err, RB_EBIT_PAGE_REF);
+    // the first warp to take the row's count frees it; a row named twice is then empty
+    int held = 0;
+    if (lane == 0) held = atomicExch(a.num_blocks + r, 0);
+    held = __shfl_sync(0xffffffffu, held, 0);
+    if (held < 0 || held > a.MB) {
+      bits |= RB_EBIT_ROW;
+      continue;
     }
-    freed += was == 1;
+    int32_t* row = a.table + static_cast<size_t>(r) * a.MB;
+    auto drop = [&](int id) {
+      if (!valid_page(a, id)) {
+        bits |= RB_EBIT_BLOCK_ID;
+        return;
+      }
+      const int was = atomicSub(a.ref + id, 1);
+      if (was < 1) {
+        atomicAdd(a.ref + id, 1);
+        bits |= RB_EBIT_PAGE_REF;
+      }
+      freed += was == 1;
+    };
+    constexpr int kPer = 4;
+    for (int j = lane; j < held; j += kPer * 32) {
+      int id[kPer];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        if (j + 32 * k < held) id[k] = row[j + 32 * k];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        if (j + 32 * k < held) {
+          row[j + 32 * k] = -1;
+          drop(id[k]);
+        }
+    }
   }
-  if (num_freed != nullptr) {
-    for (int o = 16; o > 0; o >>= 1) freed += __shfl_xor_sync(0xffffffffu, freed, o);
-    if ((threadIdx.x & 31) == 0 && freed) atomicAdd(num_freed, freed);
+  if (bits) raise_error(a.err, bits);
+  if (num_freed == nullptr) return;
+  freed = __reduce_add_sync(0xffffffffu, freed);
+  if (lane == 0 && freed) atomicAdd(&s_freed, freed);
+  cluster.sync();
+  if (blockIdx.x == 0 && threadIdx.x < 32) {
+    int sum = lane < kClusterCtas ? *cluster.map_shared_rank(&s_freed, lane) : 0;
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == 0) *num_freed = sum;
   }
+  cluster.sync();  // nobody leaves while its sum may be read
 }
 
 // ----------------------------------------------------------------------------------- compact
@@ -306,80 +374,89 @@ __device__ __forceinline__ int is_live(const PageArgs& a, int id) {
   return id < a.entries && id != a.null_entry && a.ref[id] > 0;
 }
 
-__global__ void __launch_bounds__(kCheckThreads)
-    compact_count_kernel(PageArgs a, int32_t* counts) {
-  __shared__ int s_n;
-  if (threadIdx.x == 0) s_n = 0;
+// Plan, by one cluster: each CTA counts the live pages of its range of ids, the counts meet in
+// shared memory, and each CTA classifies its ids (code[id] = id where it stays or is the reserved
+// page, -1 if free, -2 - m for mover number m) and lists movers and holes.  A cooperative grid that
+// did plan and copies in one launch took 10 us more host time than the two launches.
+__global__ void __launch_bounds__(kCheckThreads) __cluster_dims__(kClusterCtas, 1, 1)
+    compact_plan_kernel(PageArgs a, PagesWs w, int32_t* num_live) {
+  __shared__ int tmp[32];
+  __shared__ int s_count, s_low;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, cta = blockIdx.x;
+  const int per = (a.entries + kClusterCtas - 1) / kClusterCtas;
+  const int begin = min(a.entries, cta * per), end = min(a.entries, begin + per);
+  if (tid == 0) s_count = s_low = 0;
   __syncthreads();
   int n = 0, bits = 0;
-  for (int k = threadIdx.x; k < kScan; k += kCheckThreads) {
-    const int id = blockIdx.x * kScan + k;
-    n += is_live(a, id);
-    if (id < a.entries && id != a.null_entry && a.ref[id] < 0) bits |= RB_EBIT_PAGE_REF;
+#pragma unroll 4
+  for (int id = begin + tid; id < end; id += kCheckThreads) {
+    const int held = id != a.null_entry ? a.ref[id] : 0;
+    n += held > 0;
+    if (held < 0) bits |= RB_EBIT_PAGE_REF;
   }
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  if ((threadIdx.x & 31) == 0) atomicAdd(&s_n, n);
-  __syncthreads();
-  if (threadIdx.x == 0) counts[blockIdx.x] = s_n;
   if (bits) raise_error(a.err, bits);
-}
-
-// Classifies the ids of one chunk: code[id] = id (stays, or the null page), -1 (free), or
-// -2 - m for mover number m; lists the movers and the holes they go to.
-__global__ void __launch_bounds__(kCheckThreads)
-    compact_list_kernel(PageArgs a, PagesWs w, int chunks, int32_t* num_live) {
-  __shared__ int tmp[32];
-  __shared__ int s_before, s_total, s_low;
-  const int tid = threadIdx.x;
-  // live pages in all, and before this chunk
-  if (tid == 0) s_before = s_total = s_low = 0;
-  __syncthreads();
-  int before = 0, total = 0;
-  for (int c = tid; c < chunks; c += kCheckThreads) {
-    const int n = w.counts[c];
-    total += n;
-    before += c < static_cast<int>(blockIdx.x) ? n : 0;
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0 && n) atomicAdd(&s_count, n);
+  cluster.sync();
+  // live pages in all, below this range, and already in the packed region: every id below
+  // `limit` but the reserved page
+  int before = 0, total = 0, low = 0;
+  int counts[kClusterCtas];
+#pragma unroll
+  for (int c = 0; c < kClusterCtas; ++c) {
+    counts[c] = *cluster.map_shared_rank(&s_count, c);
+    total += counts[c];
+    before += c < cta ? counts[c] : 0;
   }
-  atomicAdd(&s_before, before);
-  atomicAdd(&s_total, total);
-  __syncthreads();
-  before = s_before;
-  total = s_total;
-  // the packed region is every id below `limit` but the null page; live pages already in it
   const int limit = total + (a.null_entry <= total);
-  const int at = limit / kScan;  // its last chunk, partly inside
-  int low = 0;
-  for (int c = tid; c < min(at, chunks); c += kCheckThreads) low += w.counts[c];
-  for (int id = at * kScan + tid; id < min(limit, a.entries); id += kCheckThreads)
-    low += is_live(a, id);
-  atomicAdd(&s_low, low);
+  const int part = limit / per;  // the range partly inside
+#pragma unroll
+  for (int c = 0; c < kClusterCtas; ++c) low += c < part ? counts[c] : 0;
+  n = 0;
+#pragma unroll 4
+  for (int id = part * per + tid; id < min(limit, a.entries); id += kCheckThreads)
+    n += is_live(a, id);
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0 && n) atomicAdd(&s_low, n);
   __syncthreads();
-  low = s_low;
-  if (blockIdx.x == 0 && tid == 0) {
-    w.header[kHMoves] = total - low;
+  low += s_low;
+  if (cta == 0 && tid == 0) {
+    w.header[1] = total - low;
     if (num_live != nullptr) *num_live = total;
   }
-  int rank = before;  // live pages below the id
-  for (int k = 0; k < kScan; k += kCheckThreads) {
-    const int id = blockIdx.x * kScan + k + tid;
-    const int live = is_live(a, id);
+  constexpr int kPer = 4;  // ids per thread and block scan
+  int rank = before;       // live pages below the id
+  for (int base = begin; base < end; base += kPer * kCheckThreads) {
+    const int id0 = base + kPer * tid;
+    unsigned live = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (id0 + k < end && is_live(a, id0 + k)) live |= 1u << k;
     int all;
-    const int mine = rank + block_prefix(live, tmp, &all);
+    int mine = rank + block_prefix(__popc(live), tmp, &all);
     rank += all;
-    if (id >= a.entries) continue;
-    int code = -1;
-    if (id == a.null_entry) {
-      code = id;
-    } else if (live) {
-      code = id < limit ? id : -2 - (mine - low);
-      if (id >= limit) w.movers[mine - low] = id;
-    } else if (id < limit) {
-      w.holes[id - (id > a.null_entry) - mine] = id;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int id = id0 + k;
+      if (id >= end) break;
+      int code = -1;
+      if (id == a.null_entry) {
+        code = id;
+      } else if (live >> k & 1) {
+        code = id < limit ? id : -2 - (mine - low);
+        if (id >= limit) w.movers[mine - low] = id;
+        ++mine;
+      } else if (id < limit) {
+        w.holes[id - (id > a.null_entry) - mine] = id;
+      }
+      w.code[id] = code;
     }
-    w.code[id] = code;
   }
+  cluster.sync();  // nobody leaves while its count may be read
 }
 
+// The table's entries and the map, by the first `table_ctas` CTAs; the pages, by the others.
 __global__ void __launch_bounds__(kCopyThreads)
     compact_move_kernel(PageArgs a, PagesWs w, int32_t* page_map, int table_ctas) {
   const int tid = threadIdx.x;
@@ -388,7 +465,6 @@ __global__ void __launch_bounds__(kCopyThreads)
     return c <= -2 ? w.holes[-2 - c] : c;
   };
   if (static_cast<int>(blockIdx.x) < table_ctas) {
-    // the page table's entries, and the map
     for (int r = blockIdx.x; r < a.rows; r += table_ctas) {
       const int n = a.num_blocks[r];
       if (n < 0 || n > a.MB) {
@@ -409,25 +485,23 @@ __global__ void __launch_bounds__(kCopyThreads)
         page_map[id] = moved(id);
     return;
   }
-  const int moves = w.header[kHMoves];
-  const long long chunk = 4 * kCopyThreads;
-  const long long parts = (a.page_chunks + chunk - 1) / chunk;
-  const long long units = 2LL * moves * parts;
-  for (long long u = blockIdx.x - table_ctas; u < units; u += gridDim.x - table_ctas) {
-    const long long i = u / (2 * parts), rest = u - i * 2 * parts;
-    const int s = w.movers[i], d = w.holes[i];
-    if (rest == 0 && tid == 0) {
-      a.ref[d] = a.ref[s];
-      a.ref[s] = 0;
-    }
-    int4* base = rest >= parts ? a.v : a.k;
-    const long long c0 = (rest >= parts ? rest - parts : rest) * chunk;
-    copy_chunks(base + d * a.page_chunks, base + s * a.page_chunks, c0,
-                min(a.page_chunks, c0 + chunk), tid, kCopyThreads);
-  }
+  copy_pages(
+      a, w.header[1], blockIdx.x - table_ctas, gridDim.x - table_ctas,
+      [&](long long i) { return w.movers[i]; }, [&](long long i) { return w.holes[i]; },
+      [&](long long i) {  // (nothing in this launch reads the counts)
+        a.ref[w.holes[i]] = a.ref[w.movers[i]];
+        a.ref[w.movers[i]] = 0;
+      });
 }
 
 // ---------------------------------------------------------------------------------- host side
+// CTAs of a grid that copies at most `pages` pages.
+int copy_grid(const PageArgs& a, long long pages) {
+  const long long units = 2 * pages * ((a.page_chunks + kCopyThreads - 1) / kCopyThreads);
+  const long long most = static_cast<long long>(kCopyPerSm) * max(1, device_sm_count());
+  return static_cast<int>(units < most ? units : most);
+}
+
 // Checks what every entry point shares and fills `a`.  `tables`, the caches and the workspace
 // are checked only where the entry point uses them.
 rb_status setup(const rb_dims* dims, const rb_page_tables* t, bool use_tables, void* d_k,
@@ -517,10 +591,7 @@ extern "C" rb_status rb_pages_copy(const rb_dims* dims, int32_t num_pairs, const
   if (num_pairs > a.entries) return RB_ERR_CAPACITY;
   if (num_pairs == 0) return RB_OK;
   if (d_src == nullptr || d_dst == nullptr) return RB_ERR_INVALID_ARG;
-  const long long chunk = 4 * kCopyThreads;
-  const long long units = 2LL * num_pairs * ((a.page_chunks + chunk - 1) / chunk);
-  const long long most = 8LL * max(1, device_sm_count());
-  const int grid = 1 + static_cast<int>(units < most ? units : most);
+  const int grid = 1 + copy_grid(a, num_pairs);
   pages_copy_kernel<<<grid, kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(
       a, num_pairs, d_src, d_dst, ws_of(d_workspace, a.entries, dims->max_num_reqs).code);
   if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
@@ -568,11 +639,9 @@ extern "C" rb_status rb_pages_free(const rb_dims* dims, const rb_page_tables* ta
                        d_error_word, &a);
   if (st != RB_OK) return st;
   if (num_free < 0 || (num_free > 0 && d_rows == nullptr)) return RB_ERR_INVALID_ARG;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d_num_freed != nullptr && cudaMemsetAsync(d_num_freed, 0, sizeof(int32_t), s) != cudaSuccess)
-    return RB_ERR_CUDA;
-  if (num_free == 0) return RB_OK;
-  pages_free_kernel<<<num_free, 256, 0, s>>>(a, d_rows, d_num_freed);
+  if (num_free == 0 && d_num_freed == nullptr) return RB_OK;
+  pages_free_kernel<<<kClusterCtas, kCheckThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+      a, num_free, d_rows, d_num_freed);
   if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
   note_launches(1);
   return RB_OK;
@@ -590,16 +659,14 @@ extern "C" rb_status rb_pages_compact(const rb_dims* dims, const rb_page_tables*
   if (st != RB_OK) return st;
   const PagesWs w = ws_of(d_workspace, a.entries, dims->max_num_reqs);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int chunks = (a.entries + kScan - 1) / kScan;
-  compact_count_kernel<<<chunks, kCheckThreads, 0, s>>>(a, w.counts);
+  compact_plan_kernel<<<kClusterCtas, kCheckThreads, 0, s>>>(a, w, d_num_live);
   if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
   note_launches(1);
-  compact_list_kernel<<<chunks, kCheckThreads, 0, s>>>(a, w, chunks, d_num_live);
-  if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
-  note_launches(1);
-  const int sms = max(1, device_sm_count());
-  const int table_ctas = min(max(a.rows, 1), sms);
-  compact_move_kernel<<<table_ctas + 8 * sms, kCopyThreads, 0, s>>>(a, w, d_page_map, table_ctas);
+  const int table_ctas = 
+      min(max(a.rows, (a.entries + 4095) / 4096), max(1, device_sm_count()));
+  // at most half of the pages move
+  const int grid = table_ctas + copy_grid(a, a.entries / 2);
+  compact_move_kernel<<<grid, kCopyThreads, 0, s>>>(a, w, d_page_map, table_ctas);
   if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
   note_launches(1);
   return RB_OK;

@@ -12,9 +12,14 @@
 // x_i it saw.  ln Z and H follow from s and w.  The difference comes before the factor, so the
 // terms that matter (x_i near r) keep their bits however large the logits are.
 //
-// The top k takes no part in that loop but the threads' maxima: the k-th largest maximum of
-// 128 lane groups bounds the k-th largest logit from below, only threads whose maximum reaches
-// it hold candidates, and their share of the row (about k of 512) is read again, from L2.
+// The top k takes no part in that loop but maxima: each thread keeps the largest logit of each of
+// up to four segments of its share.  The k-th largest of 128 lane groups' maxima bounds the k-th
+// largest logit from below; only segments whose maximum reaches it hold candidates, about k of
+// the 1024 of a CTA, and those are read again (mostly from L2).
+//
+// Bound by HBM for many rows, by the chain of dependent steps (about 8 us) for few.  The next
+// batch of 16-byte loads is issued before the current one is worked on, and four CTAs per SM of
+// 256 threads hide each other's selection step.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
@@ -25,9 +30,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kGroups = 128;      // lane groups (of 4 threads) whose maxima bound the k-th logit
+constexpr int kGroups = 128;      // lane groups (of 2 threads) whose maxima bound the k-th logit
+constexpr int kSegments = 4;      // of a thread's share of the row, each with its own maximum
 constexpr int kMaxTop = 32;
 constexpr int kMaxSplits = 8;     // CTAs of a cluster that share one row
 constexpr int kCandidates = 1024;
@@ -134,107 +140,126 @@ __device__ __forceinline__ bool before(const Entry& a, const Entry& b) {  // a r
   return a.x > b.x || (a.x == b.x && a.i < b.i);
 }
 
-struct Part {  // what one CTA of a row's cluster found
+struct Part {  // what one thread, warp, CTA or cluster found
   Sums sums;
   float max;
-  int above, top;
+  int above;
+  __device__ __forceinline__ void merge(const Part& o) {
+    sums.merge(o.sums);
+    max = fmaxf(max, o.max);
+    above += o.above;
+  }
+  __device__ __forceinline__ Part from_lane(int mask) const {
+    Part q;
+    q.sums.ref = __shfl_xor_sync(0xffffffffu, sums.ref, mask);
+    q.sums.s = __shfl_xor_sync(0xffffffffu, sums.s, mask);
+    q.sums.w = __shfl_xor_sync(0xffffffffu, sums.w, mask);
+    q.max = __shfl_xor_sync(0xffffffffu, max, mask);
+    q.above = __shfl_xor_sync(0xffffffffu, above, mask);
+    return q;
+  }
 };
+__device__ __forceinline__ Part no_part() { return Part{Sums{kLowest, 0.f, 0.f}, -INFINITY, 0}; }
 
 struct Shared {
+  alignas(16) float group_max[kGroups];  // read four at a time
   Part warp[kWarps];
   Part part;
-  Entry best[kMaxTop];
-  alignas(16) float group_max[kGroups];  // read four at a time
+  Part parts[kMaxSplits];  // first CTA of a cluster: the others' sums
   float tau;
-  int n_threads, n_cand, found, fill;
-  unsigned short threads[kThreads];
+  int n_shares, n_cand;
+  unsigned short shares[kThreads * kSegments];  // (thread, segment) pairs with candidates
   Entry cand[kCandidates];
   Entry red[kWarps];
   int warp_count[kWarps];
-  Entry merged[kMaxSplits * kMaxTop];
+  Entry best[kMaxTop];
+  Entry merged[kMaxSplits * kMaxTop];  // first CTA of a cluster: every CTA's entries
 };
 
-// One CTA's part of a row: 16-byte vectors [v0, v1) of the row's aligned vectors.
+// One CTA's part of a row: 16-byte vectors [v0, v1) of the row's aligned vectors, of which
+// [w0, w1) lie wholly in the row; the elements before and after those are taken one by one.
 template <class T>
 struct Slice {
   using E = Elem<T>;
   const T* row;
-  int vocab, off, v0, v1;  // off: elements of vector 0 that lie before the row
+  int vocab, off, v0, v1, w0, w1;  // off: elements of vector 0 that lie before the row
 
   __device__ __forceinline__ int first(int v) const { return v * E::kPer - off; }
-  __device__ __forceinline__ bool whole(int v) const {
-    return first(v) >= 0 && first(v) + E::kPer <= vocab;
+  __device__ __forceinline__ void bound() {
+    w0 = v0;
+    if (w0 < v1 && first(w0) < 0) ++w0;
+    w1 = max(w0, first(v1) > vocab ? v1 - 1 : v1);
   }
   __device__ __forceinline__ uint4 load(int v) const {
     return __ldg(reinterpret_cast<const uint4*>(row + first(v)));
   }
   __device__ __forceinline__ int lo() const { return max(0, first(v0)); }
   __device__ __forceinline__ int hi() const { return min(vocab, first(v1)); }
-  // fn(x, index) for each element of vector v that is in the row
-  template <class F>
-  __device__ __forceinline__ void each(int v, F&& fn) const {
-    if (whole(v)) {
-      float2 x[E::kPer / 2];
-      E::unpack(load(v), x);
-#pragma unroll
-      for (int k = 0; k < E::kPer / 2; ++k) {
-        fn(x[k].x, first(v) + 2 * k);
-        fn(x[k].y, first(v) + 2 * k + 1);
-      }
-    } else {
-      for (int i = max(0, first(v)); i < min(vocab, first(v) + E::kPer); ++i)
-        fn(E::one(row + i), i);
-    }
+  // The element outside the whole vectors that thread t takes (threads 0 to 31), or -1: those
+  // before vector w0 and those from vector w1 on, at most 7 of each.
+  __device__ __forceinline__ int edge(int t) const {
+    const int lo_ = lo(), hi_ = hi(), front = min(hi_, first(w0)) - lo_;
+    if (t < 16) return t < front ? lo_ + t : -1;
+    const int i = max(lo_ + max(front, 0), first(w1)) + t - 16;
+    return t < 32 && i < hi_ ? i : -1;
   }
 };
 
-// The top entries of a slice in order, into sh.best; returns how many (min(k, elements)).
-// `mine`: the largest element this thread read (vectors v0 + tid, + kThreads, ...).
-template <class T>
-__device__ int slice_top(const Slice<T>& sl, int k, float mine, Shared& sh) {
+// The top entries of a slice, in order, through emit(rank, entry); returns how many there are
+// (min(k, elements)).  Thread t read vectors w0 + t + j * kThreads; segment g of its share are
+// j in [g * per, (g + 1) * per), with maximum seg[g]; `edge_x` is its edge element (edge_i >= 0).
+template <class T, class Emit>
+__device__ __forceinline__ int slice_top(const Slice<T>& sl, int k, const float (&seg)[kSegments],
+                                         int per, float edge_x, int edge_i, Shared& sh,
+                                         Emit&& emit) {
+  using E = Elem<T>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int count = max(0, sl.hi() - sl.lo());
-  const int want = min(k, count);
+  const int want = min(k, max(0, sl.hi() - sl.lo()));
   if (want == 0) return 0;
-  float g = mine;
-  g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1));
-  g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
-  if ((lane & 3) == 0) sh.group_max[tid >> 2] = g;
-  if (tid == 0) sh.n_threads = sh.n_cand = 0;
-  __syncthreads();
-  if (tid < kGroups) {
-    const float x = sh.group_max[tid];
+  {  // rank of each group's maximum, half of the others per thread
+    const int g = tid >> 1, half = tid & 1;
+    const float x = sh.group_max[g];
     int rank = 0;
 #pragma unroll 4
-    for (int j = 0; j < kGroups; j += 4) {
+    for (int j = half * (kGroups / 2); j < (half + 1) * (kGroups / 2); j += 4) {
       const float4 o = *reinterpret_cast<const float4*>(sh.group_max + j);
-      rank += (o.x > x) + (o.y > x) + (o.z > x) + (o.w > x);
-      rank += (o.x == x && j < tid) + (o.y == x && j + 1 < tid) + (o.z == x && j + 2 < tid) +
-              (o.w == x && j + 3 < tid);
+      rank += (o.x > x || (o.x == x && j < g)) + (o.y > x || (o.y == x && j + 1 < g)) +
+              (o.z > x || (o.z == x && j + 2 < g)) + (o.w > x || (o.w == x && j + 3 < g));
     }
-    if (rank == want - 1) sh.tau = x;
+    rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+    if (half == 0 && rank == want - 1) sh.tau = x;
   }
   __syncthreads();
   const float tau = sh.tau;  // at least `want` elements are >= tau (-inf: fewer groups had any)
   // Many elements equal to tau (masked logits above all): take those above it, then the first
   // equal ones in the order of their index.
   const bool many = tau == -INFINITY;
-  if (mine > tau || (!many && mine == tau))
-    sh.threads[atomicAdd(&sh.n_threads, 1)] = static_cast<unsigned short>(tid);
+#pragma unroll
+  for (int g = 0; g < kSegments; ++g)
+    if (seg[g] > tau || (!many && seg[g] == tau))
+      sh.shares[atomicAdd(&sh.n_shares, 1)] = static_cast<unsigned short>(tid + g * kThreads);
   __syncthreads();
-  const int n_threads = sh.n_threads;
-  const int per = (sl.v1 - sl.v0 + kThreads - 1) / kThreads;
+  const int work = sh.n_shares * per;
   auto collect = [&](bool ties) {
-    for (int w = tid; w < n_threads * per; w += kThreads) {
-      const int v = sl.v0 + sh.threads[w % n_threads] + (w / n_threads) * kThreads;
-      if (v >= sl.v1) continue;
-      sl.each(v, [&](float x, int i) {
-        if (x > tau || (ties && x == tau)) {
-          const int c = atomicAdd(&sh.n_cand, 1);
-          if (c < kCandidates) sh.cand[c] = Entry{x, i};
-        }
-      });
+    auto check = [&](float x, int i) {
+      if (x > tau || (ties && x == tau)) {
+        const int c = atomicAdd(&sh.n_cand, 1);
+        if (c < kCandidates) sh.cand[c] = Entry{x, i};
+      }
+    };
+    for (int w = tid; w < work; w += kThreads) {
+      const int q = sh.shares[w / per];
+      const int v = sl.w0 + q % kThreads + (q / kThreads * per + w % per) * kThreads;
+      if (v >= sl.w1) continue;
+      float2 x[E::kPer / 2];
+      E::unpack(sl.load(v), x);
+#pragma unroll
+      for (int j = 0; j < E::kPer / 2; ++j) {
+        check(x[j].x, sl.first(v) + 2 * j);
+        check(x[j].y, sl.first(v) + 2 * j + 1);
+      }
     }
+    if (edge_i >= 0) check(edge_x, edge_i);
     __syncthreads();
   };
   if (!many) collect(true);
@@ -248,7 +273,7 @@ __device__ int slice_top(const Slice<T>& sl, int k, float mine, Shared& sh) {
       __syncthreads();
       for (int base = sl.lo(); base < sl.hi() && have < want; base += kThreads) {
         const int i = base + tid;
-        const bool hit = i < sl.hi() && Elem<T>::one(sl.row + i) == tau;
+        const bool hit = i < sl.hi() && E::one(sl.row + i) == tau;
         const unsigned m = __ballot_sync(0xffffffffu, hit);
         if (lane == 0) sh.warp_count[warp] = __popc(m);
         __syncthreads();
@@ -273,20 +298,18 @@ __device__ int slice_top(const Slice<T>& sl, int k, float mine, Shared& sh) {
       const Entry e = sh.cand[c];
       int rank = 0;
       for (int j = 0; j < n; ++j) rank += before(sh.cand[j], e);
-      if (rank < want) sh.best[rank] = e;
+      if (rank < want) emit(rank, e);
     }
-    __syncthreads();
     return want;
   }
   // More candidates than the buffer holds even so: one selection over the slice per entry.
   Entry last{INFINITY, -1};
   for (int s = 0; s < want; ++s) {
     Entry e{-INFINITY, 0x7fffffff};
-    for (int v = sl.v0 + tid; v < sl.v1; v += kThreads)
-      sl.each(v, [&](float x, int i) {
-        const Entry c{x, i};
-        if (before(last, c) && before(c, e)) e = c;
-      });
+    for (int i = sl.lo() + tid; i < sl.hi(); i += kThreads) {
+      const Entry c{E::one(sl.row + i), i};
+      if (before(last, c) && before(c, e)) e = c;
+    }
     for (int o = 16; o > 0; o >>= 1) {
       const Entry c{__shfl_xor_sync(0xffffffffu, e.x, o), __shfl_xor_sync(0xffffffffu, e.i, o)};
       if (before(c, e)) e = c;
@@ -296,17 +319,35 @@ __device__ int slice_top(const Slice<T>& sl, int k, float mine, Shared& sh) {
     e = sh.red[0];
     for (int w = 1; w < kWarps; ++w)
       if (before(sh.red[w], e)) e = sh.red[w];
-    if (tid == 0) sh.best[s] = e;
+    if (tid == 0) emit(s, e);
     last = e;
     __syncthreads();
   }
   return want;
 }
 
+// What a row's sums give: bad (NaN or +inf: no distribution), none (every logit is -inf: nothing
+// has probability), ln Z relative to the maximum, and the entropy.
+struct RowResult {
+  bool bad, none;
+  float max, ln_z, entropy;
+  __device__ __forceinline__ explicit RowResult(const Part& p)
+      : bad(isnan(p.sums.s) || p.max == INFINITY), none(p.max == -INFINITY), max(p.max) {
+    Sums z = p.sums;
+    z.move_to(p.max);
+    const float log2z = log2f(z.s);
+    ln_z = kLn2 * log2z;
+    entropy = bad ? NAN : none ? 0.f : fmaxf(0.f, kLn2 * (log2z - z.w / z.s));
+  }
+  __device__ __forceinline__ float logprob(float x) const {
+    return bad ? NAN : (none || x == -INFINITY) ? -INFINITY : (x - max) - ln_z;
+  }
+};
+
 template <class T>
-__global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(LogprobArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs a) {
   using E = Elem<T>;
-  __shared__ __align__(16) Shared sh;
+  __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int splits = static_cast<int>(cluster.num_blocks());
   const int split = static_cast<int>(cluster.block_rank());
@@ -321,160 +362,145 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(LogprobArgs
   const int per_split = (nvec + splits - 1) / splits;
   sl.v0 = min(nvec, split * per_split);
   sl.v1 = min(nvec, sl.v0 + per_split);
+  sl.bound();
 
+  const int stop = sl.w1;
+  uint4 next[kBatch];
+  auto fetch = [&](int v) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (v + k * kThreads < stop) next[k] = sl.load(v + k * kThreads);
+  };
+  fetch(sl.w0 + tid);
   const int token = a.tokens != nullptr ? __ldg(a.tokens + r) : -1;
   const bool has_token = token >= 0 && token < a.vocab;
   const float xt = has_token ? E::one(sl.row + token) : INFINITY;
+  const int edge_i = tid < 32 ? sl.edge(tid) : -1;
+  const float edge_x = edge_i >= 0 ? E::one(sl.row + edge_i) : -INFINITY;
+  if (tid == 0) sh.n_shares = sh.n_cand = 0;
 
-  Sums sums{kLowest, 0.f, 0.f};
-  float mine = -INFINITY;  // largest element this thread read
-  int above = 0;
-  auto add_one = [&](float x) {
-    mine = fmaxf(mine, x);
-    above += x > xt;
-    if (x > sums.ref + kGrowth) sums.move_to(x);
-    const float t = max_nan(x - sums.ref, kFar) * kLog2e, e = fast_exp2(t);
-    sums.s += e;
-    sums.w = fmaf(e, t, sums.w);
-  };
-  // ends of the row that do not fill a vector, then the whole vectors
-  int b0 = sl.v0, b1 = sl.v1;
-  if (b0 < b1 && !sl.whole(b0)) {
-    if (tid == 0) sl.each(b0, [&](float x, int) { add_one(x); });
+  Part mine = no_part();
+  Sums& sums = mine.sums;
+  if (edge_i >= 0) {
+    mine.max = edge_x;
+    mine.above = edge_x > xt;
+    if (edge_x > sums.ref + kGrowth) sums.move_to(edge_x);
+    const float t = max_nan(edge_x - sums.ref, kFar) * kLog2e;
+    sums.s = fast_exp2(t);
+    sums.w = sums.s * t;
   }
-  if (b1 - 1 > b0 && !sl.whole(b1 - 1)) {
-    if (tid == (b1 - 1 - b0) % kThreads) sl.each(b1 - 1, [&](float x, int) { add_one(x); });
-    --b1;
-  }
-  const bool skip_first = b0 < b1 && !sl.whole(b0);
-  for (int v = b0 + tid; v < b1; v += kBatch * kThreads) {
-    uint4 u[kBatch];
-    bool on[kBatch];
+  // a thread's share: `batches` rounds of kBatch vectors, cut into segments of `seg_batches`
+  const int batches = (stop - sl.w0 + kBatch * kThreads - 1) / (kBatch * kThreads);
+  const int seg_batches = max(1, (batches + kSegments - 1) / kSegments);
+  float seg[kSegments];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int vk = v + k * kThreads;
-      on[k] = vk < b1 && !(skip_first && vk == b0);
-      if (on[k]) u[k] = sl.load(vk);
-    }
+  for (int g = 0; g < kSegments; ++g) {
+    float top = -INFINITY;  // largest element of this segment
+    for (int b = g * seg_batches; b < min(batches, (g + 1) * seg_batches); ++b) {
+      const int v = sl.w0 + tid + b * (kBatch * kThreads);
+      uint4 u[kBatch];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (!on[k]) continue;
-      float2 x[E::kPer / 2];
-      E::unpack(u[k], x);
-      float mx = fmaxf(x[0].x, x[0].y);
+      for (int k = 0; k < kBatch; ++k) u[k] = next[k];
+      fetch(v + kBatch * kThreads);
 #pragma unroll
-      for (int j = 1; j < E::kPer / 2; ++j) mx = fmax3(mx, x[j].x, x[j].y);
-      mine = fmaxf(mine, mx);
-      if (mx > xt) {
+      for (int k = 0; k < kBatch; ++k) {
+        if (v + k * kThreads >= stop) break;
+        float2 x[E::kPer / 2];
+        E::unpack(u[k], x);
+        float mx = fmaxf(x[0].x, x[0].y);
 #pragma unroll
-        for (int j = 0; j < E::kPer / 2; ++j) above += (x[j].x > xt) + (x[j].y > xt);
+        for (int j = 1; j < E::kPer / 2; ++j) mx = fmax3(mx, x[j].x, x[j].y);
+        top = fmaxf(top, mx);
+        if (mx > xt) {
+#pragma unroll
+          for (int j = 0; j < E::kPer / 2; ++j) mine.above += (x[j].x > xt) + (x[j].y > xt);
+        }
+        if (mx > sums.ref + kGrowth) sums.move_to(mx);
+        const float2 l2 = make_float2(kLog2e, kLog2e), nr = make_float2(-sums.ref, -sums.ref);
+        float2 s2 = make_float2(0.f, 0.f), w2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < E::kPer / 2; ++j) {
+          const float2 d = __fadd2_rn(x[j], nr);
+          const float2 t = __fmul2_rn(make_float2(max_nan(d.x, kFar), max_nan(d.y, kFar)), l2);
+          const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+          s2 = __fadd2_rn(s2, e);
+          w2 = __ffma2_rn(e, t, w2);
+        }
+        sums.s += s2.x + s2.y;
+        sums.w += w2.x + w2.y;
       }
-      if (mx > sums.ref + kGrowth) sums.move_to(mx);
-      const float2 l2 = make_float2(kLog2e, kLog2e), nr = make_float2(-sums.ref, -sums.ref);
-      float2 s2 = make_float2(0.f, 0.f), w2 = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int j = 0; j < E::kPer / 2; ++j) {
-        const float2 d = __fadd2_rn(x[j], nr);
-        const float2 t = __fmul2_rn(make_float2(max_nan(d.x, kFar), max_nan(d.y, kFar)), l2);
-        const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
-        s2 = __fadd2_rn(s2, e);
-        w2 = __ffma2_rn(e, t, w2);
-      }
-      sums.s += s2.x + s2.y;
-      sums.w += w2.x + w2.y;
     }
+    seg[g] = top;
+    mine.max = fmaxf(mine.max, top);
   }
-
-  // the CTA's sums
-  {
-    Part p{sums, mine, above, 0};
+  const float pair_max = fmaxf(mine.max, __shfl_xor_sync(0xffffffffu, mine.max, 1));
+  if ((lane & 1) == 0) sh.group_max[tid >> 1] = pair_max;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const Sums q{__shfl_xor_sync(0xffffffffu, p.sums.ref, o),
-                   __shfl_xor_sync(0xffffffffu, p.sums.s, o),
-                   __shfl_xor_sync(0xffffffffu, p.sums.w, o)};
-      p.sums.merge(q);
-      p.max = fmaxf(p.max, __shfl_xor_sync(0xffffffffu, p.max, o));
-      p.above += __shfl_xor_sync(0xffffffffu, p.above, o);
-    }
-    if (lane == 0) sh.warp[warp] = p;
-    __syncthreads();
-    if (tid == 0) {
-      for (int w = 1; w < kWarps; ++w) {
-        p.sums.merge(sh.warp[w].sums);
-        p.max = fmaxf(p.max, sh.warp[w].max);
-        p.above += sh.warp[w].above;
-      }
-      sh.part = p;
-    }
-  }
+  for (int o = 16; o > 0; o >>= 1) mine.merge(mine.from_lane(o));
+  if (lane == 0) sh.warp[warp] = mine;
   __syncthreads();
-  int n_top = 0;
-  if (a.top > 0) n_top = slice_top(sl, a.top, mine, sh);
-  if (tid == 0) sh.part.top = n_top;
-  __syncthreads();
+  // the CTA's sums, in every lane
+  Part p = sh.warp[lane % kWarps];
+#pragma unroll
+  for (int o = 1; o < kWarps; o <<= 1) p.merge(p.from_lane(o));
 
-  if (splits > 1) {
-    cluster.sync();
-    if (split == 0) {
-      // every CTA's sums and entries into this one's shared memory
-      if (tid == 0) {
-        for (int c = 1; c < splits; ++c) {
-          const Part q = *cluster.map_shared_rank(&sh.part, c);
-          sh.part.sums.merge(q.sums);
-          sh.part.max = fmaxf(sh.part.max, q.max);
-          sh.part.above += q.above;
-        }
-      }
-      if (a.top > 0) {
-        const Entry none{-INFINITY, 0x7fffffff};
-        for (int c = tid; c < splits * kMaxTop; c += kThreads) {
-          const int from = c / kMaxTop, j = c % kMaxTop;
-          const bool have = j < cluster.map_shared_rank(&sh.part, from)->top;
-          sh.merged[c] = have ? cluster.map_shared_rank(sh.best, from)[j] : none;
-        }
-        __syncthreads();
-        n_top = min(a.top, a.vocab);
-        for (int c = tid; c < splits * kMaxTop; c += kThreads) {
-          const Entry e = sh.merged[c];
-          if (e.i == none.i) continue;
-          int rank = 0;
-          for (int j = 0; j < splits * kMaxTop; ++j) rank += before(sh.merged[j], e);
-          if (rank < n_top) sh.cand[rank] = e;
-        }
-        __syncthreads();
-        for (int c = tid; c < n_top; c += kThreads) sh.best[c] = sh.cand[c];
-      }
+  const long long top_row = static_cast<long long>(r) * a.top;
+  int n_top = min(a.top, a.vocab);
+  if (splits == 1) {
+    const RowResult row(p);
+    if (a.top > 0)
+      slice_top(sl, a.top, seg, seg_batches * kBatch, edge_x, edge_i, sh,
+                [&](int rank, const Entry& e) {
+                  if (row.bad) return;
+                  a.top_ids[top_row + rank] = e.i;
+                  a.top_logprobs[top_row + rank] = row.logprob(e.x);
+                });
+  } else {
+    cluster.sync();  // every CTA has started: its shared memory may be written
+    Shared* first = cluster.map_shared_rank(&sh, 0);
+    if (tid == 0) first->parts[split] = p;
+    if (a.top > 0) {
+      for (int c = tid; c < kMaxTop; c += kThreads)
+        first->merged[split * kMaxTop + c] = Entry{-INFINITY, 0x7fffffff};
       __syncthreads();
+      slice_top(sl, a.top, seg, seg_batches * kBatch, edge_x, edge_i, sh,
+                [&](int rank, const Entry& e) { first->merged[split * kMaxTop + rank] = e; });
     }
-    cluster.sync();  // nobody leaves while another CTA may read its shared memory
+    cluster.sync();
     if (split != 0) return;
+    p = lane % kMaxSplits < splits ? sh.parts[lane % kMaxSplits] : no_part();
+#pragma unroll
+    for (int o = 1; o < kMaxSplits; o <<= 1) p.merge(p.from_lane(o));
+    const RowResult row(p);
+    if (a.top > 0 && !row.bad) {
+      for (int c = tid; c < splits * kMaxTop; c += kThreads) {
+        const Entry e = sh.merged[c];
+        if (e.i == 0x7fffffff) continue;
+        int rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < splits * kMaxTop; ++j) rank += before(sh.merged[j], e);
+        if (rank < n_top) {
+          a.top_ids[top_row + rank] = e.i;
+          a.top_logprobs[top_row + rank] = row.logprob(e.x);
+        }
+      }
+    }
   }
-
-  const Part p = sh.part;
-  const bool bad = isnan(p.sums.s) || p.max == INFINITY;  // NaN or +inf: no distribution
-  const bool none = p.max == -INFINITY;  // every logit is -inf: nothing has probability
-  Sums z = p.sums;
-  z.move_to(p.max);
-  const float log2z = log2f(z.s), ln_z = kLn2 * log2z;
-  auto logprob = [&](float x) {
-    return bad ? NAN : (none || x == -INFINITY) ? -INFINITY : (x - p.max) - ln_z;
-  };
-  if (tid == 0) {
+  if (warp != 0) return;
+  const RowResult row(p);
+  if (lane == 0) {
     int bits = 0;
-    if (bad) bits |= RB_EBIT_LOGITS;
+    if (row.bad) bits |= RB_EBIT_LOGITS;
     if (a.tokens != nullptr && !has_token && token != -1) bits |= RB_EBIT_TOKEN_ID;
     if (bits) raise_error(a.err, bits);
-    if (a.logprobs != nullptr) a.logprobs[r] = has_token ? logprob(xt) : bad ? NAN : 0.f;
-    if (a.ranks != nullptr) a.ranks[r] = has_token && !bad ? 1 + p.above : 0;
-    if (a.entropy != nullptr)
-      a.entropy[r] = bad ? NAN : none ? 0.f : fmaxf(0.f, kLn2 * (log2z - z.w / z.s));
+    if (a.logprobs != nullptr) a.logprobs[r] = has_token ? row.logprob(xt) : row.bad ? NAN : 0.f;
+    if (a.ranks != nullptr) a.ranks[r] = has_token && !row.bad ? 1 + p.above : 0;
+    if (a.entropy != nullptr) a.entropy[r] = row.entropy;
   }
-  if (tid < a.top) {
-    const bool have = tid < n_top && !bad;
-    a.top_ids[static_cast<long long>(r) * a.top + tid] = have ? sh.best[tid].i : -1;
-    a.top_logprobs[static_cast<long long>(r) * a.top + tid] =
-        have ? logprob(sh.best[tid].x) : bad ? NAN : -INFINITY;
+  if (row.bad) n_top = 0;
+  if (lane >= n_top && lane < a.top) {  // entries there is no token for
+    a.top_ids[top_row + lane] = -1;
+    a.top_logprobs[top_row + lane] = row.bad ? NAN : -INFINITY;
   }
 }
 

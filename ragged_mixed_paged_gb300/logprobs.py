@@ -39,9 +39,11 @@ def token_logprobs(logits, token_ids, top_k: int = 0, out: TokenLogprobs = None,
 
     if logits.dim() != 2 or not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor [rows, vocab]")
-    kinds = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-    if logits.dtype not in kinds:
+    f32, i32 = torch.float32, torch.int32
+    kind = {torch.bfloat16: 0, torch.float16: 1, f32: 2}.get(logits.dtype)
+    if kind is None:
         raise ValueError(f"logits must be bf16, fp16 or fp32, got {logits.dtype}")
+    device = logits.device
     rows, vocab = logits.shape
     stride = logits.stride(0) if rows > 1 else vocab
     if vocab > 1 and logits.stride(1) != 1:
@@ -54,7 +56,6 @@ def token_logprobs(logits, token_ids, top_k: int = 0, out: TokenLogprobs = None,
         s = stream if stream is not None else torch.cuda.current_stream(logits.device)
         with torch.cuda.stream(s):
             out = TokenLogprobs.allocate(rows, top_k, logits.device)
-    i32, f32 = torch.int32, torch.float32
     pointers = []
     for name, dtype, shape in (("logprobs", f32, (rows,)), ("ranks", i32, (rows,)),
                                ("entropy", f32, (rows,)), ("top_ids", i32, (rows, top_k)),
@@ -62,14 +63,16 @@ def token_logprobs(logits, token_ids, top_k: int = 0, out: TokenLogprobs = None,
         t = getattr(out, name)
         if t.shape != shape:
             raise ValueError(f"out.{name} must be {list(shape)}")
-        if t.device != logits.device:
-            raise ValueError(f"out.{name} is on {t.device}, the logits are on {logits.device}")
-        pointers.append(rb._ptr(t, dtype, f"out.{name}"))
+        if t.device != device:
+            raise ValueError(f"out.{name} is on {t.device}, the logits are on {device}")
+        if t.dtype != dtype or not t.is_contiguous():
+            rb._ptr(t, dtype, f"out.{name}")  # names what is wrong
+        pointers.append(t.data_ptr())
     for name, t in (("token_ids", token_ids), ("error_word", error_word)):
-        if t is not None and t.device != logits.device:
-            raise ValueError(f"{name} is on {t.device}, the logits are on {logits.device}")
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the logits are on {device}")
     rb._check("rb_token_logprobs", rb.lib.rb_token_logprobs(
-        rows, vocab, stride, kinds[logits.dtype], logits.data_ptr(),
+        rows, vocab, stride, kind, logits.data_ptr(),
         rb._ptr(token_ids, i32, "token_ids"), top_k, *pointers,
-        rb._ptr(error_word, i32, "error_word"), rb._stream_on(logits.device, stream)))
+        rb._ptr(error_word, i32, "error_word"), rb._stream_on(device, stream)))
     return out

@@ -41,6 +41,7 @@ class PagePool:
         self.k_cache, self.v_cache = k_cache, v_cache
         self.block_table, self.num_blocks = block_table, num_blocks
         self.device = k_cache.device
+        self._i32 = torch.int32
         rows = dims.num_blocks * dims.block_size
         for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
             if t.dim() != 3 or tuple(t.shape) != (rows, dims.num_kv_heads, dims.head_dim):
@@ -53,6 +54,7 @@ class PagePool:
         self._err = self._pointer(self.error_word, torch.int32, "error_word")
         self.workspace = (new(max(1, pages_workspace_size(dims)), torch.uint8)
                           if workspace is None else workspace)
+        self._ws_bytes = self.workspace.numel()
         self._ws = self._pointer(self.workspace, torch.uint8, "workspace")
         self._dims = dims.c()
         self._d = ctypes.byref(self._dims)
@@ -78,9 +80,13 @@ class PagePool:
             self.count(stream=stream)
 
     def _pointer(self, t, dtype, name):
-        if t is not None and t.device != self.device:
+        if t is None:
+            return None
+        if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, the caches are on {self.device}")
-        return rb._ptr(t, dtype, name)
+        if t.dtype != dtype or not t.is_contiguous():
+            return rb._ptr(t, dtype, name)  # names what is wrong
+        return t.data_ptr()
 
     def _t(self):
         if self._tables is None:
@@ -90,18 +96,14 @@ class PagePool:
         return ctypes.byref(self._tables)
 
     def _index(self, t, name):
-        import torch
-
         if t.dim() != 1:
             raise ValueError(f"{name} must have one dimension")
-        return self._pointer(t, torch.int32, name)
+        return self._pointer(t, self._i32, name)
 
     def _one(self, t, name):
-        import torch
-
         if t is not None and t.numel() < 1:
             raise ValueError(f"{name} must hold a value")
-        return self._pointer(t, torch.int32, name)
+        return self._pointer(t, self._i32, name)
 
     def count(self, stream=None) -> None:
         """``ref_count`` from the table: the rows that hold each page."""
@@ -114,7 +116,7 @@ class PagePool:
             raise ValueError("src and dst differ in length")
         rb._check("rb_pages_copy", rb.lib.rb_pages_copy(
             self._d, src.numel(), self._index(src, "src"), self._index(dst, "dst"), self._k,
-            self._v, self._ws, self.workspace.numel(), self._err,
+            self._v, self._ws, self._ws_bytes, self._err,
             rb._stream_on(self.device, stream)))
 
     def fork(self, src_rows, dst_rows, num_cached, stream=None) -> None:
@@ -129,7 +131,7 @@ class PagePool:
         rb._check("rb_pages_fork", rb.lib.rb_pages_fork(
             self._d, tables, src_rows.numel(), self._index(src_rows, "src_rows"),
             self._index(dst_rows, "dst_rows"), self._index(num_cached, "num_cached"), self._k,
-            self._v, self._ws, self.workspace.numel(), self._err,
+            self._v, self._ws, self._ws_bytes, self._err,
             rb._stream_on(self.device, stream)))
 
     def free(self, rows, num_freed=None, stream=None) -> None:
@@ -145,4 +147,4 @@ class PagePool:
         rb._check("rb_pages_compact", rb.lib.rb_pages_compact(
             self._d, self._t(), None if page_map is None else self._index(page_map, "page_map"),
             self._one(num_live, "num_live"), self._k, self._v, self._ws,
-            self.workspace.numel(), self._err, rb._stream_on(self.device, stream)))
+            self._ws_bytes, self._err, rb._stream_on(self.device, stream)))
