@@ -137,36 +137,60 @@ __global__ void __launch_bounds__(256) pages_count_kernel(PageArgs a) {
 }
 
 // -------------------------------------------------------------------------------------- copy
+constexpr int kSource = 1 << 30;  // bit of a page's mark: it is a source
+
 // CTA 0 checks the pairs (a destination twice, or also a source) while the others copy: where
 // it finds one the error bit is set and the pages' contents are unspecified.
 __global__ void __launch_bounds__(kCopyThreads)
     pages_copy_kernel(PageArgs a, int n, const int32_t* src, const int32_t* dst, int32_t* mark) {
   const int tid = threadIdx.x;
   if (blockIdx.x == 0) {
+    // eight pairs per thread and round, so that the three passes stay shorter than the copies
+    constexpr int kPer = 8;
     int bits = 0;
-    for (int i = tid; i < n; i += kCopyThreads) {
-      const int s = src[i], d = dst[i];
-      if (s < 0 || d < 0) continue;  // skipped pair
-      if (!valid_page(a, s) || !valid_page(a, d)) {
-        bits |= RB_EBIT_BLOCK_ID;
-        continue;
+    auto each = [&](auto&& fn) {
+      for (int base = tid; base < n; base += kPer * kCopyThreads) {
+        int s[kPer], d[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const int i = base + k * kCopyThreads;
+          s[k] = i < n ? __ldg(src + i) : -1;
+          d[k] = i < n ? __ldg(dst + i) : -1;
+        }
+        fn(s, d);
       }
-      mark[s] = 0;
-      mark[d] = 0;
-    }
+    };
+    each([&](const int (&s)[kPer], const int (&d)[kPer]) {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        if (s[k] < 0 || d[k] < 0) continue;  // skipped pair
+        if (!valid_page(a, s[k]) || !valid_page(a, d[k])) {
+          bits |= RB_EBIT_BLOCK_ID;
+          continue;
+        }
+        mark[s[k]] = 0;
+        mark[d[k]] = 0;
+      }
+    });
     __syncthreads();
-    for (int i = tid; i < n; i += kCopyThreads) {
-      const int s = src[i], d = dst[i];
-      if (!valid_page(a, s) || !valid_page(a, d)) continue;
-      atomicOr(mark + s, 1 << 30);
-      if (atomicAdd(mark + d, 1) & 0xffffff) bits |= RB_EBIT_PAGE_PAIR;
-    }
+    each([&](const int (&s)[kPer], const int (&d)[kPer]) {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        if (!valid_page(a, s[k]) || !valid_page(a, d[k])) continue;
+        atomicOr(mark + s[k], kSource);
+        if (atomicAdd(mark + d[k], 1) & (kSource - 1)) bits |= RB_EBIT_PAGE_PAIR;
+      }
+    });
     __syncthreads();
-    for (int i = tid; i < n; i += kCopyThreads) {
-      const int s = src[i], d = dst[i];
-      if (valid_page(a, s) && valid_page(a, d) && (__ldcg(mark + d) & (1 << 30)))
-        bits |= RB_EBIT_PAGE_PAIR;
-    }
+    each([&](const int (&s)[kPer], const int (&d)[kPer]) {
+      int m[kPer];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        m[k] = valid_page(a, s[k]) && valid_page(a, d[k]) ? __ldcg(mark + d[k]) : 0;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        if (m[k] & kSource) bits |= RB_EBIT_PAGE_PAIR;
+    });
     if (bits) raise_error(a.err, bits);
     return;
   }
