@@ -25,6 +25,7 @@ constexpr int kPlanThreads = 1024;
 
 template <bool kScored>
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnArgs a, int head_dim) {
+  if constexpr (kScored) grid_release();  // the attention launch sets itself up meanwhile
   plan_body<kScored>(a, head_dim, ReqSrc{a.qsl, a.seq_lens, nullptr});
 }
 

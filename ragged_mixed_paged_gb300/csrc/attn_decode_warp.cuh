@@ -57,7 +57,7 @@ __device__ void combine_splits(const AttnArgs& a, int h, int first, int nsplit, 
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
   float lsum = 0.f;
-#pragma unroll 2
+#pragma unroll 4
   for (int sp = 0; sp < nsplit; ++sp) {
     const size_t u = static_cast<size_t>(first + sp * a.nkv + h);
     const float2 ml = __ldcg(a.part_ml + u * kMaxCols + c);

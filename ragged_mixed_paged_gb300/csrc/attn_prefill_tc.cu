@@ -1045,13 +1045,22 @@ __global__ void __launch_bounds__(TcCfg<HD>::kThreads, 1)
     for (int w = 0; w < 8; ++w)
       for (int st = 0; st < DecCfg<128>::kStages; ++st) mbar_init(&sh.dec_bars[w][st], 1);
     sh.abort = 0;
-    sh.role_rank = atomicAdd(a.header + kHRoleNext, 1);
-    sh.decode_first = sh.role_rank < a.header[kHDecodeCtas];
+    if constexpr (!kScored) {
+      sh.role_rank = atomicAdd(a.header + kHRoleNext, 1);
+      sh.decode_first = sh.role_rank < a.header[kHDecodeCtas];
+    }
     fence_barrier_init();
   }
   if (warp == C::kMmaWarp) {
     tc::tmem_alloc(&sh.tmem_base, C::kTmemCols);
     tc::tmem_relinquish();
+  }
+  if constexpr (kScored) {  // launched beside the planner: its results from here on
+    grid_wait();
+    if (tid == 0) {
+      sh.role_rank = atomicAdd(a.header + kHRoleNext, 1);
+      sh.decode_first = sh.role_rank < a.header[kHDecodeCtas];
+    }
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -1121,6 +1130,9 @@ rb_status launch_hd(const AttnArgs& a, const CUtensorMap& qmap, const CUtensorMa
     configured[dev] = true;
   }
   const int grid = max(1, device_sm_count());
+  if constexpr (is_scored(kRules))
+    return launch_after_plan(attn_prefill_tc_kernel<HD, kRules>, grid, C::kThreads, C::kSmemBytes,
+                             s, qmap, kmap, vmap, a);
   attn_prefill_tc_kernel<HD, kRules><<<grid, C::kThreads, C::kSmemBytes, s>>>(qmap, kmap, vmap, a);
   if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
   note_launches(1);

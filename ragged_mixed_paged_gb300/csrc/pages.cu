@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(kCheckThreads)
   __shared__ int tmp[32];
   __shared__ int s_bits;
   const int tid = threadIdx.x;
+  grid_release();
   if (tid == 0) s_bits = 0;
   for (int r = tid; r < a.rows; r += kCheckThreads) claim[r] = 0;
   __syncthreads();
@@ -297,6 +298,7 @@ __global__ void __launch_bounds__(kCheckThreads)
 __global__ void __launch_bounds__(kCopyThreads)
     fork_apply_kernel(PageArgs a, int n, const int32_t* src, const int32_t* dst,
                       const int32_t* cached, const int32_t* fresh, const int32_t* header) {
+  grid_wait();
   if (!header[0]) return;
   const int i = blockIdx.x, tid = threadIdx.x;
   const int s = src[i], d = dst[i], c = cached[s];
@@ -407,6 +409,7 @@ __global__ void __launch_bounds__(kCheckThreads) __cluster_dims__(kClusterCtas, 
   __shared__ int tmp[32];
   __shared__ int s_count, s_low;
   cg::cluster_group cluster = cg::this_cluster();
+  grid_release();
   const int tid = threadIdx.x, lane = tid & 31, cta = blockIdx.x;
   const int per = (a.entries + kClusterCtas - 1) / kClusterCtas;
   const int begin = min(a.entries, cta * per), end = min(a.entries, begin + per);
@@ -484,6 +487,7 @@ __global__ void __launch_bounds__(kCheckThreads) __cluster_dims__(kClusterCtas, 
 __global__ void __launch_bounds__(kCopyThreads)
     compact_move_kernel(PageArgs a, PagesWs w, int32_t* page_map, int table_ctas) {
   const int tid = threadIdx.x;
+  grid_wait();
   auto moved = [&](int id) {
     const int c = w.code[id];
     return c <= -2 ? w.holes[-2 - c] : c;
@@ -646,11 +650,8 @@ extern "C" rb_status rb_pages_fork(const rb_dims* dims, const rb_page_tables* ta
                                                w.header);
   if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
   note_launches(1);
-  fork_apply_kernel<<<num_forks, kCopyThreads, 0, s>>>(a, num_forks, d_src_rows, d_dst_rows,
-                                                       d_num_cached, w.movers, w.header);
-  if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
-  note_launches(1);
-  return RB_OK;
+  return launch_after_plan(fork_apply_kernel, num_forks, kCopyThreads, 0, s, a, num_forks,
+                           d_src_rows, d_dst_rows, d_num_cached, w.movers, w.header);
 }
 
 extern "C" rb_status rb_pages_free(const rb_dims* dims, const rb_page_tables* tables,
@@ -690,8 +691,6 @@ extern "C" rb_status rb_pages_compact(const rb_dims* dims, const rb_page_tables*
       min(max(a.rows, (a.entries + 4095) / 4096), max(1, device_sm_count()));
   // at most half of the pages move
   const int grid = table_ctas + copy_grid(a, a.entries / 2);
-  compact_move_kernel<<<grid, kCopyThreads, 0, s>>>(a, w, d_page_map, table_ctas);
-  if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
-  note_launches(1);
-  return RB_OK;
+  return launch_after_plan(compact_move_kernel, grid, kCopyThreads, 0, s, a, w, d_page_map,
+                           table_ctas);
 }

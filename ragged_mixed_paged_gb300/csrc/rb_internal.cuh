@@ -60,9 +60,41 @@ bool encode_kv_tensor_map(CUtensorMap* map, const void* base, int head_dim, int 
 bool encode_q_tensor_map(CUtensorMap* map, const void* base, int head_dim, int num_q_heads,
                          long long num_tokens, int group);
 
+// Launches `kernel` so that it may start while the kernel before it on the stream still runs
+// (programmatic dependent launch): the kernel calls grid_wait() before it touches anything the
+// one before it writes or reads.  Saves the launch latency between a plan and its grid.
+template <class... Params, class... Args>
+rb_status launch_after_plan(void (*kernel)(Params...), int grid, int threads, size_t smem,
+                            cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...) != cudaSuccess)
+    return RB_ERR_CUDA;
+  note_launches(1);
+  return RB_OK;
+}
+
 // ---------------------------------------------------------------------------------------------
 // device side
 // ---------------------------------------------------------------------------------------------
+// Waits until the kernels before this one on the stream have completed, their writes visible.
+__device__ __forceinline__ void grid_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Lets the next kernel of the stream start (one launched with launch_after_plan: it still waits
+// for this one's end where it calls grid_wait).
+__device__ __forceinline__ void grid_release() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __device__ __forceinline__ void raise_error(int32_t* err, int32_t bit) {
   if (err != nullptr) atomicOr(err, bit);
 }
