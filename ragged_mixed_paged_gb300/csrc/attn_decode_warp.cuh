@@ -35,43 +35,57 @@ struct DecCfg {
   static constexpr int kKS = HD / 16;
 };
 
-// Log-sum-exp merge of the split partials of one (request, kv head) by one warp: 4 lanes per
-// column (8 columns), each lane owning a quarter of head_dim; the split maxima are also spread
-// over the 4 lanes.  Partials written by other SMs are read through L2 (ld.global.cg).
-template <int HD>
-__device__ void combine_splits(const AttnArgs& a, int h, int first, int nsplit, int t0,
-                               int cols) {
-  constexpr int kLanesPerCol = 4;
-  constexpr int kPer = HD / kLanesPerCol;  // values of one column per lane
+// Log-sum-exp merge of the split partials of one (request, kv head) by one warp, kLanes lanes per
+// column, each lane owning that part of head_dim; the split maxima are also spread over the
+// lanes.  Partials written by other SMs are read through L2 (ld.global.cg), kBatch splits' loads
+// in flight at a time: a merge of 20 splits is a chain of L2 round trips, 8 to 16 us of a small
+// decode call when each waited for its own.
+template <int HD, int kLanes>
+__device__ void combine_columns(const AttnArgs& a, int h, int first, int nsplit, int t0,
+                                int cols) {
+  constexpr int kPer = HD / kLanes;         // values of one column per lane
+  constexpr int kVec = kPer / 4;
+  constexpr int kBatch = 16 / kVec;         // 16 four-value loads in flight
   const int lane = threadIdx.x & 31;
-  const int col = lane / kLanesPerCol, part = lane % kLanesPerCol;
+  const int col = lane / kLanes, part = lane % kLanes;
   const bool active = col < cols;
   const int c = active ? col : 0;
   float mx = -INFINITY;
-  for (int sp = part; sp < nsplit; sp += kLanesPerCol)
+#pragma unroll 2
+  for (int sp = part; sp < nsplit; sp += kLanes)
     mx = fmaxf(mx, __ldcg(&a.part_ml[static_cast<size_t>(first + sp * a.nkv + h) * kMaxCols + c].x));
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   if (mx == -INFINITY) mx = 0.f;
   float acc[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
   float lsum = 0.f;
-#pragma unroll 4
-  for (int sp = 0; sp < nsplit; ++sp) {
-    const size_t u = static_cast<size_t>(first + sp * a.nkv + h);
-    const float2 ml = __ldcg(a.part_ml + u * kMaxCols + c);
-    const float w = fast_exp2(ml.x - mx);
-    lsum += w * ml.y;
-    const float4* o = reinterpret_cast<const float4*>(a.part_o + (u * kMaxCols + c) * HD +
-                                                      part * kPer);
+#pragma unroll 1
+  for (int sp0 = 0; sp0 < nsplit; sp0 += kBatch) {
+    float2 ml[kBatch];
+    float4 x[kBatch][kVec];
 #pragma unroll
-    for (int v = 0; v < kPer / 4; ++v) {
-      const float4 x = __ldcg(o + v);
-      acc[4 * v + 0] += w * x.x;
-      acc[4 * v + 1] += w * x.y;
-      acc[4 * v + 2] += w * x.z;
-      acc[4 * v + 3] += w * x.w;
+    for (int k = 0; k < kBatch; ++k) {
+      const size_t u = static_cast<size_t>(first + min(sp0 + k, nsplit - 1) * a.nkv + h);
+      ml[k] = __ldcg(a.part_ml + u * kMaxCols + c);
+      const float4* o = reinterpret_cast<const float4*>(a.part_o + (u * kMaxCols + c) * HD +
+                                                        part * kPer);
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) x[k][v] = __ldcg(o + v);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (sp0 + k >= nsplit) break;
+      const float w = fast_exp2(ml[k].x - mx);
+      lsum += w * ml[k].y;
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) {
+        acc[4 * v + 0] += w * x[k][v].x;
+        acc[4 * v + 1] += w * x[k][v].y;
+        acc[4 * v + 2] += w * x[k][v].z;
+        acc[4 * v + 3] += w * x[k][v].w;
+      }
     }
   }
   if (!active) return;
@@ -88,26 +102,31 @@ __device__ void combine_splits(const AttnArgs& a, int h, int first, int nsplit, 
       if (ps >= a.prefix_splits) break;
       const float4* o1 = reinterpret_cast<const float4*>(cascade_row<HD>(a, ps, row) + part * kPer);
 #pragma unroll
-      for (int v = 0; v < kPer / 4; ++v) {
-        const float4 x = __ldg(o1 + v);
-        acc[4 * v + 0] += x.x * wp[ps];
-        acc[4 * v + 1] += x.y * wp[ps];
-        acc[4 * v + 2] += x.z * wp[ps];
-        acc[4 * v + 3] += x.w * wp[ps];
+      for (int v = 0; v < kVec; ++v) {
+        const float4 y = __ldg(o1 + v);
+        acc[4 * v + 0] += y.x * wp[ps];
+        acc[4 * v + 1] += y.y * wp[ps];
+        acc[4 * v + 2] += y.z * wp[ps];
+        acc[4 * v + 3] += y.w * wp[ps];
       }
     }
     inv = 1.f;
   }
-  uint4* dst = reinterpret_cast<uint4*>(a.out + row * HD + part * kPer);
+  uint2* dst = reinterpret_cast<uint2*>(a.out + row * HD + part * kPer);
 #pragma unroll
-  for (int v = 0; v < kPer / 8; ++v) {
-    uint4 wv;
-    wv.x = pack_bf16x2(acc[8 * v + 0] * inv, acc[8 * v + 1] * inv);
-    wv.y = pack_bf16x2(acc[8 * v + 2] * inv, acc[8 * v + 3] * inv);
-    wv.z = pack_bf16x2(acc[8 * v + 4] * inv, acc[8 * v + 5] * inv);
-    wv.w = pack_bf16x2(acc[8 * v + 6] * inv, acc[8 * v + 7] * inv);
+  for (int v = 0; v < kVec; ++v) {
+    uint2 wv;
+    wv.x = pack_bf16x2(acc[4 * v + 0] * inv, acc[4 * v + 1] * inv);
+    wv.y = pack_bf16x2(acc[4 * v + 2] * inv, acc[4 * v + 3] * inv);
     dst[v] = wv;
   }
+}
+
+template <int HD>
+__device__ void combine_splits(const AttnArgs& a, int h, int first, int nsplit, int t0,
+                               int cols) {
+  if (cols <= 4) combine_columns<HD, 8>(a, h, first, nsplit, t0, cols);
+  else combine_columns<HD, 4>(a, h, first, nsplit, t0, cols);
 }
 
 // One decode warp: pulls (request, kv head, split) units from the shared counter until none
