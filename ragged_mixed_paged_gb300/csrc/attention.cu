@@ -173,8 +173,9 @@ rb_status attn_set_rules(AttnSetup* su, const rb_score_rules* rules, float softm
       if (!fits) z = std::fmin(z, z_without[k]);
       f *= static_cast<double>(a.cap_in) * a.cap_in;
     }
-    a.cap_z = static_cast<float>(
-        std::fmin(3e38, z / (static_cast<double>(a.cap_in) * a.cap_in)));
+    z = std::fmin(1e37, z / (static_cast<double>(a.cap_in) * a.cap_in));
+    a.cap_z = static_cast<float>(z);
+    a.cap_s = static_cast<float>(std::sqrt(z));
   }
   a.slopes = rules->d_head_slopes;
   if (a.slopes != nullptr) a.rules |= kBiased;

@@ -124,7 +124,7 @@ struct AttnArgs {
   int rules;                 // Rules the kernel applies
   float cap_in, cap_log2;    // softcap: score = cap_log2 * tanh(cap_in * q.k) in log2 units
   float cap_poly[4];         // the same as s * (cap_poly[0] + s^2 (cap_poly[1] + ...)), s = q.k
-  float cap_z;               // for s^2 up to cap_z
+  float cap_z, cap_s;        // for s^2 up to cap_z, |s| up to cap_s
   const float* slopes;       // [nh] distance bias -slope * |p - k|, or null
   const int32_t* key_start;  // [N] first visible key of each query token, or null
   const int32_t* prefix;     // [R] keys every query of the request sees, or null
@@ -165,37 +165,20 @@ __device__ __forceinline__ int scored_first_page(const AttnArgs& a, int t0, int 
 constexpr float kTanhPoly[4] = {1.0f, -0.3329871892929077f, 0.12897320091724396f, -0.03759901970624924f};
 constexpr float kTanhZ = 0.5f;
 
-// kCount raw products, in place.
+// kCount raw products, in place.  Both forms are evaluated and one chosen per score: tiles and
+// pages that need their scores in place are few.
 template <int kCount>
 __device__ __forceinline__ void cap_scores(const AttnArgs& a, float (&s)[kCount]) {
-  static_assert(kCount % 4 == 0, "scores are taken in pairs of pairs");
-  float2 y[kCount / 2];
-  float top[2] = {0.f, 0.f};
+  const float in2 = a.cap_in * (2.f * 1.4426950408889634f);
 #pragma unroll
-  for (int i = 0; i < kCount / 2; ++i) {
-    const float2 x = make_float2(s[2 * i], s[2 * i + 1]), z = __fmul2_rn(x, x);
-    top[i & 1] = fmax3(top[i & 1], z.x, z.y);
-    float2 p = make_float2(a.cap_poly[3], a.cap_poly[3]);
-#pragma unroll
-    for (int k = 2; k >= 0; --k) p = __ffma2_rn(p, z, make_float2(a.cap_poly[k], a.cap_poly[k]));
-    y[i] = __fmul2_rn(x, p);
-  }
-  if (__any_sync(0xffffffffu, fmaxf(top[0], top[1]) > a.cap_z)) {
-    const float in2 = a.cap_in * (2.f * 1.4426950408889634f);
-#pragma unroll
-    for (int i = 0; i < kCount; ++i) {
-      float r;
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fast_exp2(s[i] * in2) + 1.f));
-      const float far = fmaf(-2.f * a.cap_log2, r, a.cap_log2);
-      const float near = i & 1 ? y[i / 2].y : y[i / 2].x;
-      s[i] = s[i] * s[i] > a.cap_z ? far : near;  // (a NaN stays one)
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kCount / 2; ++i) {
-      s[2 * i] = y[i].x;
-      s[2 * i + 1] = y[i].y;
-    }
+  for (int i = 0; i < kCount; ++i) {
+    const float z = s[i] * s[i];
+    float f = fmaf(a.cap_poly[3], z, a.cap_poly[2]);
+    f = fmaf(f, z, a.cap_poly[1]);
+    f = fmaf(f, z, a.cap_poly[0]);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fast_exp2(s[i] * in2) + 1.f));
+    s[i] = z > a.cap_z ? fmaf(-2.f * a.cap_log2, r, a.cap_log2) : s[i] * f;  // (NaN stays NaN)
   }
 }
 

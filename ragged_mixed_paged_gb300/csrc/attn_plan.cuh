@@ -100,6 +100,9 @@ __device__ __forceinline__ int scored_pair_tiles(const AttnArgs& a, int t0, int 
 constexpr float kDecUnitUs = 6.f, kDecPageUs = 0.6f, kDecBytesPerUsPerCta = 73e3f;
 constexpr float kHbmBytesPerUs = 6.4e6f;
 constexpr float kPreUnitUs = 8.f, kPreTileUs = 2.3f;
+// What score rules add to a key tile of a prefill unit (chunks alone, 128-key tiles of two 128-row
+// query tiles at head_dim 128: 1.8 us without rules, +0.4 biased, +0.9 capped).
+constexpr float kBiasTileUs = 0.4f, kCapTileUs = 0.9f;
 constexpr int kTileBins = 512;  // histogram bins of prefill units by key tiles (longer: last bin)
 
 // The planner, run by one whole CTA of any size: validates the metadata, classifies requests,
@@ -174,6 +177,8 @@ __device__ __forceinline__ void plan_body(const AttnArgs& a, int head_dim, ReqSr
   __shared__ float s_pre_us;
   __shared__ int s_pre_max;
   const bool fused = a.fused_ctas > 0;
+  const float tile_us = kPreTileUs + ((a.rules & kBiased) != 0 ? kBiasTileUs : 0.f) +
+                        ((a.rules & kCapped) != 0 ? kCapTileUs : 0.f);
   auto key_tiles = [&](int r, int c, int q, int p) {
     if constexpr (kScored) return scored_pair_tiles(a, src.qsl[r], r, c, q, a.tile_tokens, p);
     else return pair_key_tiles(c, q, a.tile_tokens, p);
@@ -211,7 +216,7 @@ __device__ __forceinline__ void plan_body(const AttnArgs& a, int head_dim, ReqSr
     warp_pairs([&](int r, int c, int q, int p) {
       const int n = key_tiles(r, c, q, p);
       atomicAdd(&s_bin[min(n, kTileBins - 1)], 1);
-      my_us += kPreUnitUs + kPreTileUs * n;
+      my_us += kPreUnitUs + tile_us * n;
       my_max = max(my_max, n);
     });
 #pragma unroll
@@ -255,7 +260,7 @@ __device__ __forceinline__ void plan_body(const AttnArgs& a, int head_dim, ReqSr
     const int C = a.fused_ctas;
     const float dec_bytes = static_cast<float>(page_heads) * (2.f * kPage * head_dim * 2.f);
     const float t_unit = kDecUnitUs + kDecPageUs * sp;
-    const float pre_total = s_pre_us * a.nkv, pre_long = kPreUnitUs + kPreTileUs * s_pre_max;
+    const float pre_total = s_pre_us * a.nkv, pre_long = kPreUnitUs + tile_us * s_pre_max;
     auto t_dec = [&](int d) {
       if (tot_d == 0) return 0.f;
       const int waves = (tot_d + a.decode_warps_per_cta * d - 1) / (a.decode_warps_per_cta * d);

@@ -161,6 +161,10 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t phase, volatile 
 // P <= 2^20 keeps P V and the row sum far inside fp32 and bf16 range.
 constexpr float kSumLimit = 1048576.f;
 
+// Soft caps (log2 units) up to which a capped row's reference bounds its exponents from above and
+// below, and how far below the cap that reference may lie.
+constexpr float kMaxBoundedCap = 90.f, kCapHeadroom = 80.f;
+
 __device__ __forceinline__ int tiles_for(int c, int jmax) { return (c + jmax + 1 + 127) / 128; }
 constexpr int kKeysPerTile = 128;  // keys per K/V tile
 
@@ -684,7 +688,13 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<is_scored(kRules)>& sh, u
     // rows with visible keys take the first tile's maximum
     float m_ref = valid ? -INFINITY : 0.f, l = 0.f;
     bool ok = true;
-    bool far = false;  // a score of this unit lay outside the capping polynomial's range
+    // Capped scores are at most cap_log2 (a bias that falls with distance only lowers them), so a
+    // reference of at least cap_log2 - kCapHeadroom keeps every exponent below 2^kCapHeadroom, and a
+    // row's largest score, its own key's at least -cap_log2, keeps its terms above 2^-100 up to
+    // kMaxBoundedCap.  Then no tile is ever taken again, and its scores need not be kept.
+    bool bounded = false;
+    if constexpr ((kRules & kCapped) != 0)
+      bounded = a.cap_log2 <= kMaxBoundedCap && __all_sync(0xffffffffu, slope >= 0.f);
     for (int j = 0; j < n; ++j) {
       const uint32_t tj = tc_x + j;
       if (!wait_all(&sh.s_full[x], tj & 1)) { ok = false; break; }
@@ -715,8 +725,7 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<is_scored(kRules)>& sh, u
       // the rules applied to the tile's scores, in log2 units, in place
       auto rule_scores = [&](int base) {
         if constexpr ((kRules & kCapped) != 0) {
-#pragma unroll
-          for (int c = 0; c < 128; c += 16) cap_scores(a, *reinterpret_cast<float(*)[16]>(s + c));
+          cap_scores(a, s);
         } else if constexpr (ruled) {
 #pragma unroll
           for (int i = 0; i < 128; ++i) s[i] *= a.scale_log2;
@@ -739,7 +748,18 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<is_scored(kRules)>& sh, u
         if constexpr (ruled) {
           // a key past its query, where the distance changes sign, needs |p - k| taken
           const bool past = (kRules & kBiased) != 0 && kv_base + C::kN > un.c + tok_base + 1;
-          fused = !(masked || past || far || fresh);
+          fused = !(masked || past || fresh);
+          if constexpr ((kRules & kCapped) != 0) {
+            fused = fused && bounded;
+            if (fused) {  // every score inside the polynomial's range?
+              float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int i = 0; i < 128; i += 2)
+                top[(i >> 1) & 3] = fmax3(top[(i >> 1) & 3], fabsf(s[i]), fabsf(s[i + 1]));
+              const float most = fmaxf(fmax3(top[0], top[1], top[2]), top[3]);
+              fused = !__any_sync(0xffffffffu, most > a.cap_s);
+            }
+          }
           if (!fused) rule_scores(kv_base);
         }
         if (masked) {
@@ -794,7 +814,11 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<is_scored(kRules)>& sh, u
           m_ref = m_new;
         }
       };
-      if (fresh) take_tile_max();
+      if (fresh) {
+        take_tile_max();
+        if constexpr ((kRules & kCapped) != 0)
+          if (bounded && m_ref != -INFINITY) m_ref = fmaxf(m_ref, a.cap_log2 - kCapHeadroom);
+      }
       // keys at or past the end of the sequence may hold anything: zero their V rows (only the
       // unit's last K/V tile can reach them; tile A zeroes it when it uses that tile)
       // (scored: nor are keys before the first visible one known, in the unit's first tile)
@@ -842,11 +866,9 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<is_scored(kRules)>& sh, u
         return rsum.x + rsum.y;
       };
       // the same from raw scores, none of them masked and no key past its query
-      float z_max = 0.f;
       auto ruled_exponents = [&]() -> float {
         float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                         make_float2(0.f, 0.f)};
-        float zm[2] = {0.f, 0.f};
         // bias slope * (k - p) less the reference: slope * i + base
         const float base = (kRules & kBiased) != 0
                                ? fmaf(slope, static_cast<float>(kv_base - (un.c + jt)), -m_ref)
@@ -864,7 +886,6 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<is_scored(kRules)>& sh, u
                               fmaf(slope, static_cast<float>(at + 1), base));
             if constexpr ((kRules & kCapped) != 0) {
               const float2 z = __fmul2_rn(y, y);
-              zm[i & 1] = fmax3(zm[i & 1], z.x, z.y);
               f = __ffma2_rn(cap2[3], z, cap2[2]);
               f = __ffma2_rn(f, z, cap2[1]);
               f = __ffma2_rn(f, z, cap2[0]);
@@ -876,7 +897,6 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<is_scored(kRules)>& sh, u
           }
           tc::st16(col_s + c * 16, pk);
         }
-        z_max = fmaxf(zm[0], zm[1]);
         const float2 rs01 = __fadd2_rn(rs[0], rs[1]), rs23 = __fadd2_rn(rs[2], rs[3]);
         const float2 rsum = __fadd2_rn(rs01, rs23);
         return rsum.x + rsum.y;
@@ -884,20 +904,19 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<is_scored(kRules)>& sh, u
       float rsum;
       if constexpr (ruled) rsum = fused ? ruled_exponents() : exponents();
       else rsum = exponents();
-      bool again = !(rsum <= kSumLimit);
-      if constexpr ((kRules & kCapped) != 0) again = again || z_max > a.cap_z;
-      if (__any_sync(0xffffffffu, again)) {  // rare: re-reference this tile
+      // rare: re-reference this tile (a capped row with a bounded reference never needs it)
+      constexpr bool capped_rules = (kRules & kCapped) != 0;
+      if (!(capped_rules && fused) &&
+          __any_sync(0xffffffffu, !(rsum <= kSumLimit) && !(capped_rules && bounded))) {
         tc::wait_st();
-        if constexpr (ruled) {
+        if constexpr (ruled && !capped_rules) {
           if (fused) {
-            // (the empty asm keeps the squares and polynomials of the pass before, 128 of each,
-            // from being carried in registers to here)
+            // (the empty asm keeps what the pass before derived from the scores from being
+            // carried in registers to here)
 #pragma unroll
             for (int i = 0; i < 128; ++i) asm volatile("" : "+f"(s[i]));
             rule_scores(kv_base);
           }
-          if constexpr ((kRules & kCapped) != 0)
-            far = far || __any_sync(0xffffffffu, z_max > a.cap_z);
         }
         take_tile_max();
         rsum = exponents();
