@@ -157,6 +157,7 @@ rb_status attn_set_rules(AttnSetup* su, const rb_score_rules* rules, float softm
     return RB_ERR_INVALID_ARG;
   AttnArgs& a = su->a;
   a.rules = kMasked;
+  a.v = static_cast<const __nv_bfloat16*>(su->v_cache);
   if (rules->softcap > 0.f) {
     a.rules |= kCapped;
     a.cap_in = softmax_scale / rules->softcap;

@@ -122,6 +122,7 @@ struct AttnArgs {
   int withhold_first_unit;
   // score rules (rb_paged_attention_scored); the ordinary kernels do not read them
   int rules;                 // Rules the kernel applies
+  const __nv_bfloat16* v;    // V cache
   float cap_in, cap_log2;    // softcap: score = cap_log2 * tanh(cap_in * q.k) in log2 units
   float cap_poly[4];         // the same as s * (cap_poly[0] + s^2 (cap_poly[1] + ...)), s = q.k
   float cap_z, cap_s;        // for s^2 up to cap_z, |s| up to cap_s
@@ -154,6 +155,63 @@ __device__ __forceinline__ int scored_first_page(const AttnArgs& a, int t0, int 
 #pragma unroll 1
   for (int j = 0; j < q; ++j) lo = min(lo, key_lo(a, t0 + j));
   return min(lo / kPage, (L + kPage - 1) / kPage - 1);
+}
+
+// A product of probability 0 with an infinite or NaN value is NaN, so where only some queries of
+// a tile (or page) see a key, a V that is not finite would reach the others' rows.  Such elements
+// are taken out of the staged V (set to 0) and added, as they are, to the results of the rows
+// that see the key: any positive weight times infinity or NaN is that.  (Out of line: rare, and
+// kept out of the attention loops' registers and instruction stream.)
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {  // bit 15 of each bf16 half
+  return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+__device__ __forceinline__ bool not_finite(const uint4& w) {
+  return ((not_finite(w.x) | not_finite(w.y)) | (not_finite(w.z) | not_finite(w.w))) != 0;
+}
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w) {  // the others set to 0
+  const uint32_t f = not_finite(w);
+  return w & ~((f & 0x8000u ? 0xffffu : 0u) | (f & 0x80000000u ? 0xffff0000u : 0u));
+}
+// A warp takes what is not finite out of `count` runs of 512 bytes, `stride` apart, of staged V;
+// returns whether there was any.
+static __device__ __noinline__ bool take_out_not_finite(uint8_t* p, int count, int stride) {
+  p += (threadIdx.x & 31) * 16;
+  bool odd = false;
+#pragma unroll 8
+  for (int i = 0; i < count; ++i) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p + i * stride);
+    odd |= ((not_finite(w.x) | not_finite(w.y)) | (not_finite(w.z) | not_finite(w.w))) != 0;
+  }
+  if (!__any_sync(0xffffffffu, odd)) return false;
+  for (int i = 0; i < count; ++i) {
+    uint4* q = reinterpret_cast<uint4*>(p + i * stride);
+    const uint4 w = *q;
+    *q = make_uint4(finite_halves(w.x), finite_halves(w.y), finite_halves(w.z),
+                    finite_halves(w.w));
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  return true;
+}
+// V row of a request's key, or null where its page id is invalid.
+__device__ __forceinline__ const __nv_bfloat16* v_row(const AttnArgs& a, int r, int h, int key,
+                                                      int head_dim) {
+  const int id = kernel_page(a.block_table + static_cast<size_t>(r) * a.MB, key / kPage, a.ratio,
+                             a.num_blocks, a.null_block);
+  if (id < 0) return nullptr;
+  return a.v + ((static_cast<size_t>(id) * kPage + key % kPage) * a.nkv + h) * head_dim;
+}
+// One thread adds the infinities and NaN in V of keys [k0, k1) to its output row.
+static __device__ __noinline__ void add_not_finite(const AttnArgs& a, int r, int h, int k0, int k1,
+                                                   int head_dim, __nv_bfloat16* out) {
+  for (int key = k0; key < k1; ++key) {
+    const __nv_bfloat16* v = v_row(a, r, h, key, head_dim);
+    if (v == nullptr) continue;
+    for (int d = 0; d < head_dim; ++d) {
+      const float x = __bfloat162float(v[d]);
+      if (!isfinite(x)) out[d] = __float2bfloat16_rn(__bfloat162float(out[d]) + x);
+    }
+  }
 }
 
 // Capped scores (log2 units): cap_log2 * tanh(u), u = cap_in * s.  For u^2 <= kTanhZ tanh(u) =

@@ -129,6 +129,38 @@ __device__ void combine_splits(const AttnArgs& a, int h, int first, int nsplit, 
   else combine_columns<HD, 4>(a, h, first, nsplit, t0, cols);
 }
 
+// A warp adds the infinities and NaN in V of keys [k0, k1) to the results of the columns that see
+// them: the unit's fp32 partial, or (null) the output rows.  The warp has just written them.
+static __device__ __noinline__ void add_not_finite_columns(const AttnArgs& a, int r, int h, int t0,
+                                                           int q, int L, int k0, int k1,
+                                                           int head_dim, float* partial) {
+  __syncwarp();
+  __threadfence();
+  const int prefix = key_prefix(a, r, L);
+  for (int key = k0; key < min(k1, L); ++key) {
+    const __nv_bfloat16* v = v_row(a, r, h, key, head_dim);
+    if (v == nullptr) continue;
+    for (int d = threadIdx.x & 31; d < head_dim; d += 32) {
+      const float x = __bfloat162float(v[d]);
+      if (isfinite(x)) continue;
+      for (int c = 0; c < q * a.group; ++c) {
+        const int j = c / a.group;
+        if (key < key_lo(a, t0 + j) || key >= max(L - q + j + 1, prefix)) continue;
+        if (partial != nullptr) {
+          volatile float* p = partial + c * head_dim + d;
+          *p = *p + x;
+        } else {
+          volatile unsigned short* p = reinterpret_cast<volatile unsigned short*>(
+              a.out + (static_cast<size_t>(t0 + j) * a.nh + h * a.group + c % a.group) * head_dim +
+              d);
+          *p = __bfloat16_as_ushort(
+              __float2bfloat16_rn(__bfloat162float(__ushort_as_bfloat16(*p)) + x));
+        }
+      }
+    }
+  }
+}
+
 // One decode warp: pulls (request, kv head, split) units from the shared counter until none
 // are left.  `bars` are this warp's kStages mbarriers (initialised, count 1) and `wbase` /
 // `wbase_ptr` the shared-memory address / pointer of its kStages stages (1024-byte aligned).
@@ -189,7 +221,7 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
     const int lim1 = c1 < cols ? c + c1 / a.group : c;
     // scored: first visible key, past the last and slope of the lane's two columns, and the
     // first key any column sees
-    int lo0 = 0, lo1 = 0, hi0 = 0, hi1 = 0, lo_all = 0;
+    int lo0 = 0, lo1 = 0, hi0 = 0, hi1 = 0, lo_all = 0, lo_max = 0, hi_min = 0;
     float slope0 = 0.f, slope1 = 0.f;
     if constexpr (kScored) {
       const int j0 = c0 < cols ? c0 / a.group : 0, j1 = c1 < cols ? c1 / a.group : 0;
@@ -204,9 +236,9 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
         slope0 = __ldg(a.slopes + h * a.group + h0) * kLog2e;
         slope1 = __ldg(a.slopes + h * a.group + h1) * kLog2e;
       }
-      lo_all = min(lo0, lo1);
-      lo_all = min(lo_all, __shfl_xor_sync(0xffffffffu, lo_all, 1));
-      lo_all = min(lo_all, __shfl_xor_sync(0xffffffffu, lo_all, 2));
+      lo_all = __reduce_min_sync(0xffffffffu, min(lo0, lo1));
+      lo_max = __reduce_max_sync(0xffffffffu, max(lo0, lo1));
+      hi_min = __reduce_min_sync(0xffffffffu, min(hi0, hi1));
     }
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     float acc[C::kKS][4];
@@ -254,7 +286,7 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
     for (int i = 0; i < C::kStages && i < n_pages; ++i)
       issue(i, (it + i) % C::kStages);
 
-    bool dead = false;
+    bool dead = false, odd = false;  // odd: infinities or NaN were taken out of some page's V
     for (int i = 0; i < n_pages; ++i) {
       const int pg = page_of(i);
       const uint32_t stage = it % C::kStages, phase = (it / C::kStages) & 1u;
@@ -381,6 +413,14 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
           __syncwarp();
         }
       }
+      if constexpr (kScored) {
+        // keys of this page that some columns see and others do not (one token's columns all see
+        // the same keys)
+        if ((lo_all < lo_max && pg * kPage < lo_max) || (hi_min < L && pg * kPage + kPage > hi_min)) {
+          odd |= take_out_not_finite(wbase_ptr + stage * C::kStageBytes + C::kPageBytes,
+                                     C::kPageBytes / 512, 512);
+        }
+      }
       // P^T fragments from S^T's by a register transpose
       const uint32_t pb0 = movmatrix_trans(pack_bf16x2(p0, p1));
       const uint32_t pb1 = movmatrix_trans(pack_bf16x2(p2, p3));
@@ -427,6 +467,9 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
         if (o0) { o0[d0] = __float2bfloat16_rn(acc[mt][0] * inv0); o0[d1] = __float2bfloat16_rn(acc[mt][2] * inv0); }
         if (o1) { o1[d0] = __float2bfloat16_rn(acc[mt][1] * inv1); o1[d1] = __float2bfloat16_rn(acc[mt][3] * inv1); }
       }
+      if constexpr (kScored)
+        if (odd)
+          add_not_finite_columns(a, r, h, t0, q, L, p_begin * kPage, p_end * kPage, HD, nullptr);
     } else {
       float* po = a.part_o + static_cast<size_t>(u) * kMaxCols * HD;
 #pragma unroll
@@ -441,6 +484,8 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
         a.part_ml[static_cast<size_t>(u) * kMaxCols + c0] = make_float2(m0, l0);
         a.part_ml[static_cast<size_t>(u) * kMaxCols + c1] = make_float2(m1, l1);
       }
+      if constexpr (kScored)
+        if (odd) add_not_finite_columns(a, r, h, t0, q, L, p_begin * kPage, p_end * kPage, HD, po);
       // the last split of this (request, kv head) to finish merges all partials
       __threadfence();
       __syncwarp();

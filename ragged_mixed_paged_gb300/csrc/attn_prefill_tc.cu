@@ -101,6 +101,7 @@ struct ScoredUnit : TcUnit {
   int lo;         // first key any row sees
   int prefix;     // keys every row sees (from its own lo on)
   int lo_max[2];  // largest first key of each tile's rows (rows that see no key left out)
+  int odd_first, odd_last;  // key tiles whose V held infinities or NaN that were taken out
 };
 template <bool kScored>
 struct UnitOf {
@@ -280,6 +281,8 @@ __device__ __forceinline__ ScoredUnit scored_unit(const AttnArgs& a, int u, int 
     lo = min(lo, mn);
   }
   un.lo = lo;
+  un.odd_first = 0x7fffffff;
+  un.odd_last = -1;
   const int last_tok = min(un.tok0 + 2 * T, un.q) - 1;
   const int n = (max(un.c + last_tok + 1, un.prefix) + kKeysPerTile - 1) / kKeysPerTile;
   un.j0 = min(lo / kKeysPerTile, n - 1);  // at least one tile, also when no row sees a key
@@ -823,8 +826,14 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<is_scored(kRules)>& sh, u
       // unit's last K/V tile can reach them; tile A zeroes it when it uses that tile)
       // (scored: nor are keys before the first visible one known, in the unit's first tile)
       bool unknown = kv_base + C::kN > un.L;
-      if constexpr (kScored) unknown = unknown || kv_base < un.lo;
-      if (unknown && (x == 0 || j >= un.n[0])) {
+      // scored: keys that some rows of the unit see and others do not
+      bool mixed = false;
+      if constexpr (kScored) {
+        unknown = unknown || kv_base < un.lo;
+        mixed = kv_base < max(un.lo_max[0], un.lo_max[1]) ||
+                kv_base + C::kN > max(un.c + un.tok0 + 1, un.prefix);
+      }
+      if ((unknown || mixed) && (x == 0 || j >= un.n[0])) {
         const uint32_t kt = itk + j, sv = kt % C::kStagesV;
         if (!wait_all(&sh.v_full[sv], (kt / C::kStagesV) & 1)) { ok = false; break; }
         const int kmin = max(un.L - kv_base, 0);
@@ -839,6 +848,20 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<is_scored(kRules)>& sh, u
               *reinterpret_cast<uint4*>(vrow + hf * C::kHalfBytes + c * 16) =
                   make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
+        }
+        if constexpr (kScored) {
+          if (mixed) {  // this warp's 32 keys, 512 bytes at a time
+            __syncwarp();
+            uint8_t* rows = smem_ptr + C::kVOffset + sv * C::kTileBytes + (t >> 5) * 32 * 128;
+            bool odd = false;
+            for (int hf = 0; hf < C::kHalves; ++hf)
+              odd |= take_out_not_finite(rows + hf * C::kHalfBytes, 8, 512);
+            if (odd && lane0) {
+              atomicMin(&sh.units[slot].odd_first, kv_base / C::kN);
+              atomicMax(&sh.units[slot].odd_last, kv_base / C::kN);
+              __threadfence_block();
+            }
+          }
         }
       }
       // exponents and the row sum two columns at a time with the paired fp32 FMA / add
@@ -1013,6 +1036,12 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<is_scored(kRules)>& sh, u
 #pragma unroll
           for (int v = 0; v < HD / 8; ++v)
             reinterpret_cast<uint4*>(dst)[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+        }
+        if constexpr (kScored) {  // V's infinities and NaN that were taken out
+          const volatile auto& now = sh.units[slot];
+          if (now.odd_last >= 0 && !blind)
+            add_not_finite(a, un.r, un.h, max(lo, now.odd_first * C::kN),
+                           min(hi, (now.odd_last + 1) * C::kN), HD, dst);
         }
       }
     }

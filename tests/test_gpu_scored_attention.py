@@ -302,3 +302,37 @@ def test_bad_pages_and_metadata_are_flagged(rb):
         bt[row, 0] = 0                                        # the null page
         assert call(bt, sl) == rb.EBIT_BLOCK_ID
     assert call(spec.block_table, sl) == 0
+
+
+@pytest.mark.parametrize("nh,nkv,hd", [(8, 2, 128), (4, 4, 64), (12, 2, 64), (16, 1, 128)])
+@pytest.mark.parametrize("kind", ["documents", "window", "prefix", "causal"])
+def test_infinities_and_nan_stay_with_the_rows_that_see_them(rb, nh, nkv, hd, kind):
+    """K and V of some keys are infinite or NaN: rows that do not see those keys are as without
+    them, rows that do get infinities and NaN (the oracle leaves unseen keys out of its sums)."""
+    spec = wl.batch_from_lists([300, 0, 40, 17, 500], [200, 390, 2, 1, 3], num_q_heads=nh,
+                               num_kv_heads=nkv, head_dim=hd, seed=nh + hd)
+    tens = wl.make_tensors(spec, device="cuda")
+    rng = np.random.default_rng(3)
+    pos = _positions(spec)
+    qsl = np.concatenate([[0], np.cumsum(spec.num_scheduled)])
+    rules = {"documents": lambda: dict(key_start=_documents(spec, rng, 60)),
+             "window": lambda: dict(key_start=pos - 20, softcap=30.0),
+             "prefix": lambda: dict(prefix_lens=[350, 33, 41, 5, 499], slopes=_alibi(nh)),
+             "causal": lambda: dict()}[kind]()
+    bad = [float("inf"), float("-inf"), float("nan")]
+    for i in range(spec.num_reqs):
+        c, q = int(spec.num_computed[i]), int(spec.num_scheduled[i])
+        for n, p in enumerate(rng.choice(c + q, size=5, replace=False).tolist() + [c + q - 1]):
+            hist = p < c
+            kv = (tens.hist_v[i] if hist else tens.v)
+            row = p if hist else int(qsl[i]) + p - c
+            kv[row, int(rng.integers(nkv)), int(rng.integers(hd))] = bad[n % 3]
+            if n == 2:   # a key that is NaN makes its readers' rows NaN, and only theirs
+                (tens.hist_k[i] if hist else tens.k)[row, :, 5] = float("nan")
+    wl.place_history(spec, tens.hist_k, tens.k_cache)
+    wl.place_history(spec, tens.hist_v, tens.v_cache)
+    got, _, _, _ = _check(rb, spec, tens=tens, **rules)
+    finite = torch.isfinite(got.float()).flatten(1).all(1)
+    assert not bool(finite.all())
+    if kind != "prefix":      # (there every row may see a NaN key)
+        assert bool(finite.any())
