@@ -1179,7 +1179,7 @@ rb_status launch_hd(const AttnArgs& a, const CUtensorMap& qmap, const CUtensorMa
   }
   const int grid = max(1, device_sm_count());
   if constexpr (is_scored(kRules))
-    return launch_after_plan(attn_prefill_tc_kernel<HD, kRules>, grid, C::kThreads, C::kSmemBytes,
+    return launch_overlapped(attn_prefill_tc_kernel<HD, kRules>, grid, C::kThreads, C::kSmemBytes,
                              s, qmap, kmap, vmap, a);
   attn_prefill_tc_kernel<HD, kRules><<<grid, C::kThreads, C::kSmemBytes, s>>>(qmap, kmap, vmap, a);
   if (last_launch_status() != RB_OK) return RB_ERR_CUDA;

@@ -143,6 +143,7 @@ constexpr int kSource = 1 << 30;  // bit of a page's mark: it is a source
 // it finds one the error bit is set and the pages' contents are unspecified.
 __global__ void __launch_bounds__(kCopyThreads)
     pages_copy_kernel(PageArgs a, int n, const int32_t* src, const int32_t* dst, int32_t* mark) {
+  grid_wait();
   const int tid = threadIdx.x;
   if (blockIdx.x == 0) {
     // eight pairs per thread and round, so that the three passes stay shorter than the copies
@@ -239,6 +240,7 @@ __global__ void __launch_bounds__(kCheckThreads)
                      int32_t* header) {
   __shared__ int tmp[32];
   __shared__ int s_bits;
+  grid_wait();
   const int tid = threadIdx.x;
   grid_release();
   if (tid == 0) s_bits = 0;
@@ -335,6 +337,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 __global__ void __launch_bounds__(kCheckThreads) __cluster_dims__(kClusterCtas, 1, 1)
     pages_free_kernel(PageArgs a, int n, const int32_t* list, int32_t* num_freed) {
   __shared__ int s_freed;
+  grid_wait();
   cg::cluster_group cluster = cg::this_cluster();
   const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) s_freed = 0;
@@ -408,6 +411,7 @@ __global__ void __launch_bounds__(kCheckThreads) __cluster_dims__(kClusterCtas, 
     compact_plan_kernel(PageArgs a, PagesWs w, int32_t* num_live) {
   __shared__ int tmp[32];
   __shared__ int s_count, s_low;
+  grid_wait();
   cg::cluster_group cluster = cg::this_cluster();
   grid_release();
   const int tid = threadIdx.x, lane = tid & 31, cta = blockIdx.x;
@@ -620,11 +624,9 @@ extern "C" rb_status rb_pages_copy(const rb_dims* dims, int32_t num_pairs, const
   if (num_pairs == 0) return RB_OK;
   if (d_src == nullptr || d_dst == nullptr) return RB_ERR_INVALID_ARG;
   const int grid = 1 + copy_grid(a, num_pairs);
-  pages_copy_kernel<<<grid, kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-      a, num_pairs, d_src, d_dst, ws_of(d_workspace, a.entries, dims->max_num_reqs).code);
-  if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
-  note_launches(1);
-  return RB_OK;
+  return launch_overlapped(pages_copy_kernel, grid, kCopyThreads, 0,
+                           static_cast<cudaStream_t>(stream), a, num_pairs, d_src, d_dst,
+                           ws_of(d_workspace, a.entries, dims->max_num_reqs).code);
 }
 
 extern "C" rb_status rb_pages_fork(const rb_dims* dims, const rb_page_tables* tables,
@@ -645,12 +647,10 @@ extern "C" rb_status rb_pages_fork(const rb_dims* dims, const rb_page_tables* ta
     return RB_ERR_INVALID_ARG;
   const PagesWs w = ws_of(d_workspace, a.entries, dims->max_num_reqs);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  fork_plan_kernel<<<1, kCheckThreads, 0, s>>>(a, num_forks, d_src_rows, d_dst_rows,
-                                               d_num_cached, w.code, w.movers, w.holes,
-                                               w.header);
-  if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
-  note_launches(1);
-  return launch_after_plan(fork_apply_kernel, num_forks, kCopyThreads, 0, s, a, num_forks,
+  st = launch_overlapped(fork_plan_kernel, 1, kCheckThreads, 0, s, a, num_forks, d_src_rows,
+                         d_dst_rows, d_num_cached, w.code, w.movers, w.holes, w.header);
+  if (st != RB_OK) return st;
+  return launch_overlapped(fork_apply_kernel, num_forks, kCopyThreads, 0, s, a, num_forks,
                            d_src_rows, d_dst_rows, d_num_cached, w.movers, w.header);
 }
 
@@ -665,11 +665,8 @@ extern "C" rb_status rb_pages_free(const rb_dims* dims, const rb_page_tables* ta
   if (st != RB_OK) return st;
   if (num_free < 0 || (num_free > 0 && d_rows == nullptr)) return RB_ERR_INVALID_ARG;
   if (num_free == 0 && d_num_freed == nullptr) return RB_OK;
-  pages_free_kernel<<<kClusterCtas, kCheckThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-      a, num_free, d_rows, d_num_freed);
-  if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
-  note_launches(1);
-  return RB_OK;
+  return launch_overlapped(pages_free_kernel, kClusterCtas, kCheckThreads, 0,
+                           static_cast<cudaStream_t>(stream), a, num_free, d_rows, d_num_freed);
 }
 
 extern "C" rb_status rb_pages_compact(const rb_dims* dims, const rb_page_tables* tables,
@@ -684,13 +681,13 @@ extern "C" rb_status rb_pages_compact(const rb_dims* dims, const rb_page_tables*
   if (st != RB_OK) return st;
   const PagesWs w = ws_of(d_workspace, a.entries, dims->max_num_reqs);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  compact_plan_kernel<<<kClusterCtas, kCheckThreads, 0, s>>>(a, w, d_num_live);
-  if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
-  note_launches(1);
+  st = launch_overlapped(compact_plan_kernel, kClusterCtas, kCheckThreads, 0, s, a, w,
+                         d_num_live);
+  if (st != RB_OK) return st;
   const int table_ctas = 
       min(max(a.rows, (a.entries + 4095) / 4096), max(1, device_sm_count()));
   // at most half of the pages move
   const int grid = table_ctas + copy_grid(a, a.entries / 2);
-  return launch_after_plan(compact_move_kernel, grid, kCopyThreads, 0, s, a, w, d_page_map,
+  return launch_overlapped(compact_move_kernel, grid, kCopyThreads, 0, s, a, w, d_page_map,
                            table_ctas);
 }

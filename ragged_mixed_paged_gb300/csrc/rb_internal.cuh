@@ -60,11 +60,11 @@ bool encode_kv_tensor_map(CUtensorMap* map, const void* base, int head_dim, int 
 bool encode_q_tensor_map(CUtensorMap* map, const void* base, int head_dim, int num_q_heads,
                          long long num_tokens, int group);
 
-// Launches `kernel` so that it may start while the kernel before it on the stream still runs
-// (programmatic dependent launch): the kernel calls grid_wait() before it touches anything the
-// one before it writes or reads.  Saves the launch latency between a plan and its grid.
+// Launches `kernel` so that it may be set up while the kernel before it on the stream still runs,
+// and start once that one calls grid_release (programmatic dependent launch): the kernel calls
+// grid_wait() before it touches anything the one before it writes or reads.
 template <class... Params, class... Args>
-rb_status launch_after_plan(void (*kernel)(Params...), int grid, int threads, size_t smem,
+rb_status launch_overlapped(void (*kernel)(Params...), int grid, int threads, size_t smem,
                             cudaStream_t s, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -89,7 +89,7 @@ rb_status launch_after_plan(void (*kernel)(Params...), int grid, int threads, si
 __device__ __forceinline__ void grid_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
-// Lets the next kernel of the stream start (one launched with launch_after_plan: it still waits
+// Lets the next kernel of the stream start (one launched with launch_overlapped: it still waits
 // for this one's end where it calls grid_wait).
 __device__ __forceinline__ void grid_release() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

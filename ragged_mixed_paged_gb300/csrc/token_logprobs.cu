@@ -13,9 +13,9 @@
 // terms that matter (x_i near r) keep their bits however large the logits are.
 //
 // The top k takes no part in that loop but maxima: each thread keeps the largest logit of each of
-// up to four segments of its share.  The k-th largest of 128 lane groups' maxima bounds the k-th
+// up to eight segments of its share.  The k-th largest of 64 lane groups' maxima bounds the k-th
 // largest logit from below; only segments whose maximum reaches it hold candidates, about k of
-// the 1024 of a CTA, and those are read again (mostly from L2).
+// the 2048 of a CTA, and those are read again (mostly from L2).
 //
 // Bound by HBM for many rows, by the chain of dependent steps (about 8 us) for few.  The next
 // batch of 16-byte loads is issued before the current one is worked on, and four CTAs per SM of
@@ -32,8 +32,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kGroups = 128;      // lane groups (of 2 threads) whose maxima bound the k-th logit
-constexpr int kSegments = 4;      // of a thread's share of the row, each with its own maximum
+constexpr int kGroups = 64;       // lane groups (of 4 threads) whose maxima bound the k-th logit
+constexpr int kSegments = 8;      // of a thread's share of the row, each with its own maximum
 constexpr int kMaxTop = 32;
 constexpr int kMaxSplits = 8;     // CTAs of a cluster that share one row
 constexpr int kCandidates = 1024;
@@ -123,13 +123,6 @@ struct Sums {
     }
     ref = to;
   }
-  __device__ __forceinline__ void merge(Sums o) {
-    const float to = fmaxf(ref, o.ref);
-    move_to(to);
-    o.move_to(to);
-    s += o.s;
-    w += o.w;
-  }
 };
 
 struct Entry {
@@ -144,22 +137,29 @@ struct Part {  // what one thread, warp, CTA or cluster found
   Sums sums;
   float max;
   int above;
-  __device__ __forceinline__ void merge(const Part& o) {
-    sums.merge(o.sums);
-    max = fmaxf(max, o.max);
-    above += o.above;
-  }
-  __device__ __forceinline__ Part from_lane(int mask) const {
-    Part q;
-    q.sums.ref = __shfl_xor_sync(0xffffffffu, sums.ref, mask);
-    q.sums.s = __shfl_xor_sync(0xffffffffu, sums.s, mask);
-    q.sums.w = __shfl_xor_sync(0xffffffffu, sums.w, mask);
-    q.max = __shfl_xor_sync(0xffffffffu, max, mask);
-    q.above = __shfl_xor_sync(0xffffffffu, above, mask);
-    return q;
-  }
 };
 __device__ __forceinline__ Part no_part() { return Part{Sums{kLowest, 0.f, 0.f}, -INFINITY, 0}; }
+
+// Largest value of a warp's lanes (no NaN among them), by the integer order of the bits.
+__device__ __forceinline__ float warp_max(float x) {
+  const int b = __float_as_int(x);
+  const int m = __reduce_max_sync(0xffffffffu, b >= 0 ? b : b ^ 0x7fffffff);
+  return __int_as_float(m >= 0 ? m : m ^ 0x7fffffff);
+}
+// The parts of a warp's lanes as one, in every lane; kLanes: how many lanes in a row hold parts
+// of their own (the others repeat them).  Each sum moves once, to the largest reference.
+template <int kLanes>
+__device__ __forceinline__ Part warp_merge(Part p) {
+  p.sums.move_to(warp_max(p.sums.ref));
+  p.max = warp_max(p.max);
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) {
+    p.sums.s += __shfl_xor_sync(0xffffffffu, p.sums.s, o);
+    p.sums.w += __shfl_xor_sync(0xffffffffu, p.sums.w, o);
+    p.above += __shfl_xor_sync(0xffffffffu, p.above, o);
+  }
+  return p;
+}
 
 struct Shared {
   alignas(16) float group_max[kGroups];  // read four at a time
@@ -216,18 +216,20 @@ __device__ __forceinline__ int slice_top(const Slice<T>& sl, int k, const float 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int want = min(k, max(0, sl.hi() - sl.lo()));
   if (want == 0) return 0;
-  {  // rank of each group's maximum, half of the others per thread
-    const int g = tid >> 1, half = tid & 1;
+  {  // rank of each group's maximum, a quarter of the others per thread
+    const int g = tid >> 2, quarter = tid & 3;
     const float x = sh.group_max[g];
     int rank = 0;
-#pragma unroll 4
-    for (int j = half * (kGroups / 2); j < (half + 1) * (kGroups / 2); j += 4) {
+#pragma unroll
+    for (int i = 0; i < kGroups / 4; i += 4) {
+      const int j = quarter * (kGroups / 4) + i;
       const float4 o = *reinterpret_cast<const float4*>(sh.group_max + j);
       rank += (o.x > x || (o.x == x && j < g)) + (o.y > x || (o.y == x && j + 1 < g)) +
               (o.z > x || (o.z == x && j + 2 < g)) + (o.w > x || (o.w == x && j + 3 < g));
     }
     rank += __shfl_xor_sync(0xffffffffu, rank, 1);
-    if (half == 0 && rank == want - 1) sh.tau = x;
+    rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+    if (quarter == 0 && rank == want - 1) sh.tau = x;
   }
   __syncthreads();
   const float tau = sh.tau;  // at least `want` elements are >= tau (-inf: fewer groups had any)
@@ -247,16 +249,30 @@ __device__ __forceinline__ int slice_top(const Slice<T>& sl, int k, const float 
         if (c < kCandidates) sh.cand[c] = Entry{x, i};
       }
     };
-    for (int w = tid; w < work; w += kThreads) {
-      const int q = sh.shares[w / per];
-      const int v = sl.w0 + q % kThreads + (q / kThreads * per + w % per) * kThreads;
-      if (v >= sl.w1) continue;
-      float2 x[E::kPer / 2];
-      E::unpack(sl.load(v), x);
+    constexpr int kAhead = 4;
+    for (int w0 = tid; w0 < work; w0 += kAhead * kThreads) {
+      int v[kAhead];
+      uint4 u[kAhead];
 #pragma unroll
-      for (int j = 0; j < E::kPer / 2; ++j) {
-        check(x[j].x, sl.first(v) + 2 * j);
-        check(x[j].y, sl.first(v) + 2 * j + 1);
+      for (int k = 0; k < kAhead; ++k) {
+        const int w = w0 + k * kThreads;
+        v[k] = sl.w1;
+        if (w < work) {
+          const int q = sh.shares[w / per];
+          v[k] = sl.w0 + q % kThreads + (q / kThreads * per + w % per) * kThreads;
+        }
+        if (v[k] < sl.w1) u[k] = sl.load(v[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (v[k] >= sl.w1) continue;
+        float2 x[E::kPer / 2];
+        E::unpack(u[k], x);
+#pragma unroll
+        for (int j = 0; j < E::kPer / 2; ++j) {
+          check(x[j].x, sl.first(v[k]) + 2 * j);
+          check(x[j].y, sl.first(v[k]) + 2 * j + 1);
+        }
       }
     }
     if (edge_i >= 0) check(edge_x, edge_i);
@@ -433,16 +449,13 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
     seg[g] = top;
     mine.max = fmaxf(mine.max, top);
   }
-  const float pair_max = fmaxf(mine.max, __shfl_xor_sync(0xffffffffu, mine.max, 1));
-  if ((lane & 1) == 0) sh.group_max[tid >> 1] = pair_max;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine.merge(mine.from_lane(o));
+  float group = fmaxf(mine.max, __shfl_xor_sync(0xffffffffu, mine.max, 1));
+  group = fmaxf(group, __shfl_xor_sync(0xffffffffu, group, 2));
+  if ((lane & 3) == 0) sh.group_max[tid >> 2] = group;
+  mine = warp_merge<32>(mine);
   if (lane == 0) sh.warp[warp] = mine;
   __syncthreads();
-  // the CTA's sums, in every lane
-  Part p = sh.warp[lane % kWarps];
-#pragma unroll
-  for (int o = 1; o < kWarps; o <<= 1) p.merge(p.from_lane(o));
+  Part p = warp_merge<kWarps>(sh.warp[lane % kWarps]);  // the CTA's sums, in every lane
 
   const long long top_row = static_cast<long long>(r) * a.top;
   int n_top = min(a.top, a.vocab);
@@ -468,9 +481,8 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
     }
     cluster.sync();
     if (split != 0) return;
-    p = lane % kMaxSplits < splits ? sh.parts[lane % kMaxSplits] : no_part();
-#pragma unroll
-    for (int o = 1; o < kMaxSplits; o <<= 1) p.merge(p.from_lane(o));
+    p = warp_merge<kMaxSplits>(lane % kMaxSplits < splits ? sh.parts[lane % kMaxSplits]
+                                                          : no_part());
     const RowResult row(p);
     if (a.top > 0 && !row.bad) {
       for (int c = tid; c < splits * kMaxTop; c += kThreads) {
