@@ -23,6 +23,8 @@
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "rb_internal.cuh"
 
 namespace rb {
@@ -65,49 +67,111 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
   return y;
 }
 
+// Elements of a 16-byte vector: their number, one of them, all as floats, all less a reference,
+// the largest of several vectors' (NaN left out), and the vector of -inf.
 template <class T>
 struct Elem;
 template <>
 struct Elem<float> {
   static constexpr int kPer = 4;
+  static constexpr uint32_t kNegInf = 0xff800000u;
   static __device__ __forceinline__ float one(const float* p) { return __ldg(p); }
   static __device__ __forceinline__ void unpack(const uint4& u, float2 (&x)[2]) {
     x[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
     x[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
   }
-};
-template <>
-struct Elem<__nv_bfloat16> {
-  static constexpr int kPer = 8;
-  static __device__ __forceinline__ float one(const __nv_bfloat16* p) {
-    return __uint_as_float(
-        static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(p))) << 16);
+  static __device__ __forceinline__ void less(const uint4& u, float ref, float2 (&d)[2]) {
+    unpack(u, d);
+    const float2 nr = make_float2(-ref, -ref);
+    d[0] = __fadd2_rn(d[0], nr);
+    d[1] = __fadd2_rn(d[1], nr);
   }
+  template <int N>
+  static __device__ __forceinline__ float largest(const uint4 (&u)[N]) {
+    float m[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      m[0] = fmax3(m[0], __uint_as_float(u[k].x), __uint_as_float(u[k].y));
+      m[1] = fmax3(m[1], __uint_as_float(u[k].z), __uint_as_float(u[k].w));
+    }
+    return fmaxf(m[0], m[1]);
+  }
+};
+// 16-bit types, two per word; less() is the mixed-precision subtraction, which converts as it
+// subtracts (an unpacking instruction less per element).
+template <class T, class Ops>
+struct Elem16 {
+  static constexpr int kPer = 8;
+  static __device__ __forceinline__ float one(const T* p) {
+    return Ops::two(__ldg(reinterpret_cast<const unsigned short*>(p))).x;
+  }
+  static __device__ __forceinline__ void unpack(const uint4& u, float2 (&x)[4]) {
+    x[0] = Ops::two(u.x);
+    x[1] = Ops::two(u.y);
+    x[2] = Ops::two(u.z);
+    x[3] = Ops::two(u.w);
+  }
+  static __device__ __forceinline__ void less(const uint4& u, float ref, float2 (&d)[4]) {
+    d[0] = Ops::less(u.x, ref);
+    d[1] = Ops::less(u.y, ref);
+    d[2] = Ops::less(u.z, ref);
+    d[3] = Ops::less(u.w, ref);
+  }
+  template <int N>
+  static __device__ __forceinline__ float largest(const uint4 (&u)[N]) {
+    uint32_t m[2] = {Ops::max2(u[0].x, u[0].y), Ops::max2(u[0].z, u[0].w)};
+#pragma unroll
+    for (int k = 1; k < N; ++k) {
+      m[0] = Ops::max2(m[0], Ops::max2(u[k].x, u[k].y));
+      m[1] = Ops::max2(m[1], Ops::max2(u[k].z, u[k].w));
+    }
+    const float2 x = Ops::two(Ops::max2(m[0], m[1]));
+    return fmax3(x.x, x.y, -INFINITY);  // (both halves NaN: none)
+  }
+};
+struct Bf16Ops {
   static __device__ __forceinline__ float2 two(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
-  static __device__ __forceinline__ void unpack(const uint4& u, float2 (&x)[4]) {
-    x[0] = two(u.x);
-    x[1] = two(u.y);
-    x[2] = two(u.z);
-    x[3] = two(u.w);
+  static __device__ __forceinline__ float2 less(uint32_t w, float ref) {
+    float2 d;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tsub.rn.f32.bf16 %0, l, %3;\n\t"
+        "sub.rn.f32.bf16 %1, h, %3;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "r"(w), "f"(ref));
+    return d;
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t y;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
   }
 };
-template <>
-struct Elem<__half> {
-  static constexpr int kPer = 8;
-  static __device__ __forceinline__ float one(const __half* p) {
-    return __half2float(__ushort_as_half(__ldg(reinterpret_cast<const unsigned short*>(p))));
-  }
+struct Fp16Ops {
   static __device__ __forceinline__ float2 two(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
   }
-  static __device__ __forceinline__ void unpack(const uint4& u, float2 (&x)[4]) {
-    x[0] = two(u.x);
-    x[1] = two(u.y);
-    x[2] = two(u.z);
-    x[3] = two(u.w);
+  static __device__ __forceinline__ float2 less(uint32_t w, float ref) {
+    float2 d;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tsub.rn.f32.f16 %0, l, %3;\n\t"
+        "sub.rn.f32.f16 %1, h, %3;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "r"(w), "f"(ref));
+    return d;
   }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t y;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+  }
+};
+template <>
+struct Elem<__nv_bfloat16> : Elem16<__nv_bfloat16, Bf16Ops> {
+  static constexpr uint32_t kNegInf = 0xff80ff80u;
+};
+template <>
+struct Elem<__half> : Elem16<__half, Fp16Ops> {
+  static constexpr uint32_t kNegInf = 0xfc00fc00u;
 };
 
 // s = sum 2^t, w = sum 2^t t with t = (x - ref) log2(e).
@@ -395,16 +459,47 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
   const float edge_x = edge_i >= 0 ? E::one(sl.row + edge_i) : -INFINITY;
   if (tid == 0) sh.n_shares = sh.n_cand = 0;
 
-  Part mine = no_part();
-  Sums& sums = mine.sums;
+  // the thread's sums, even and odd elements apart, and largest element
+  float ref = kLowest;
+  float2 s2 = make_float2(0.f, 0.f), w2 = make_float2(0.f, 0.f);
+  int above = 0;
+  auto move_to = [&](float to) {
+    Sums x{ref, s2.x, w2.x}, y{ref, s2.y, w2.y};
+    x.move_to(to);
+    y.move_to(to);
+    s2 = make_float2(x.s, y.s);
+    w2 = make_float2(x.w, y.w);
+    ref = to;
+  };
+  float most = -INFINITY;
   if (edge_i >= 0) {
-    mine.max = edge_x;
-    mine.above = edge_x > xt;
-    if (edge_x > sums.ref + kGrowth) sums.move_to(edge_x);
-    const float t = max_nan(edge_x - sums.ref, kFar) * kLog2e;
-    sums.s = fast_exp2(t);
-    sums.w = sums.s * t;
+    most = edge_x;
+    above = edge_x > xt;
+    if (edge_x > ref + kGrowth) ref = edge_x;
+    const float t = max_nan(edge_x - ref, kFar) * kLog2e;
+    s2.x = fast_exp2(t);
+    w2.x = s2.x * t;
   }
+  // sums of one batch; kClamp: with -inf among the elements (2^t t would be 0 * inf)
+  auto batch_sums = [&](const uint4 (&u)[kBatch], auto clamp, float2& bs, float2& bw) {
+    constexpr bool kClamp = decltype(clamp)::value;
+    const float2 l2 = make_float2(kLog2e, kLog2e);
+    bs = bw = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      float2 d[E::kPer / 2];
+      E::less(u[k], ref, d);
+#pragma unroll
+      for (int j = 0; j < E::kPer / 2; ++j) {
+        if constexpr (kClamp) d[j] = make_float2(max_nan(d[j].x, kFar), max_nan(d[j].y, kFar));
+        const float2 t = __fmul2_rn(d[j], l2);
+        const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+        bs = __fadd2_rn(bs, e);
+        bw = __ffma2_rn(e, t, bw);
+      }
+    }
+  };
+  bool clamp = false;  // this thread's part of the row has -inf (or NaN) logits
   // a thread's share: `batches` rounds of kBatch vectors, cut into segments of `seg_batches`
   const int batches = (stop - sl.w0 + kBatch * kThreads - 1) / (kBatch * kThreads);
   const int seg_batches = max(1, (batches + kSegments - 1) / kSegments);
@@ -412,43 +507,44 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
 #pragma unroll
   for (int g = 0; g < kSegments; ++g) {
     float top = -INFINITY;  // largest element of this segment
+#pragma unroll 1
     for (int b = g * seg_batches; b < min(batches, (g + 1) * seg_batches); ++b) {
       const int v = sl.w0 + tid + b * (kBatch * kThreads);
       uint4 u[kBatch];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) u[k] = next[k];
-      fetch(v + kBatch * kThreads);
-#pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        if (v + k * kThreads >= stop) break;
-        float2 x[E::kPer / 2];
-        E::unpack(u[k], x);
-        float mx = fmaxf(x[0].x, x[0].y);
-#pragma unroll
-        for (int j = 1; j < E::kPer / 2; ++j) mx = fmax3(mx, x[j].x, x[j].y);
-        top = fmaxf(top, mx);
-        if (mx > xt) {
-#pragma unroll
-          for (int j = 0; j < E::kPer / 2; ++j) mine.above += (x[j].x > xt) + (x[j].y > xt);
+        u[k] = next[k];
+        if (v + k * kThreads >= stop) {  // past the end: -inf counts for nothing
+          u[k] = make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
+          clamp = true;
         }
-        if (mx > sums.ref + kGrowth) sums.move_to(mx);
-        const float2 l2 = make_float2(kLog2e, kLog2e), nr = make_float2(-sums.ref, -sums.ref);
-        float2 s2 = make_float2(0.f, 0.f), w2 = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < E::kPer / 2; ++j) {
-          const float2 d = __fadd2_rn(x[j], nr);
-          const float2 t = __fmul2_rn(make_float2(max_nan(d.x, kFar), max_nan(d.y, kFar)), l2);
-          const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
-          s2 = __fadd2_rn(s2, e);
-          w2 = __ffma2_rn(e, t, w2);
-        }
-        sums.s += s2.x + s2.y;
-        sums.w += w2.x + w2.y;
       }
+      fetch(v + kBatch * kThreads);
+      const float mx = E::largest(u);
+      top = fmaxf(top, mx);
+      if (mx > xt) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          float2 x[E::kPer / 2];
+          E::unpack(u[k], x);
+#pragma unroll
+          for (int j = 0; j < E::kPer / 2; ++j) above += (x[j].x > xt) + (x[j].y > xt);
+        }
+      }
+      if (mx > ref + kGrowth) move_to(mx);
+      float2 bs, bw;
+      if (!clamp) {
+        batch_sums(u, std::false_type{}, bs, bw);
+        clamp = isnan(bw.x + bw.y);
+      }
+      if (clamp) batch_sums(u, std::true_type{}, bs, bw);
+      s2 = __fadd2_rn(s2, bs);
+      w2 = __fadd2_rn(w2, bw);
     }
     seg[g] = top;
-    mine.max = fmaxf(mine.max, top);
+    most = fmaxf(most, top);
   }
+  Part mine{Sums{ref, s2.x + s2.y, w2.x + w2.y}, most, above};
   float group = fmaxf(mine.max, __shfl_xor_sync(0xffffffffu, mine.max, 1));
   group = fmaxf(group, __shfl_xor_sync(0xffffffffu, group, 2));
   if ((lane & 3) == 0) sh.group_max[tid >> 2] = group;
