@@ -1,4 +1,4 @@
-"""Host checks of the page and log-probability entry points: bad arguments are refused before
+"""Host checks of the scored-attention, page and log-probability entry points: bad arguments are refused before
 anything is enqueued (no GPU is touched)."""
 import ctypes
 
@@ -88,6 +88,31 @@ def test_token_logprobs_host_checks(lib):  # noqa: F811
     assert call(rows=0, logits=None) == 0
 
 
+def test_scored_attention_host_checks(lib):  # noqa: F811
+    def call(d=None, rules="none", R=2, N=4, Np=4, ws=FAKE, ws_bytes=1 << 30, scale=0.1, **kw):
+        d = _dims(lib) if d is None else d
+        c = lib.rb_score_rules(0.0, 0, None, None, None)
+        for k, v in kw.items():
+            setattr(c, k, v)
+        return lib.lib.rb_paged_attention_scored(
+            ctypes.byref(d), R, N, Np, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, ctypes.c_float(scale),
+            ctypes.byref(c) if rules == "none" else None, FAKE, ws, ws_bytes, None, None)
+
+    d = _dims(lib)
+    need = lib.lib.rb_paged_attention_workspace_size(ctypes.byref(d), 2, 4)
+    assert call(rules=None) == 1
+    assert call(reserved=1) == 1
+    for cap in (-1.0, float("nan"), float("inf"), 1e-40):
+        assert call(softcap=cap) == 1, cap
+    assert call(softcap=30.0, scale=float("inf")) == 1
+    assert call(d=_dims(lib, head_dim=96)) == 5
+    assert call(d=_dims(lib, num_q_heads=64, num_kv_heads=2)) == 5
+    assert call(R=9) == 2
+    assert call(N=5, Np=4) == 1
+    assert call(ws_bytes=need - 1) == 2
+    assert call(ws=ctypes.c_void_p(0x100010)) == 1
+
+
 def test_python_checks_come_first(lib):  # noqa: F811
     """The Python face names the tensor that does not fit before the library is called."""
     import torch
@@ -105,3 +130,10 @@ def test_python_checks_come_first(lib):  # noqa: F811
         rb.PagePool(dims, kv, kv, block_table=torch.zeros(4, 4, dtype=torch.int32))
     with pytest.raises(ValueError, match="CUDA"):
         rb.PagePool(dims, kv, kv)
+    q = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="key_start must have 4 entries"):
+        rb.paged_attention_scored(dims, 1, 4, q, kv, kv, kv, kv, kv,
+                                  rb.ScoreRules(key_start=torch.zeros(3, dtype=torch.int32)))
+    with pytest.raises(ValueError, match="prefix_lens must have 2 entries"):
+        rb.paged_attention_scored(dims, 2, 4, q, kv, kv, kv, kv, kv,
+                                  rb.ScoreRules(prefix_lens=torch.zeros(1, dtype=torch.int32)))
