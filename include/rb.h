@@ -274,10 +274,11 @@ typedef struct rb_score_rules {
  * visible keys of the ruled scores.  A query that sees no key gets a row of zeros.
  * Arguments, layouts, workspace (rb_paged_attention_workspace_size), supported shapes and
  * errors are those of rb_paged_attention; RB_ERR_INVALID_ARG also for NULL rules, a nonzero
- * `reserved`, and a softcap that is negative, not finite, or so small that softmax_scale /
- * softcap overflows.
- * Pages that no query of the request sees are not read and their page-table entries are not
- * checked (a window's old pages may be gone), and the rows of such keys may hold anything.
+ * `reserved`, a softmax_scale that is not positive, and a softcap that is negative, not finite,
+ * or so small that softmax_scale / softcap overflows.
+ * Pages before the first key that any query of the request sees are not read and their
+ * page-table entries are not checked (a window's old pages may be gone), and what K and V hold
+ * for keys that a query does not see, infinities and NaN too, does not reach its row.
  */
 rb_status rb_paged_attention_scored(const rb_dims* dims, int32_t num_reqs, int32_t num_tokens,
                                     int32_t num_tokens_padded, const void* d_q,

@@ -153,7 +153,11 @@ rb_status attn_setup(const rb_dims* dims, int32_t num_reqs, int32_t num_tokens,
 
 rb_status attn_set_rules(AttnSetup* su, const rb_score_rules* rules, float softmax_scale) {
   if (rules == nullptr || rules->reserved != 0 || !std::isfinite(rules->softcap) ||
-      rules->softcap < 0.f)
+      rules->softcap < 0.f || !(softmax_scale > 0.f))
+    return RB_ERR_INVALID_ARG;
+  auto aligned4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
+  if (!aligned4(rules->d_head_slopes) || !aligned4(rules->d_key_start) ||
+      !aligned4(rules->d_prefix_lens))
     return RB_ERR_INVALID_ARG;
   AttnArgs& a = su->a;
   a.rules = kMasked;

@@ -164,7 +164,7 @@ constexpr float kSumLimit = 1048576.f;
 
 // Soft caps (log2 units) up to which a capped row's reference bounds its exponents from above and
 // below, and how far below the cap that reference may lie.
-constexpr float kMaxBoundedCap = 90.f, kCapHeadroom = 80.f;
+constexpr float kMaxBoundedCap = 74.f, kCapHeadroom = 48.f;
 
 __device__ __forceinline__ int tiles_for(int c, int jmax) { return (c + jmax + 1 + 127) / 128; }
 constexpr int kKeysPerTile = 128;  // keys per K/V tile
@@ -692,12 +692,16 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<is_scored(kRules)>& sh, u
     float m_ref = valid ? -INFINITY : 0.f, l = 0.f;
     bool ok = true;
     // Capped scores are at most cap_log2 (a bias that falls with distance only lowers them), so a
-    // reference of at least cap_log2 - kCapHeadroom keeps every exponent below 2^kCapHeadroom, and a
-    // row's largest score, its own key's at least -cap_log2, keeps its terms above 2^-100 up to
-    // kMaxBoundedCap.  Then no tile is ever taken again, and its scores need not be kept.
+    // reference of at least cap_log2 - kCapHeadroom keeps every exponent below 2^kCapHeadroom.  A
+    // row's largest score is at least -cap_log2 (biased: its own key's, if it sees that one), so
+    // up to kMaxBoundedCap its terms stay above 2^-100.  Then no tile is ever taken again, and
+    // its scores need not be kept.
     bool bounded = false;
-    if constexpr ((kRules & kCapped) != 0)
-      bounded = a.cap_log2 <= kMaxBoundedCap && __all_sync(0xffffffffu, slope >= 0.f);
+    if constexpr ((kRules & kCapped) != 0) {
+      bounded = a.cap_log2 <= kMaxBoundedCap;
+      if constexpr ((kRules & kBiased) != 0)
+        bounded = bounded && __all_sync(0xffffffffu, slope >= 0.f && lo <= un.c + jt);
+    }
     for (int j = 0; j < n; ++j) {
       const uint32_t tj = tc_x + j;
       if (!wait_all(&sh.s_full[x], tj & 1)) { ok = false; break; }

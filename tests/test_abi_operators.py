@@ -105,6 +105,8 @@ def test_scored_attention_host_checks(lib):  # noqa: F811
     for cap in (-1.0, float("nan"), float("inf"), 1e-40):
         assert call(softcap=cap) == 1, cap
     assert call(softcap=30.0, scale=float("inf")) == 1
+    assert call(scale=0.0) == 1 and call(scale=-0.1) == 1
+    assert call(d_key_start=0x100001) == 1
     assert call(d=_dims(lib, head_dim=96)) == 5
     assert call(d=_dims(lib, num_q_heads=64, num_kv_heads=2)) == 5
     assert call(R=9) == 2

@@ -181,6 +181,30 @@ def test_soft_caps_of_any_size(rb, softcap):
     _check(rb, spec, softcap=softcap)
 
 
+def test_prefix_rows_that_do_not_see_their_own_key(rb):
+    """A prefix ahead of the query and a first key past it: with a steep bias every visible score
+    lies far below the soft cap's range (by hundreds of log2 units)."""
+    spec = wl.batch_from_lists([0, 100, 5], [300, 150, 1], num_q_heads=8, num_kv_heads=2,
+                               head_dim=128, seed=12)
+    start = np.concatenate([np.full(300, 280), np.full(150, 240), [0]])
+    for softcap in (30.0, 60.0, 0.0):
+        _check(rb, spec, softcap=softcap, slopes=[1.0 + h for h in range(8)], key_start=start,
+               prefix_lens=[300, 250, 6])
+
+
+def test_capped_scores_at_both_ends_and_large_values(rb):
+    """Scores that go from -cap to cap along a row, with V up to 1e12."""
+    spec = wl.batch_from_lists([600, 0, 700], [300, 400, 1], num_q_heads=8, num_kv_heads=2,
+                               head_dim=128, seed=14)
+    tens = jump_tensors(spec, {(0, 256): 3.0, (300, 340): -20.0, (560, 700): 20.0})
+    for v in [tens.v] + tens.hist_v:
+        v.mul_(2.0 ** 40)
+    wl.place_history(spec, tens.hist_v, tens.v_cache)
+    for softcap in (20.0, 50.0, 70.0):
+        _check(rb, spec, tens=tens, softcap=softcap)
+        _check(rb, spec, tens=tens, softcap=softcap, slopes=_alibi(8))
+
+
 def test_long_decodes_are_split(rb):
     spec = wl.batch_from_lists([20000, 9000, 100], [1, 1, 2], num_q_heads=8, num_kv_heads=2,
                                head_dim=128, seed=2)
