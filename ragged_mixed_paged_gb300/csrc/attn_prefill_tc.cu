@@ -711,6 +711,41 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<is_scored(kRules)>& sh, u
         if (j > 0) tc::mbar_arrive(&sh.v_empty[(kt - 1) % C::kStagesV]);
         if (j + 1 == n) tc::mbar_arrive(&sh.q_empty);
       }
+      if constexpr (kScored) {
+        // V of the tile, by tile A for both sides and before the scores are in registers: keys at
+        // or past the end of the sequence and before the unit's first visible one may hold
+        // anything (zeroed); of keys that some rows of the unit see and others do not, what is not
+        // finite is taken out and noted.
+        const int first = (un.j0 + n - 1 - j) * C::kN;
+        const bool unknown = first + C::kN > un.L || first < un.lo;
+        const bool mixed = first < max(un.lo_max[0], un.lo_max[1]) ||
+                           first + C::kN > max(un.c + un.tok0 + 1, un.prefix);
+        if (x == 0 && (unknown || mixed)) {
+          const uint32_t kt = itk + j, sv = kt % C::kStagesV;
+          if (!wait_all(&sh.v_full[sv], (kt / C::kStagesV) & 1)) { ok = false; break; }
+          uint8_t* v = smem_ptr + C::kVOffset + sv * C::kTileBytes;
+          if (t >= un.L - first || t < un.lo - first) {
+#pragma unroll 1
+            for (int hf = 0; hf < C::kHalves; ++hf)
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                *reinterpret_cast<uint4*>(v + hf * C::kHalfBytes + t * 128 + c * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+          }
+          if (mixed) {  // this warp's 32 keys, 512 bytes at a time
+            __syncwarp();
+            bool odd = false;
+            for (int hf = 0; hf < C::kHalves; ++hf)
+              odd |= take_out_not_finite(v + hf * C::kHalfBytes + (t >> 5) * 32 * 128, 8, 512);
+            if (odd && lane0) {
+              atomicMin(&sh.units[slot].odd_first, first / C::kN);
+              atomicMax(&sh.units[slot].odd_last, first / C::kN);
+              __threadfence_block();
+            }
+          }
+        }
+      }
       tc::fence_after_sync();
       float s[128];
       {
@@ -828,22 +863,11 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<is_scored(kRules)>& sh, u
       }
       // keys at or past the end of the sequence may hold anything: zero their V rows (only the
       // unit's last K/V tile can reach them; tile A zeroes it when it uses that tile)
-      // (scored: nor are keys before the first visible one known, in the unit's first tile)
-      bool unknown = kv_base + C::kN > un.L;
-      // scored: keys that some rows of the unit see and others do not
-      bool mixed = false;
-      if constexpr (kScored) {
-        unknown = unknown || kv_base < un.lo;
-        mixed = kv_base < max(un.lo_max[0], un.lo_max[1]) ||
-                kv_base + C::kN > max(un.c + un.tok0 + 1, un.prefix);
-      }
-      if ((unknown || mixed) && (x == 0 || j >= un.n[0])) {
+      if (!kScored && kv_base + C::kN > un.L && (x == 0 || j >= un.n[0])) {
         const uint32_t kt = itk + j, sv = kt % C::kStagesV;
         if (!wait_all(&sh.v_full[sv], (kt / C::kStagesV) & 1)) { ok = false; break; }
         const int kmin = max(un.L - kv_base, 0);
-        bool zero = t >= kmin;
-        if constexpr (kScored) zero = zero || t < un.lo - kv_base;
-        if (zero) {
+        if (t >= kmin) {
           uint8_t* vrow = smem_ptr + C::kVOffset + sv * C::kTileBytes + t * 128;
 #pragma unroll
           for (int hf = 0; hf < C::kHalves; ++hf)
@@ -852,20 +876,6 @@ __device__ void softmax_wg(const AttnArgs& a, TcShared<is_scored(kRules)>& sh, u
               *reinterpret_cast<uint4*>(vrow + hf * C::kHalfBytes + c * 16) =
                   make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
-        }
-        if constexpr (kScored) {
-          if (mixed) {  // this warp's 32 keys, 512 bytes at a time
-            __syncwarp();
-            uint8_t* rows = smem_ptr + C::kVOffset + sv * C::kTileBytes + (t >> 5) * 32 * 128;
-            bool odd = false;
-            for (int hf = 0; hf < C::kHalves; ++hf)
-              odd |= take_out_not_finite(rows + hf * C::kHalfBytes, 8, 512);
-            if (odd && lane0) {
-              atomicMin(&sh.units[slot].odd_first, kv_base / C::kN);
-              atomicMax(&sh.units[slot].odd_last, kv_base / C::kN);
-              __threadfence_block();
-            }
-          }
         }
       }
       // exponents and the row sum two columns at a time with the paired fp32 FMA / add
