@@ -312,6 +312,8 @@ rb_status attn_main(const AttnSetup& su, cudaStream_t s);
 // Adds rb_paged_attention_scored's rules to a set-up call.
 rb_status attn_set_rules(AttnSetup* su, const rb_score_rules* rules, float softmax_scale);
 
+rb_status launch_scored_tc(const AttnArgs& a, int head_dim, const CUtensorMap& qmap,
+                           const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s);
 rb_status launch_prefill_tc(const AttnArgs& a, int head_dim, const CUtensorMap& qmap,
                             const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s);
 

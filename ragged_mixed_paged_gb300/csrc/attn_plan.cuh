@@ -101,8 +101,8 @@ constexpr float kDecUnitUs = 6.f, kDecPageUs = 0.6f, kDecBytesPerUsPerCta = 73e3
 constexpr float kHbmBytesPerUs = 6.4e6f;
 constexpr float kPreUnitUs = 8.f, kPreTileUs = 2.3f;
 // What score rules add to a key tile of a prefill unit (chunks alone, 128-key tiles of two 128-row
-// query tiles at head_dim 128: 1.8 us without rules, +0.4 biased, +0.9 capped).
-constexpr float kBiasTileUs = 0.4f, kCapTileUs = 0.9f;
+// query tiles at head_dim 128: 1.9 us without rules, +0.4 biased, +0.6 capped).
+constexpr float kBiasTileUs = 0.4f, kCapTileUs = 0.6f;
 constexpr int kTileBins = 512;  // histogram bins of prefill units by key tiles (longer: last bin)
 
 // The planner, run by one whole CTA of any size: validates the metadata, classifies requests,
