@@ -63,11 +63,11 @@ FLUSH_BYTES = 512 << 20
 # its planner's code, comments left out): a figure is reported only while the code is the code
 # it was measured on.
 KNOWN_TRAFFIC = {
-    (2, "9a8026878da7e19f"): 78976256 + 3943680,
-    (3, "9a8026878da7e19f"): 4545474816 + 26148352,
+    (2, "dc5594e866228332"): 78999808 + 3906048,
+    (3, "dc5594e866228332"): 4545301248 + 26047488,
     # the stream: mean over the launches of stream steps 5..99 (the default timed steps)
-    (4, "9a8026878da7e19f"): 9567950312 + 80911815,
-    (5, "9a8026878da7e19f"): 8588893440 + 115581440,
+    (4, "dc5594e866228332"): 9545384569 + 80824829,
+    (5, "dc5594e866228332"): 7021283840 + 114328832,
 }
 
 WORKLOAD_NAMES = {1: "pages' worked example A/B/C", 2: "pages' padding example",
