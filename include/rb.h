@@ -31,7 +31,7 @@
  *  - Every pointer named d_* is DEVICE memory on the current CUDA device; the caller owns it,
  *    allocates it and keeps it alive until the work queued on `stream` has finished.  The
  *    library allocates no device memory and never synchronises: each call only enqueues
- *    kernels (and, for rb_prepare_inputs, one 4-byte memset) on `stream`, a cudaStream_t passed
+ *    kernels (and, for rb_prepare_inputs and rb_pages_count, one memset) on `stream`, a cudaStream_t passed
  *    as void* (NULL = the legacy default stream); rb_step_host and rb_step_host_async also
  *    enqueue the caller's copies, the latter on the caller's copy streams with event records
  *    and waits between them.  The one exception to "no device memory" is
