@@ -176,7 +176,8 @@ def peaks():
     return FALLBACK_PEAKS, "fallback"
 
 
-FUSED_SOURCES = ("attn_prefill_tc.cu", "attn_prefill_tc.cuh", "attn_decode_warp.cuh", "tc_ptx.cuh", "attn_common.cuh",
+FUSED_SOURCES = ("attn_prefill_tc.cu", "attn_prefill_tc.cuh", "attn_decode_warp.cuh",
+                 "tc_ptx.cuh", "attn_common.cuh",
                  "rb_internal.cuh", "attn_plan.cuh")
 
 

@@ -5,9 +5,9 @@
 // key tiles are taken last to first (ScoredUnit).  The softmax differs.  A ruled score costs up
 // to four more multiply-adds, and straight-line code for a row's 128 scores runs at the rate of
 // instruction fetch: a third of an instruction per cycle and scheduler, with 8 softmax warps and
-// with 16 alike, and the same loop of 16 columns unrolled is a quarter slower than rolled.  So a row's
-// scores are read from tensor memory 64 columns at a time by a loop of two rounds, and P goes
-// over columns already read.  A score above the running reference by more than kGrowth is met
+// with 16 alike, and the same loop of 16 columns unrolled is a quarter slower than rolled.  So a
+// row's scores are read from tensor memory 64 columns at a time by a loop of two rounds, and P
+// goes over columns already read.  A score above the running reference by more than kGrowth is met
 // when its columns are read: reference, sum, O and the row's P so far then move by a power of
 // two, which is exact in bf16.
 //
