@@ -614,6 +614,9 @@ rb_status rb_batch_apply_update(const rb_batch* batch, const rb_batch_update* up
  * null_block) neither live nor free.  Rows outside [0, num_rows) and entries past a row's count
  * are not read or written.  The caches are those of rb_kv_write; a token's row
  * (2 * nkv * head_dim bytes) must be a multiple of 16 bytes and the bases 16-byte aligned.
+ * fork and compact act on one layer's caches and the table; the caches of other layers that
+ * share the table follow with rb_pages_copy: after a fork from the source row's entry c / page to
+ * the new row's, after compact from page i to d_page_map[i] (skipping -1 and i itself).
  */
 typedef struct rb_page_tables {
   int32_t num_rows;        /* rows of the tables (<= max_num_reqs) */

@@ -684,7 +684,7 @@ extern "C" rb_status rb_pages_compact(const rb_dims* dims, const rb_page_tables*
   st = launch_overlapped(compact_plan_kernel, kClusterCtas, kCheckThreads, 0, s, a, w,
                          d_num_live);
   if (st != RB_OK) return st;
-  const int table_ctas = 
+  const int table_ctas =
       min(max(a.rows, (a.entries + 4095) / 4096), max(1, device_sm_count()));
   // at most half of the pages move
   const int grid = table_ctas + copy_grid(a, a.entries / 2);

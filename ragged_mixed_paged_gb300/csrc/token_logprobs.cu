@@ -637,7 +637,8 @@ rb_status launch(const LogprobArgs& a, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, Elem<T>::kBatch>, a) != cudaSuccess) return RB_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, Elem<T>::kBatch>, a) != cudaSuccess)
+    return RB_ERR_CUDA;
   note_launches(1);
   return RB_OK;
 }

@@ -25,6 +25,11 @@ class PagePool:
     one per page) is counted from the table when it is not given.  ``batch`` takes both columns
     from a ``PersistentBatch`` and acts on its live rows; before an ``apply`` that removes rows,
     free them (their page rows are gone afterwards), and after one that adds pages, ``count``.
+
+    Further layers whose caches the same table names follow with ``copy`` on pools of their own:
+    after ``fork`` from the source row's entry ``cached // page tokens`` to the new row's (-1
+    where the cached tokens end at a page's end), after ``compact`` from page i to
+    ``page_map[i]`` (-1 where that is -1 or i).
     """
 
     def __init__(self, dims: rb.Dims, k_cache, v_cache, block_table=None, num_blocks=None,

@@ -310,3 +310,79 @@ def test_pool_of_a_persistent_batch(rb):
     snap = batch.snapshot()
     assert [b.tolist() for b in snap["blocks"]] == [[], [3], [2, 4, 1]]
     assert int(pool.error_word.item()) == 0 and int(batch.error_word.item()) == 0
+
+
+@pytest.mark.parametrize("geo", [dict(), dict(r=2, null=2), dict(nkv=8, hd=128)])
+def test_a_second_layer_follows_with_copies(rb, geo):
+    """Fork and compact through one layer's pool; a second layer's caches follow by copies, and
+    every row reads the same tokens in both layers as before."""
+    s = State(rb, 31, rows=10, spare=30, **geo)
+    k2, v2 = s.k.flip(0).contiguous(), s.v.flip(0).contiguous()
+    layer = rb.PagePool(s.dims, k2, v2)
+    cached = s.cached.copy()
+    gone = [i for i in range(s.rows) if i % 3 == 0 and s.table[i]]
+    s.pool.free(s.i32(gone))
+    ref.free(s.table, s.ref, gone)
+    cached[gone] = 0
+    empty = [i for i in range(s.rows) if not s.table[i]][:3]
+    src = [i for i in range(s.rows) if s.table[i]][:len(empty)]
+    empty = empty[:len(src)]
+
+    def tokens(kv, row, n):
+        bt = s.bt[row].long().cpu()
+        slots = torch.cat([bt[j] * s.pt + torch.arange(s.pt) for j in range(-(-n // s.pt))])[:n]
+        return kv.view(torch.int16).cpu()[slots]
+
+    want = {d: [tokens(c, r, int(cached[r])) for c in (s.k, s.v, k2, v2)]
+            for r, d in zip(src, empty)}
+    want.update({r: want[d] for r, d in zip(src, empty)})
+
+    full = cached[src] // s.pt
+    s.pool.fork(s.i32(src), s.i32(empty), s.i32(cached))
+    at = torch.as_tensor(np.minimum(full, s.MB - 1)).long().cuda()
+    skip = s.i32(cached[src] % s.pt) == 0
+    entry = lambda rows: s.bt[torch.as_tensor(rows).cuda(), at].masked_fill(skip, -1)
+    layer.copy(entry(src).contiguous(), entry(empty).contiguous())
+    page_map = torch.empty(s.E, dtype=torch.int32, device="cuda")
+    s.pool.compact(page_map=page_map)
+    ids = torch.arange(s.E, dtype=torch.int32, device="cuda")
+    layer.copy(ids.masked_fill((page_map == ids) | (page_map < 0), -1), page_map)
+    torch.cuda.synchronize()
+    assert int(s.pool.error_word.item()) == 0 and int(layer.error_word.item()) == 0
+    assert any(int(cached[r]) % s.pt for r in src)
+    for row, parts in want.items():
+        for c, part in zip((s.k, s.v, k2, v2), parts):
+            assert torch.equal(tokens(c, row, len(part)), part)
+
+
+def test_captured_behind_a_join_of_two_streams(rb):
+    """Calls that may start beside the kernel before them, captured where two branches of the
+    graph meet, behind a memcpy and behind a memset: all of what comes before is waited for."""
+    s = State(rb, 33, rows=8, spare=40)
+    free = [i for i, c in enumerate(s.ref) if c == 0 and i != s.null]
+    live = [i for i, c in enumerate(s.ref) if c > 0]
+    n = min(len(free), len(live), 12)
+    src, dst = s.i32([-1] * n), s.i32([-1] * n)
+    src_now, dst_now = s.i32(live[:n]), s.i32(free[:n])
+    scratch = torch.zeros(1 << 24, device="cuda")
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    main.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                scratch.add_(1.0)      # the longer branch
+            src.copy_(src_now)
+        dst.add_(dst_now + 1)          # -1 + id + 1
+        main.wait_stream(side)
+        s.pool.copy(src, dst)          # two branches, one of them a memcpy
+        s.pool.count()                 # a memset and a kernel
+        s.pool.compact()
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(live[:n], free[:n]):
+        for h in s.host:
+            h[b] = h[a]
+    ref.compact(s.table, s.ref, s.null, s.host)
+    s.check()

@@ -360,3 +360,18 @@ def test_infinities_and_nan_stay_with_the_rows_that_see_them(rb, nh, nkv, hd, ki
     assert not bool(finite.all())
     if kind != "prefix":      # (there every row may see a NaN key)
         assert bool(finite.any())
+
+
+def test_a_step_without_requests_writes_padding_only(rb):
+    spec = wl.batch_from_lists([5], [3], num_q_heads=4, num_kv_heads=2, head_dim=128, seed=1)
+    tens, _ = _setup(rb, spec)
+    q = torch.randn(24, 4, 128, device="cuda").to(torch.bfloat16)
+    out = torch.full_like(q, 3.0)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    work = torch.empty(rb.workspace_size(dims_of(spec), 1, 8), dtype=torch.uint8, device="cuda")
+    r = _rules(rb, softcap=20.0, slopes=_alibi(4), key_start=[0], prefix_lens=[0])
+    rb.paged_attention_scored(dims_of(spec), 0, 0, q, tens.k_cache, tens.v_cache,
+                              i32(spec.block_table), i32([0]), i32([0]), r, out=out,
+                              workspace=work, error_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and not out.any()
