@@ -15,11 +15,11 @@
 // The top k takes no part in that loop but maxima: each thread keeps the largest logit of each of
 // up to eight segments of its share.  The k-th largest of 64 lane groups' maxima bounds the k-th
 // largest logit from below; only segments whose maximum reaches it hold candidates, about k of
-// the 2048 of a CTA, and those are read again (mostly from L2).
+// the 8 per thread of a CTA, and those are read again (mostly from L2).
 //
 // Bound by HBM for many rows, by the chain of dependent steps (about 8 us) for few.  The next
-// batch of 16-byte loads is issued before the current one is worked on, and four CTAs per SM of
-// 256 threads hide each other's selection step.
+// batch of 16-byte loads is issued before the current one is worked on, and the four CTAs of an SM
+// of 256 threads (eight of 128 for short rows) hide each other's selection step.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
@@ -32,15 +32,13 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kGroups = 64;       // lane groups whose maxima bound the k-th logit
-constexpr int kPerGroup = kThreads / kGroups;
 constexpr int kSegments = 8;      // of a thread's share of the row, each with its own maximum
-constexpr int kPerSm = 1024 / kThreads;  // CTAs per SM
-constexpr int kMaxTop = 32;
+constexpr int kThreadsPerSm = 1024;
+constexpr int kMaxTop = 32, kFew = 8;
 constexpr int kMaxSplits = 8;     // CTAs of a cluster that share one row
 constexpr int kCandidates = 1024;
+constexpr long long kNarrowRow = 128 << 10;  // bytes up to which a row takes 128 threads
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // Differences to the reference are taken as at least kFar, so that masked (-inf) logits add
 // 2^t t = 0 rather than 0 * inf.
@@ -229,7 +227,9 @@ __device__ __forceinline__ Part warp_merge(Part p) {
   return p;
 }
 
+template <int kThreads>
 struct Shared {
+  static constexpr int kWarps = kThreads / 32;
   alignas(16) float group_max[kGroups];  // read four at a time
   Part warp[kWarps];
   Part part;
@@ -276,15 +276,32 @@ struct Slice {
 // The top entries of a slice, in order, through emit(rank, entry); returns how many there are
 // (min(k, elements)).  Thread t read vectors w0 + t + j * kThreads; segment g of its share are
 // j in [g * per, (g + 1) * per), with maximum seg[g]; `edge_x` is its edge element (edge_i >= 0).
-template <class T, class Emit>
+template <class T, int kThreads, class Emit>
 __device__ __forceinline__ int slice_top(const Slice<T>& sl, int k, const float (&seg)[kSegments],
-                                         int per, float edge_x, int edge_i, Shared& sh,
+                                         int per, float edge_x, int edge_i, Shared<kThreads>& sh,
                                          Emit&& emit) {
   using E = Elem<T>;
+  constexpr int kWarps = kThreads / 32, kPerGroup = kThreads / kGroups;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int want = min(k, max(0, sl.hi() - sl.lo()));
   if (want == 0) return 0;
-  {  // rank of each group's maximum, the others shared out over its threads
+  // The want-th largest group maximum: for few, one warp takes the largest that many times; for
+  // many, every group's rank is counted, by all threads (8192 x 8000 bf16, top 5: 58 us against 64
+  // by ranks; 2047 x 100003 fp32, top 20: 147 by ranks against 150).
+  if (want <= kFew) {
+    if (warp == 0) {
+      float x = sh.group_max[lane], y = sh.group_max[lane + 32], m = 0.f;
+      for (int i = 0; i < want; ++i) {
+        m = warp_max(fmaxf(x, y));
+        const unsigned who = __ballot_sync(0xffffffffu, x == m || y == m);
+        if (lane == __ffs(who) - 1) {
+          if (x == m) x = -INFINITY;
+          else y = -INFINITY;
+        }
+      }
+      if (lane == 0) sh.tau = m;
+    }
+  } else {
     const int g = tid / kPerGroup, share = tid % kPerGroup;
     const float x = sh.group_max[g];
     int rank = 0;
@@ -428,10 +445,12 @@ struct RowResult {
   }
 };
 
-template <class T, int kBatch>
-__global__ void __launch_bounds__(kThreads, kPerSm) token_logprobs_kernel(LogprobArgs a) {
+template <class T, int kBatch, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreadsPerSm / kThreads)
+    token_logprobs_kernel(LogprobArgs a) {
   using E = Elem<T>;
-  __shared__ Shared sh;
+  constexpr int kWarps = kThreads / 32, kPerGroup = kThreads / kGroups;
+  __shared__ Shared<kThreads> sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int splits = static_cast<int>(cluster.num_blocks());
   const int split = static_cast<int>(cluster.block_rank());
@@ -572,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) token_logprobs_kernel(Logpro
                 });
   } else {
     cluster.sync();  // every CTA has started: its shared memory may be written
-    Shared* first = cluster.map_shared_rank(&sh, 0);
+    Shared<kThreads>* first = cluster.map_shared_rank(&sh, 0);
     if (tid == 0) first->parts[split] = p;
     if (a.top > 0) {
       for (int c = tid; c < kMaxTop; c += kThreads)
@@ -620,6 +639,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) token_logprobs_kernel(Logpro
 
 template <class T>
 rb_status launch(const LogprobArgs& a, cudaStream_t s) {
+  constexpr int kBatch = Elem<T>::kBatch;
   const int sms = max(1, device_sm_count());
   // CTAs per row: enough to give every SM two, each with at least 8 KiB of the row
   const long long row_bytes = static_cast<long long>(a.vocab) * sizeof(T);
@@ -627,9 +647,13 @@ rb_status launch(const LogprobArgs& a, cudaStream_t s) {
   while (splits < kMaxSplits && static_cast<long long>(a.rows) * splits < 2LL * sms &&
          row_bytes / (2 * splits) >= 8192)
     splits *= 2;
+  // A short row's fixed steps weigh as much as its elements: twice as many CTAs per SM hide them
+  // better.  4096 rows of 16-bit logits, 256 -> 128 threads: 8000 wide (8192 rows) 86 -> 64 us,
+  // 32000 83 -> 73, 50021 108 -> 100, 128000 214 -> 223; 6080 x 100000 fp32 391 -> 415.
+  const bool narrow = splits == 1 && row_bytes <= kNarrowRow;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(a.rows) * splits));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(narrow ? 128 : 256);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -637,8 +661,9 @@ rb_status launch(const LogprobArgs& a, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, Elem<T>::kBatch>, a) != cudaSuccess)
-    return RB_ERR_CUDA;
+  void (*kernel)(LogprobArgs) = narrow ? token_logprobs_kernel<T, kBatch, 128>
+                                       : token_logprobs_kernel<T, kBatch, 256>;
+  if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return RB_ERR_CUDA;
   note_launches(1);
   return RB_OK;
 }

@@ -187,3 +187,17 @@ def test_no_rows(rb):
     x = torch.empty(0, 100, device="cuda", dtype=torch.bfloat16)
     got = rb.token_logprobs(x, torch.empty(0, dtype=torch.int32, device="cuda"), 3)
     assert got.top_ids.shape == (0, 3)
+
+
+@pytest.mark.parametrize("dtype,vocab", [(torch.bfloat16, 1000), (torch.bfloat16, 65536),
+                                         (torch.bfloat16, 65537), (torch.float16, 5003),
+                                         (torch.float32, 32768), (torch.float32, 32769)])
+@pytest.mark.parametrize("top", [1, 8, 9, 32])
+def test_rows_enough_for_every_sm(rb, dtype, vocab, top):
+    """One CTA per row, of 128 or 256 threads; logits of few values, so that the bound on the
+    top entries is met many times."""
+    rows = 2 * torch.cuda.get_device_properties(0).multi_processor_count + 3
+    g = torch.Generator(device="cuda").manual_seed(vocab + top)
+    x = (torch.randn(rows, vocab, device="cuda", generator=g) * 40).round() / 8
+    tok = torch.randint(0, vocab, (rows,), device="cuda", generator=g)
+    _check(rb, x.to(dtype), tok.tolist(), top)
