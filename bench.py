@@ -63,11 +63,11 @@ FLUSH_BYTES = 512 << 20
 # its planner's code, comments left out): a figure is reported only while the code is the code
 # it was measured on.
 KNOWN_TRAFFIC = {
-    (2, "dc5594e866228332"): 78999808 + 3906048,
-    (3, "dc5594e866228332"): 4545301248 + 26047488,
+    (2, "c8f9eb99a5b6211b"): 78987008 + 3487232,
+    (3, "c8f9eb99a5b6211b"): 4545612800 + 26181120,
     # the stream: mean over the launches of stream steps 5..99 (the default timed steps)
-    (4, "dc5594e866228332"): 9545384569 + 80824829,
-    (5, "dc5594e866228332"): 7021283840 + 114328832,
+    (4, "c8f9eb99a5b6211b"): 9554043047 + 80905984,
+    (5, "c8f9eb99a5b6211b"): 7125457152 + 114908416,
 }
 
 WORKLOAD_NAMES = {1: "pages' worked example A/B/C", 2: "pages' padding example",

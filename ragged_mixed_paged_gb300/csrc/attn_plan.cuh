@@ -103,6 +103,13 @@ constexpr float kPreUnitUs = 8.f, kPreTileUs = 2.3f;
 // What score rules add to a key tile of a prefill unit (chunks alone, 128-key tiles of two 128-row
 // query tiles at head_dim 128: 1.9 us without rules, +0.4 biased, +0.6 capped).
 constexpr float kBiasTileUs = 0.4f, kCapTileUs = 0.6f;
+// Scored calls weigh the splits' merge, one warp per (request, kv head), against the pages of one
+// split: sp pages cost sp a, the merge of P / sp splits P / sp b, least at sp = sqrt(P b / a).
+// Measured with b / a = 0.8 against kMinSplitPages alone (8 kv heads unless said): one decode of
+// 32000 tokens 129 -> 80 us, 6 of 16000 174 -> 101, 24 of 500 to 8000 113 -> 78, 40 of 256 to 32000
+// with one kv head 240 -> 84; 256 of 512 to 8192, whose splits are longer anyway, 464 either way.
+// With 0.6 the second and third are 109 and 82 us, with 1.0 109 and 80, with 1.5 116 and 84.
+constexpr float kSplitCost = 0.8f;
 constexpr int kTileBins = 512;  // histogram bins of prefill units by key tiles (longer: last bin)
 
 // The planner, run by one whole CTA of any size: validates the metadata, classifies requests,
@@ -115,6 +122,7 @@ constexpr int kTileBins = 512;  // histogram bins of prefill units by key tiles 
 template <bool kScored = false>
 __device__ __forceinline__ void plan_body(const AttnArgs& a, int head_dim, ReqSrc src) {
   __shared__ unsigned long long s_pages;
+  __shared__ int s_longest;  // pages of the longest decode request (scored calls)
   const int tid = threadIdx.x, nthreads = blockDim.x, lane = tid & 31;
   const int per = (a.R + nthreads - 1) / nthreads;  // the same for every thread
   const int lo = min(tid * per, a.R), hi = min(lo + per, a.R);
@@ -135,17 +143,26 @@ __device__ __forceinline__ void plan_body(const AttnArgs& a, int head_dim, ReqSr
   int bits = 0;
   if (tid == 0) {
     s_pages = 0;
+    if constexpr (kScored) s_longest = 0;
     if (src.qsl[0] != 0 || src.qsl[a.R] != a.N) bits |= RB_EBIT_ATTN_META;
   }
   __syncthreads();
   unsigned long long my_pages = 0;
+  int my_longest = 0;
   each([&](int, const ReqInfo& x) {
     if (!x.ok) bits |= RB_EBIT_ATTN_META;
-    else if (is_decode_class(x.q, a.group)) my_pages += static_cast<unsigned long long>(x.pages);
+    else if (is_decode_class(x.q, a.group)) {
+      my_pages += static_cast<unsigned long long>(x.pages);
+      if constexpr (kScored) my_longest = max(my_longest, x.pages);
+    }
   });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) my_pages += __shfl_xor_sync(0xffffffffu, my_pages, o);
   if (lane == 0 && my_pages) atomicAdd(&s_pages, my_pages);
+  if constexpr (kScored) {
+    my_longest = __reduce_max_sync(0xffffffffu, my_longest);
+    if (lane == 0 && my_longest) atomicMax(&s_longest, my_longest);
+  }
   __syncthreads();
   const long long page_heads = static_cast<long long>(s_pages) * a.nkv;
   // Fused launch: splits are sized for every CTA of the launch (all of them may end up helping
@@ -153,8 +170,10 @@ __device__ __forceinline__ void plan_body(const AttnArgs& a, int head_dim, ReqSr
   const int target = a.fused_ctas > 0
                          ? min(kMaxTargetUnits, 4 * a.decode_warps_per_cta * a.fused_ctas)
                          : a.target_units;
-  const int sp = static_cast<int>(max(static_cast<long long>(kMinSplitPages),
-                                      (page_heads + target - 1) / target));
+  int sp = static_cast<int>(max(static_cast<long long>(kMinSplitPages),
+                                (page_heads + target - 1) / target));
+  if constexpr (kScored)
+    sp = max(sp, static_cast<int>(sqrtf(kSplitCost * static_cast<float>(s_longest))));
   auto units_of = [&](const ReqInfo& x, int* d, int* p) {
     if (!x.ok || x.q == 0) return;
     if (is_decode_class(x.q, a.group)) *d += (x.pages + sp - 1) / sp * a.nkv;

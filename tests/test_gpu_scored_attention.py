@@ -375,3 +375,17 @@ def test_a_step_without_requests_writes_padding_only(rb):
                               workspace=work, error_word=err)
     torch.cuda.synchronize()
     assert int(err.item()) == 0 and not out.any()
+
+
+@pytest.mark.parametrize("nh,nkv,hd", [(8, 1, 128), (8, 2, 64), (6, 3, 128), (16, 1, 64)])
+def test_merges_of_many_splits(rb, nh, nkv, hd):
+    """Splits of one to some hundred per request, next to each other; infinities in the last."""
+    spec = wl.batch_from_lists([33000, 12345, 4100, 130, 15, 1], [1, 1, 1, 1, 1, 1],
+                               num_q_heads=nh, num_kv_heads=nkv, head_dim=hd, seed=nh)
+    tens = wl.make_tensors(spec, device="cuda")
+    tens.hist_v[0][-1, :, 3] = float("inf")
+    tens.hist_v[1][5, :, 4] = float("-inf")
+    for hist, cache in ((tens.hist_k, tens.k_cache), (tens.hist_v, tens.v_cache)):
+        wl.place_history(spec, hist, cache)
+    _check(rb, spec, tens=tens)
+    _check(rb, spec, slopes=_alibi(nh), key_start=[1000, 0, 4090, 5, 16, 0])
