@@ -75,7 +75,7 @@ __device__ void softmax_scored(const AttnArgs& a, TcShared<true>& sh, uint32_t t
     const int n = un.n[x];
     // row t of this tile: token tok_base + t / group, head t % group of the kv head's group;
     // rows past T * group (a group that does not divide 128) or past the last token hold no
-    // query: every key is masked for them and they are never stored
+    // query: they may compute anything, have no say in the warp's votes and are never stored
     const int tok_base = un.tok0 + a.tile_tokens * x;
     const int rows_used = a.tile_tokens * a.group;
     const int jt_in = t / a.group;
@@ -83,7 +83,6 @@ __device__ void softmax_scored(const AttnArgs& a, TcShared<true>& sh, uint32_t t
     const int jt = valid ? tok_base + jt_in : 0;
     const int hh = valid ? t - jt_in * a.group : 0;
     const int pos = un.c + jt;
-    const bool partial = rows_used < C::kM || tok_base + a.tile_tokens > un.q;
     // the row's keys [lo, hi), its slope, and the smallest hi of the tile's rows
     int lo = 0, hi = 0;
     bool blind = false;
@@ -110,8 +109,11 @@ __device__ void softmax_scored(const AttnArgs& a, TcShared<true>& sh, uint32_t t
     // V slots back to the producers as its S tiles land.
     const bool releases = x == (un.n[1] > 0 ? 1 : 0);
     // Running reference (log2 units, a whole number unless fixed) and sum.  A row that has seen
-    // no key is at -inf; one without a query starts at 0.
-    float m_ref = !valid ? 0.f : bounded ? a.cap_log2 - kCapHeadroom : -INFINITY, l = 0.f;
+    // no key is at -inf; one without a query stays at +inf, where no score moves it.  (Masking
+    // such rows' keys made every tile of a group like 6 or 7 a masked one: prompts of 300 to 1500
+    // tokens with 12 / 2 heads of 64 and a bias 97 us, so 83.)
+    const float cap_s = valid ? a.cap_s : INFINITY;
+    float m_ref = !valid ? INFINITY : bounded ? a.cap_log2 - kCapHeadroom : -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const uint32_t tj = tc_x + j;
@@ -157,7 +159,7 @@ __device__ void softmax_scored(const AttnArgs& a, TcShared<true>& sh, uint32_t t
         }
       }
       tc::fence_after_sync();
-      const bool masked = partial || kv_base < un.lo_max[x] || kv_base + C::kN > hi_min;
+      const bool masked = kv_base < un.lo_max[x] || kv_base + C::kN > hi_min;
       // a key past its query, where the distance changes sign, needs |p - k| taken
       const bool past = kBias && kv_base + C::kN > un.c + tok_base + 1;
       const unsigned seen0 = static_cast<unsigned>(kv_base - lo), n_seen = hi - lo;
@@ -219,7 +221,7 @@ __device__ void softmax_scored(const AttnArgs& a, TcShared<true>& sh, uint32_t t
           float top = fmaxf(fabsf(s[0]), fabsf(s[1]));
 #pragma unroll
           for (int i = 2; i < kCols; i += 2) top = fmax3(top, fabsf(s[i]), fabsf(s[i + 1]));
-          plain_cap = bounded && !__any_sync(0xffffffffu, top > a.cap_s);
+          plain_cap = bounded && !__any_sync(0xffffffffu, top > cap_s);
         }
         float b[kCols];  // bias, less the reference where that is fixed
         if constexpr (kBias) {
