@@ -12,7 +12,7 @@
 // two, which is exact in bf16.
 //
 // Measured on four chunks of 1-2 k tokens over up to 16 k cached ones (32 / 8 heads of 128; the
-// ordinary launch 646 us, 0.74 of the bf16 rate): no rule 718 us, soft cap 910, distance bias 858.
+// ordinary launch 646 us, 0.74 of the bf16 rate): no rule 710 us, soft cap 900, distance bias 859.
 // With all 128 scores kept in registers and the maximum taken once per tile: 695, 1102, 828; in
 // rounds of 16 columns 961, 1037, 1064; of 32 763, 949, 892; with the next columns' loads ahead of
 // the current ones' work (twice the code) 850, 992, 985 for 32.
