@@ -594,27 +594,31 @@ __global__ void __launch_bounds__(kThreads, kThreadsPerSm / kThreads)
     Shared<kThreads>* first = cluster.map_shared_rank(&sh, 0);
     if (tid == 0) first->parts[split] = p;
     if (a.top > 0) {
-      for (int c = tid; c < kMaxTop; c += kThreads)
-        first->merged[split * kMaxTop + c] = Entry{-INFINITY, 0x7fffffff};
+      for (int c = tid; c < a.top; c += kThreads)
+        first->merged[split * a.top + c] = Entry{-INFINITY, 0x7fffffff};
       __syncthreads();
       slice_top(sl, a.top, seg, seg_batches * kBatch, edge_x, edge_i, sh,
-                [&](int rank, const Entry& e) { first->merged[split * kMaxTop + rank] = e; });
+                [&](int rank, const Entry& e) { first->merged[split * a.top + rank] = e; });
     }
     cluster.sync();
     if (split != 0) return;
     p = warp_merge<kMaxSplits>(lane % kMaxSplits < splits ? sh.parts[lane % kMaxSplits]
                                                           : no_part());
     const RowResult row(p);
-    if (a.top > 0 && !row.bad) {
-      for (int c = tid; c < splits * kMaxTop; c += kThreads) {
-        const Entry e = sh.merged[c];
-        if (e.i == 0x7fffffff) continue;
-        int rank = 0;
-#pragma unroll 8
-        for (int j = 0; j < splits * kMaxTop; ++j) rank += before(sh.merged[j], e);
-        if (rank < n_top) {
-          a.top_ids[top_row + rank] = e.i;
-          a.top_logprobs[top_row + rank] = row.logprob(e.x);
+    if (warp == 0 && !row.bad) {  // merges the lists, lane l at the next entry of CTA l's
+      const Entry end{-INFINITY, 0x7fffffff};
+      auto entry = [&](int at) {
+        return lane < splits && at < a.top ? sh.merged[lane * a.top + at] : end;
+      };
+      int at = 0;
+      Entry e = entry(0);
+      for (int k = 0; k < (a.top > 0 ? n_top : 0); ++k) {
+        const float x = warp_max(e.x);
+        const int i = __reduce_min_sync(0xffffffffu, e.x == x ? e.i : end.i);
+        if (e.i == i && i != end.i) {
+          a.top_ids[top_row + k] = i;
+          a.top_logprobs[top_row + k] = row.logprob(e.x);
+          e = entry(++at);
         }
       }
     }

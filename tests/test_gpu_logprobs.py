@@ -201,3 +201,14 @@ def test_rows_enough_for_every_sm(rb, dtype, vocab, top):
     x = (torch.randn(rows, vocab, device="cuda", generator=g) * 40).round() / 8
     tok = torch.randint(0, vocab, (rows,), device="cuda", generator=g)
     _check(rb, x.to(dtype), tok.tolist(), top)
+
+
+@pytest.mark.parametrize("rows", [2, 400])
+def test_zeros_of_either_sign_are_equal(rb, rows):
+    """In one CTA's list and where the lists of a row's CTAs are merged."""
+    x = torch.full((rows, 40000), -1.0)
+    x[:, 7::97] = 0.0
+    x[:, 104::194] = -0.0
+    x[::2, 39990] = -0.0
+    for top in (3, 20):
+        _check(rb, x.to(torch.bfloat16).cuda(), [104] * rows, top)
