@@ -17,7 +17,7 @@
 // largest logit from below; only segments whose maximum reaches it hold candidates, about k of
 // the 8 per thread of a CTA, and those are read again (mostly from L2).
 //
-// Bound by HBM for many rows, by the chain of dependent steps (about 8 us) for few.  The next
+// Bound by HBM for many rows, by the chain of dependent steps (4 to 7 us) for few.  The next
 // batch of 16-byte loads is issued before the current one is worked on, and the four CTAs of an SM
 // of 256 threads (eight of 128 for short rows) hide each other's selection step.
 #include <cooperative_groups.h>
@@ -38,7 +38,7 @@ constexpr int kThreadsPerSm = 1024;
 constexpr int kMaxTop = 32, kFew = 8;
 constexpr int kMaxSplits = 8;     // CTAs of a cluster that share one row
 constexpr int kCandidates = 1024;
-constexpr long long kNarrowRow = 128 << 10;  // bytes up to which a row takes 128 threads
+constexpr long long kNarrowRow = 256 << 10;  // bytes up to which a row takes 128 threads
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // Differences to the reference are taken as at least kFar, so that masked (-inf) logits add
 // 2^t t = 0 rather than 0 * inf.
@@ -98,12 +98,11 @@ struct Elem<float> {
 };
 // 16-bit types, two per word; less() is the mixed-precision subtraction, which converts as it
 // subtracts (an unpacking instruction less per element).
-// kBatch, vectors taken at a time with as many on their way, is 16 elements for every type: the
-// loop then fits the instruction cache next to the scheduler.  4096 x 128000 bf16: 214 us, with
-// 32 elements 225 us (fewer, 8, 236); 2047 x 100003 fp32: 147 us, with 8 elements 165 us.
+// kBatch, vectors taken at a time with as many on their way.  4096 x 128000 bf16: 194 us, with 3
+// vectors 196, with 2 215; 2047 x 100003 fp32: 147 us, with 2 vectors 165, with 6 (spills) 197.
 template <class T, class Ops>
 struct Elem16 {
-  static constexpr int kPer = 8, kBatch = 2;
+  static constexpr int kPer = 8, kBatch = 4;
   static __device__ __forceinline__ float one(const T* p) {
     return Ops::two(__ldg(reinterpret_cast<const unsigned short*>(p))).x;
   }
@@ -286,8 +285,8 @@ __device__ __forceinline__ int slice_top(const Slice<T>& sl, int k, const float 
   const int want = min(k, max(0, sl.hi() - sl.lo()));
   if (want == 0) return 0;
   // The want-th largest group maximum: for few, one warp takes the largest that many times; for
-  // many, every group's rank is counted, by all threads (8192 x 8000 bf16, top 5: 58 us against 64
-  // by ranks; 2047 x 100003 fp32, top 20: 147 by ranks against 150).
+  // many, every group's rank is counted, by all threads (8192 x 8000 bf16, top 5: 56 us against 58
+  // by ranks; 2047 x 100003 fp32, top 20: 145 by ranks against 150).
   if (want <= kFew) {
     if (warp == 0) {
       float x = sh.group_max[lane], y = sh.group_max[lane + 32], m = 0.f;
@@ -528,44 +527,52 @@ __global__ void __launch_bounds__(kThreads, kThreadsPerSm / kThreads)
   const int seg_batches = max(1, (batches + kSegments - 1) / kSegments);
   float seg[kSegments];
 #pragma unroll
-  for (int g = 0; g < kSegments; ++g) {
-    float top = -INFINITY;  // largest element of this segment
+  for (int g = 0; g < kSegments; ++g) seg[g] = -INFINITY;
+  float top = -INFINITY;  // largest element of segment `at`, which ends before batch `end`
+  int at = 0, end = seg_batches;
+  // (one copy of the loop's code for all segments: with one for each, fetched anew, 4096 x 128000
+  // bf16 took 214 us at its best batch, 4096 x 32000 71, now 194 and 60)
 #pragma unroll 1
-    for (int b = g * seg_batches; b < min(batches, (g + 1) * seg_batches); ++b) {
-      const int v = sl.w0 + tid + b * (kBatch * kThreads);
-      uint4 u[kBatch];
+  for (int b = 0; b < batches; ++b) {
+    const int v = sl.w0 + tid + b * (kBatch * kThreads);
+    uint4 u[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      u[k] = next[k];
+      if (v + k * kThreads >= stop) {  // past the end: -inf counts for nothing
+        u[k] = make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
+        clamp = true;
+      }
+    }
+    fetch(v + kBatch * kThreads);
+    const float mx = E::largest(u);
+    top = fmaxf(top, mx);
+    if (mx > xt) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        u[k] = next[k];
-        if (v + k * kThreads >= stop) {  // past the end: -inf counts for nothing
-          u[k] = make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
-          clamp = true;
-        }
-      }
-      fetch(v + kBatch * kThreads);
-      const float mx = E::largest(u);
-      top = fmaxf(top, mx);
-      if (mx > xt) {
+        float2 x[E::kPer / 2];
+        E::unpack(u[k], x);
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          float2 x[E::kPer / 2];
-          E::unpack(u[k], x);
-#pragma unroll
-          for (int j = 0; j < E::kPer / 2; ++j) above += (x[j].x > xt) + (x[j].y > xt);
-        }
+        for (int j = 0; j < E::kPer / 2; ++j) above += (x[j].x > xt) + (x[j].y > xt);
       }
-      if (mx > ref + kGrowth) move_to(mx);
-      float2 bs, bw;
-      if (!clamp) {
-        batch_sums(u, std::false_type{}, bs, bw);
-        clamp = isnan(bw.x + bw.y);
-      }
-      if (clamp) batch_sums(u, std::true_type{}, bs, bw);
-      s2 = __fadd2_rn(s2, bs);
-      w2 = __fadd2_rn(w2, bw);
     }
-    seg[g] = top;
-    most = fmaxf(most, top);
+    if (mx > ref + kGrowth) move_to(mx);
+    float2 bs, bw;
+    if (!clamp) {
+      batch_sums(u, std::false_type{}, bs, bw);
+      clamp = isnan(bw.x + bw.y);
+    }
+    if (clamp) batch_sums(u, std::true_type{}, bs, bw);
+    s2 = __fadd2_rn(s2, bs);
+    w2 = __fadd2_rn(w2, bw);
+    if (b + 1 == end || b + 1 == batches) {
+#pragma unroll
+      for (int g = 0; g < kSegments; ++g) seg[g] = g == at ? top : seg[g];
+      most = fmaxf(most, top);
+      top = -INFINITY;
+      ++at;
+      end += seg_batches;
+    }
   }
   Part mine{Sums{ref, s2.x + s2.y, w2.x + w2.y}, most, above};
   float group = mine.max;
@@ -652,8 +659,8 @@ rb_status launch(const LogprobArgs& a, cudaStream_t s) {
          row_bytes / (2 * splits) >= 8192)
     splits *= 2;
   // A short row's fixed steps weigh as much as its elements: twice as many CTAs per SM hide them
-  // better.  4096 rows of 16-bit logits, 256 -> 128 threads: 8000 wide (8192 rows) 86 -> 64 us,
-  // 32000 83 -> 73, 50021 108 -> 100, 128000 214 -> 223; 6080 x 100000 fp32 391 -> 415.
+  // better.  16-bit logits, 256 -> 128 threads: 8192 x 8000 85 -> 56 us, 4096 x 32000 71 -> 60,
+  // 4096 x 128000 194 -> 192; 6080 x 100000 fp32 384 -> 403.
   const bool narrow = splits == 1 && row_bytes <= kNarrowRow;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(a.rows) * splits));

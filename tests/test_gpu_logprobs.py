@@ -191,7 +191,9 @@ def test_no_rows(rb):
 
 @pytest.mark.parametrize("dtype,vocab", [(torch.bfloat16, 1000), (torch.bfloat16, 65536),
                                          (torch.bfloat16, 65537), (torch.float16, 5003),
-                                         (torch.float32, 32768), (torch.float32, 32769)])
+                                         (torch.float32, 32768), (torch.float32, 32769),
+                                         (torch.bfloat16, 131072), (torch.bfloat16, 131073),
+                                         (torch.float32, 65537)])
 @pytest.mark.parametrize("top", [1, 8, 9, 32])
 def test_rows_enough_for_every_sm(rb, dtype, vocab, top):
     """One CTA per row, of 128 or 256 threads; logits of few values, so that the bound on the
