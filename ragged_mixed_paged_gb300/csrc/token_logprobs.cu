@@ -195,7 +195,8 @@ struct Entry {
   int i;
 };
 __device__ __forceinline__ bool before(const Entry& a, const Entry& b) {  // a ranks before b
-  return a.x > b.x || (a.x == b.x && a.i < b.i);
+  // no branch: it ranks hundreds of entries (3 x 306 bf16, top 20: 50 us with one, 12 without)
+  return (a.x > b.x) | ((a.x == b.x) & (a.i < b.i));
 }
 
 struct Part {  // what one thread, warp, CTA or cluster found
