@@ -26,6 +26,10 @@ class PagePool:
     from a ``PersistentBatch`` and acts on its live rows; before an ``apply`` that removes rows,
     free them (their page rows are gone afterwards), and after one that adds pages, ``count``.
 
+    What the constructor fills and counts is queued on its ``stream`` (None: the current one) and a
+    call's work on the stream it is given; a caller that goes on with another stream lets that
+    one wait for the first, as with any tensor.
+
     Further layers whose caches the same table names follow with ``copy`` on pools of their own:
     after ``fork`` from the source row's entry ``cached // page tokens`` to the new row's (-1
     where the cached tokens end at a page's end), after ``compact`` from page i to
@@ -54,11 +58,20 @@ class PagePool:
         self._k = rb._ptr(k_cache, torch.bfloat16, "k_cache")
         self._v = self._pointer(v_cache, torch.bfloat16, "v_cache")
         self.num_pages = dims.num_blocks // max(1, dims.kernel_blocks_per_manager_block)
-        new = lambda n, dtype: torch.zeros(n, dtype=dtype, device=self.device)
-        self.error_word = new(1, torch.int32) if error_word is None else error_word
+        if stream is not None:
+            rb._stream_on(self.device, stream)  # refuses another device's
+        # what is made here is made on the stream that counts (the library clears ref_count)
+        with torch.cuda.stream(stream):
+            empty = lambda n, dtype: torch.empty(n, dtype=dtype, device=self.device)
+            if error_word is None:
+                error_word = torch.zeros(1, dtype=torch.int32, device=self.device)
+            if workspace is None:
+                workspace = empty(max(1, pages_workspace_size(dims)), torch.uint8)
+            count = block_table is not None and ref_count is None
+            if count:
+                ref_count = empty(self.num_pages, torch.int32)
+        self.error_word, self.workspace = error_word, workspace
         self._err = self._pointer(self.error_word, torch.int32, "error_word")
-        self.workspace = (new(max(1, pages_workspace_size(dims)), torch.uint8)
-                          if workspace is None else workspace)
         self._ws_bytes = self.workspace.numel()
         self._ws = self._pointer(self.workspace, torch.uint8, "workspace")
         self._dims = dims.c()
@@ -71,10 +84,7 @@ class PagePool:
             raise ValueError(f"block_table must be [rows, {dims.max_blocks_per_req}]")
         if num_blocks.numel() < block_table.shape[0]:
             raise ValueError("num_blocks is shorter than the block table")
-        count = ref_count is None
-        if count:
-            self.ref_count = new(self.num_pages, torch.int32)
-        elif ref_count.numel() != self.num_pages:
+        if ref_count.numel() != self.num_pages:
             raise ValueError(f"ref_count must have {self.num_pages} entries")
         i32 = torch.int32
         self._tables = rb.rb_page_tables(

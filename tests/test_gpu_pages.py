@@ -386,3 +386,28 @@ def test_captured_behind_a_join_of_two_streams(rb):
             h[b] = h[a]
     ref.compact(s.table, s.ref, s.null, s.host)
     s.check()
+
+
+def test_a_pool_made_on_a_busy_device(rb):
+    """A pool built for another stream while the current one is busy: what it fills and counts
+    belongs to that stream, and a fork there reads finished counts."""
+    s = State(rb, 21, rows=8, spare=12)
+    src = next(i for i in range(s.rows) if s.table[i] and s.cached[i] % s.pt)
+    dst = next(i for i in range(s.rows) if i != src)
+    s.pool.free(s.i32([dst]))
+    ref.free(s.table, s.ref, [dst])
+    s.cached[dst] = 0
+    s.check()
+    args = s.i32([src]), s.i32([dst]), s.i32(s.cached)
+    scratch = torch.zeros(1 << 26, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(200):               # some 20 ms of work on the current stream
+        scratch.add_(1.0)
+    pool = rb.PagePool(s.dims, s.k, s.v, s.bt, s.nb, stream=side)
+    pool.fork(*args, stream=side)
+    side.synchronize()
+    assert not torch.cuda.current_stream().query()      # it was busy all along
+    ref.fork(s.table, s.ref, [src], [dst], s.cached, s.pt, s.null, s.host)
+    s.pool = pool
+    s.check()
