@@ -350,9 +350,13 @@ __global__ void __launch_bounds__(kCheckThreads) __cluster_dims__(kClusterCtas, 
       bits |= RB_EBIT_ROW;
       continue;
     }
-    // the first warp to take the row's count frees it; a row named twice is then empty
+    // the first warp to take the row's count frees it; a row named twice is then empty.  A count
+    // that no row can have stays where it is.
     int held = 0;
-    if (lane == 0) held = atomicExch(a.num_blocks + r, 0);
+    if (lane == 0) {
+      held = a.num_blocks[r];
+      if (held > 0 && held <= a.MB) held = atomicCAS(a.num_blocks + r, held, 0);
+    }
     held = __shfl_sync(0xffffffffu, held, 0);
     if (held < 0 || held > a.MB) {
       bits |= RB_EBIT_ROW;

@@ -411,3 +411,24 @@ def test_a_pool_made_on_a_busy_device(rb):
     ref.fork(s.table, s.ref, [src], [dst], s.cached, s.pt, s.null, s.host)
     s.pool = pool
     s.check()
+
+
+@pytest.mark.parametrize("bad", ["over", -1, 2 ** 31 - 1, -2 ** 31])
+def test_free_leaves_a_row_with_a_bad_count_alone(rb, bad):
+    """A count outside [0, max_blocks_per_req]: the row keeps it, its entries and its pages'
+    counts; the other rows named are freed, one of them twice."""
+    s = State(rb, 10)
+    full = [i for i in range(s.rows) if s.table[i]]
+    r, other = full[0], full[1]
+    bad = s.MB + 1 if bad == "over" else bad
+    s.nb[r] = bad
+    before = s.bt.clone()
+    freed = s.i32([-9])
+    s.pool.free(s.i32([other, r, other, r]), num_freed=freed)
+    want = ref.free(s.table, s.ref, [other])
+    torch.cuda.synchronize()
+    assert int(s.pool.error_word.item()) == rb.EBIT_ROW
+    assert int(s.nb[r]) == bad and int(freed.item()) == want
+    assert torch.equal(s.bt[r], before[r])
+    s.nb[r] = len(s.table[r])
+    s.check(bits=rb.EBIT_ROW)
