@@ -146,14 +146,18 @@ __device__ __forceinline__ int key_prefix(const AttnArgs& a, int r, int L) {
   return a.prefix != nullptr ? min(L, max(0, __ldg(a.prefix + r))) : 0;
 }
 
-// First page a scored decode request (q query tokens from flat token t0, length L) reads: its
-// tokens' smallest key_start's, but always a page of the request, so that a request whose
-// tokens see nothing still has a unit that writes its zero rows.
-__device__ __forceinline__ int scored_first_page(const AttnArgs& a, int t0, int q, int L) {
+// First page a scored decode request (request r, q query tokens from flat token t0, length L) reads:
+// the one of the first key that any of its tokens sees, but always a page of the request, so
+// that a request whose tokens see nothing still has a unit that writes its zero rows.
+__device__ __forceinline__ int scored_first_page(const AttnArgs& a, int r, int t0, int q, int L) {
   if (a.key_start == nullptr) return 0;
+  const int prefix = key_prefix(a, r, L);
   int lo = 0x7fffffff;
 #pragma unroll 1
-  for (int j = 0; j < q; ++j) lo = min(lo, key_lo(a, t0 + j));
+  for (int j = 0; j < q; ++j) {
+    const int k = key_lo(a, t0 + j);
+    if (k < max(L - q + j + 1, prefix)) lo = min(lo, k);
+  }
   return min(lo / kPage, (L + kPage - 1) / kPage - 1);
 }
 

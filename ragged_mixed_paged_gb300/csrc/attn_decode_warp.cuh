@@ -196,7 +196,7 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
     const int split = local / a.nkv, h = local - split * a.nkv;
     const int t0 = a.qsl[r], q = a.qsl[r + 1] - t0, L = a.seq_lens[r];
     const int c = L - q, cols = q * a.group, pages = (L + kPage - 1) / kPage;
-    const int p_first = kScored ? scored_first_page(a, t0, q, L) : 0;
+    const int p_first = kScored ? scored_first_page(a, r, t0, q, L) : 0;
     const int p_begin = p_first + split * sp, p_end = min(p_begin + sp, pages);
     const int n_pages = p_end - p_begin;
 
@@ -219,8 +219,8 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
     const int c0 = 2 * (lane & 3), c1 = c0 + 1;
     const int lim0 = c0 < cols ? c + c0 / a.group : c;
     const int lim1 = c1 < cols ? c + c1 / a.group : c;
-    // scored: first visible key, past the last and slope of the lane's two columns, and the
-    // first key any column sees
+    // scored: first visible key, past the last and slope of the lane's two columns, and the first
+    // key any column sees (a column that sees none: past the last page, so that no page is its own)
     int lo0 = 0, lo1 = 0, hi0 = 0, hi1 = 0, lo_all = 0, lo_max = 0, hi_min = 0;
     float slope0 = 0.f, slope1 = 0.f;
     if constexpr (kScored) {
@@ -236,8 +236,10 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
         slope0 = __ldg(a.slopes + h * a.group + h0) * kLog2e;
         slope1 = __ldg(a.slopes + h * a.group + h1) * kLog2e;
       }
-      lo_all = __reduce_min_sync(0xffffffffu, min(lo0, lo1));
-      lo_max = __reduce_max_sync(0xffffffffu, max(lo0, lo1));
+      const int none = pages * kPage;
+      const int first0 = lo0 < hi0 ? lo0 : none, first1 = lo1 < hi1 ? lo1 : none;
+      lo_all = __reduce_min_sync(0xffffffffu, min(first0, first1));
+      lo_max = __reduce_max_sync(0xffffffffu, max(first0, first1));
       hi_min = __reduce_min_sync(0xffffffffu, min(hi0, hi1));
     }
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;

@@ -64,7 +64,7 @@ __device__ __forceinline__ ReqInfo req_info(const AttnArgs& a, const ReqSrc& src
   x.pages = (x.L + kPage - 1) / kPage;
   x.ok = s >= 0 && x.q >= 0 && e <= a.N && x.L >= x.q && x.pages <= a.kp_cap;
   if constexpr (kScored)  // pages a decode request reads
-    if (x.ok && is_decode_class(x.q, a.group)) x.pages -= scored_first_page(a, s, x.q, x.L);
+    if (x.ok && is_decode_class(x.q, a.group)) x.pages -= scored_first_page(a, r, s, x.q, x.L);
   return x;
 }
 

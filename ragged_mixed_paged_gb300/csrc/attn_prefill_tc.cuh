@@ -66,7 +66,7 @@ struct TcUnit {
 // B's rows see.
 struct ScoredUnit : TcUnit {
   int j0;         // first key tile
-  int lo;         // first key any row sees
+  int lo;         // first key any row sees (none: past the last page)
   int prefix;     // keys every row sees (from its own lo on)
   int lo_max[2];  // largest first key of each tile's rows (rows that see no key left out)
   int odd_first, odd_last;  // key tiles whose V held infinities or NaN that were taken out
@@ -221,7 +221,7 @@ __device__ __forceinline__ ScoredUnit scored_unit(const AttnArgs& a, int u, int 
   static_cast<TcUnit&>(un) = decode_unit(a, u);
   const int T = a.tile_tokens;
   un.prefix = key_prefix(a, un.r, un.L);
-  int lo = un.L;
+  int lo = un.pages * kPage;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     int mn = 0x7fffffff, mx = 0;
@@ -231,8 +231,9 @@ __device__ __forceinline__ ScoredUnit scored_unit(const AttnArgs& a, int u, int 
       const int end = min(un.tok0 + (x + 1) * T, un.q);
       for (int j = un.tok0 + x * T + lane; j < end; j += 32) {
         const int k = key_lo(a, un.t0 + j);
+        if (k >= max(un.c + j + 1, un.prefix)) continue;
         mn = min(mn, k);
-        if (k < max(un.c + j + 1, un.prefix)) mx = max(mx, k);
+        mx = max(mx, k);
       }
       mn = __reduce_min_sync(0xffffffffu, mn);
       mx = __reduce_max_sync(0xffffffffu, mx);

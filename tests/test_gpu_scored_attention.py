@@ -389,3 +389,42 @@ def test_merges_of_many_splits(rb, nh, nkv, hd):
         wl.place_history(spec, hist, cache)
     _check(rb, spec, tens=tens)
     _check(rb, spec, slopes=_alibi(nh), key_start=[1000, 0, 4090, 5, 16, 0])
+
+
+def _check_with_pages_gone(rb, c, q, start, gone, nh, nkv, ratio=1):
+    """One request of q tokens behind c cached ones, its pages `gone` out of the table, their
+    rows NaN and infinite."""
+    spec = wl.batch_from_lists([c], [q], num_q_heads=nh, num_kv_heads=nkv, head_dim=64, seed=c,
+                               manager_ratio=ratio)
+    tens = wl.make_tensors(spec, device="cuda")
+    table = np.array(spec.block_table)
+    for page in gone:
+        table[0, page] = -1
+        keys = slice(page * 16 * ratio, min(c, (page + 1) * 16 * ratio))
+        tens.hist_k[0][keys] = float("nan")
+        tens.hist_v[0][keys] = float("inf")
+    wl.place_history(spec, tens.hist_k, tens.k_cache)
+    wl.place_history(spec, tens.hist_v, tens.v_cache)
+    for rules in ({}, dict(softcap=20.0, slopes=_alibi(nh))):
+        _check(rb, spec, tens=tens, table=table, key_start=start, **rules)
+
+
+@pytest.mark.parametrize("ratio", [1, 2])
+def test_pages_before_rows_that_see_nothing_may_be_gone(rb, ratio):
+    """Tokens with a window of no keys do not make the pages of their empty window read: a
+    prompt (rows that see something start later), a decode of several tokens, and requests none
+    of whose tokens sees a key."""
+    old = lambda key: range(key // (16 * ratio))
+    # a chunk: positions 333 .. 422; the first ten see nothing, the others their own and 2 before
+    pos = np.arange(333, 423)
+    start = np.where(pos < 343, pos + 1, pos - 2)
+    _check_with_pages_gone(rb, 333, 90, start, old(341), 8, 2, ratio)
+    # decode of 8 tokens of one head: positions 505 .. 512, only the last sees a key, its own
+    start = np.append(np.arange(505, 512) + 1, 512)
+    _check_with_pages_gone(rb, 505, 8, start, old(512), 1, 1, ratio)
+    # nobody sees a key: no page is needed, the last one neither
+    for c, q, nh, nkv in ((500, 1, 8, 2), (500, 2, 4, 2), (300, 60, 8, 2), (31, 1, 2, 2)):
+        pos = np.arange(c, c + q)
+        pages = range(-(-(c + q) // (16 * ratio)))
+        _check_with_pages_gone(rb, c, q, pos + 1, pages, nh, nkv, ratio)
+        _check_with_pages_gone(rb, c, q, np.full(q, 1 << 30), pages, nh, nkv, ratio)
