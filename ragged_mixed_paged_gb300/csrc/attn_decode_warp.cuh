@@ -61,6 +61,10 @@ __device__ void combine_columns(const AttnArgs& a, int h, int first, int nsplit,
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
   float lsum = 0.f;
+  // A scored split's partial may hold infinities and NaN of V that its columns see: a weight that
+  // rounds to 0 would make the infinities NaN, so it stays at the least number of all, 2^-149 (a
+  // split whose column saw no key is all zeros).
+  const float least = is_scored(a.rules) ? 1.401298464e-45f : 0.f;
 #pragma unroll 1
   for (int sp0 = 0; sp0 < nsplit; sp0 += kBatch) {
     float2 ml[kBatch];
@@ -77,7 +81,8 @@ __device__ void combine_columns(const AttnArgs& a, int h, int first, int nsplit,
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       if (sp0 + k >= nsplit) break;
-      const float w = fast_exp2(ml[k].x - mx);
+      float w = fast_exp2(ml[k].x - mx);
+      w = w < least ? least : w;
       lsum += w * ml[k].y;
 #pragma unroll
       for (int v = 0; v < kVec; ++v) {

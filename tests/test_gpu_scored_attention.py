@@ -428,3 +428,17 @@ def test_pages_before_rows_that_see_nothing_may_be_gone(rb, ratio):
         pages = range(-(-(c + q) // (16 * ratio)))
         _check_with_pages_gone(rb, c, q, pos + 1, pages, nh, nkv, ratio)
         _check_with_pages_gone(rb, c, q, np.full(q, 1 << 30), pages, nh, nkv, ratio)
+
+
+
+def test_splits_of_a_decode_whose_first_tokens_see_nothing(rb):
+    """Several splits per request; a token that sees nothing beside tokens that see infinities."""
+    spec = wl.batch_from_lists([5000, 3000], [4, 2], num_q_heads=4, num_kv_heads=2, head_dim=128,
+                               seed=15)
+    tens = wl.make_tensors(spec, device="cuda")
+    tens.hist_v[0][4321, :, 3] = float("inf")
+    tens.hist_v[1][17, :, 4] = float("nan")
+    wl.place_history(spec, tens.hist_v, tens.v_cache)
+    start = [5001, 1000, 1 << 30, 4400, 3001, 0]
+    got, _, _, _ = _check(rb, spec, tens=tens, key_start=start, slopes=_alibi(4))
+    assert not got[0].any() and not got[2].any() and not got[4].any()
