@@ -169,10 +169,11 @@ rb_status attn_set_rules(AttnSetup* su, const rb_score_rules* rules, float softm
     if (!std::isfinite(a.cap_in) || !std::isfinite(a.cap_log2)) return RB_ERR_INVALID_ARG;
     // A coefficient that falls below fp32's range (a cap far above any score) is dropped, and
     // the polynomial kept to arguments where its term is below 1e-7.
-    double f = static_cast<double>(a.cap_log2) * a.cap_in, z = kTanhZ;
+    const TanhPoly& poly = a.cap_log2 <= kTanhWideCap ? kTanhWide : kTanhNarrow;
+    double f = static_cast<double>(a.cap_log2) * a.cap_in, z = poly.z;
     const double z_without[4] = {0.0, 1e-7, 1e-4, 1e-2};
     for (int k = 0; k < 4; ++k) {
-      const double c = kTanhPoly[k] * f;
+      const double c = poly.c[k] * f;
       const bool fits = std::fabs(c) >= 1e-37 && std::fabs(c) <= 3e38;
       a.cap_poly[k] = fits ? static_cast<float>(c) : 0.f;
       if (!fits) z = std::fmin(z, z_without[k]);

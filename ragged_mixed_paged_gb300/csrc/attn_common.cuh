@@ -218,14 +218,24 @@ static __device__ __noinline__ void add_not_finite(const AttnArgs& a, int r, int
   }
 }
 
-// Capped scores (log2 units): cap_log2 * tanh(u), u = cap_in * s.  For u^2 <= kTanhZ tanh(u) =
-// u P(u^2) with P(0) = 1 of degree 3, the least maximum relative error of that form (8.5e-6,
-// vanishing with u: 4e-4 log2 units for a cap of 50 at u = 0.7, a sixteenth of what rounding P
-// to bf16 costs): multiply-adds two at a time and no trip to the SFU, which the exponents keep
-// busy.  Larger |u|: tanh(u) = 1 - 2 / (1 + e^2u), two SFU operations (e^2u = inf or 0 gives
-// +-1).
-constexpr float kTanhPoly[4] = {1.0f, -0.3329871892929077f, 0.12897320091724396f, -0.03759901970624924f};
-constexpr float kTanhZ = 0.5f;
+// Capped scores (log2 units): cap_log2 * tanh(u), u = cap_in * s.  For u^2 <= z tanh(u) = u P(u^2)
+// with P(0) = 1 of degree 3, the least maximum relative error of that form on [0, z]:
+// multiply-adds two at a time and no trip to the SFU, which the exponents keep busy.  Larger |u|:
+// tanh(u) = 1 - 2 / (1 + e^2u), two SFU operations (e^2u = inf or 0 gives +-1), with an error of
+// 1.5e-7 from u = 0.3 on.
+// The error counts cap_log2 times, and 2^-11 log2 units move a probability by an eleventh of what
+// rounding it to bf16 does.  z = 1/2 (an error of 5.2e-6 in tanh) stays below that up to
+// cap_log2 = 93, a cap of 64; above, P is the one for z = 1/10 (5.5e-9), which leaves the
+// exponential form's error (2^-12 at a cap of 1000) and, from caps of thousands on, the fp32
+// rounding of scores of that size.
+struct TanhPoly {
+  float c[4], z;
+};
+constexpr TanhPoly kTanhWide = {{1.0f, -0.3329871892929077f, 0.12897320091724396f,
+                                 -0.03759901970624924f}, 0.5f};
+constexpr TanhPoly kTanhNarrow = {{1.0f, -0.33332962386243388f, 0.13310651554494919f,
+                                   -0.04998707773147634f}, 0.1f};
+constexpr float kTanhWideCap = 93.f;  // cap_log2
 
 // kCount raw products, in place.  Both forms are evaluated and one chosen per score: tiles and
 // pages that need their scores in place are few.

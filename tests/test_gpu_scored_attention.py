@@ -442,3 +442,55 @@ def test_splits_of_a_decode_whose_first_tokens_see_nothing(rb):
     start = [5001, 1000, 1 << 30, 4400, 3001, 0]
     got, _, _, _ = _check(rb, spec, tens=tens, key_start=start, slopes=_alibi(4))
     assert not got[0].any() and not got[2].any() and not got[4].any()
+
+
+@pytest.mark.parametrize("q", [1, 150])
+@pytest.mark.parametrize("softcap", [50.0, 66.0, 70.0, 100.0, 300.0, 1000.0, 4000.0, 16000.0])
+def test_soft_cap_keeps_its_precision(rb, softcap, q):
+    """Scores about 0.3 and 0.7 of the cap, the two sides of each worth +v and -v: an error of
+    the cap that differs from side to side moves the sum.
+
+    Tolerance: the raw scores are exact here (multiples of 2^-6 below 2^14, in every order of
+    summation).  With c = cap log2(e), a capped score in log2 units is off by 2^-11 at most from
+    its tanh as the polynomial has it; by 2 c r (E r 2^-22 + 2^-24 + 2^-23) with E = e^2u and
+    r = 1 / (1 + E) where the exponential form has it (ex2, the sum, the reciprocal), which is
+    below 2^-22 c for u >= 0.3; and by two roundings of its size, 2 x 2^-24 c.  Each probability
+    then moves by ln 2 of that, relatively, and o = sum p v / sum p by that times
+    sum p |v - o| <= w + |o|; P and the output are rounded to bf16 (2^-8 each) as everywhere."""
+    c = softcap * 1.4426950408889634
+    for u in (0.3162, 0.7071):
+        spec = wl.batch_from_lists([700 - q], [q], num_q_heads=4, num_kv_heads=2, head_dim=128,
+                                   seed=int(softcap))
+        tens = wl.make_tensors(spec, device="cuda")
+        g = torch.Generator().manual_seed(int(softcap))
+        L = 700
+        border = int(u * softcap)
+        fine = torch.randint(-96, 97, (L, 2), generator=g).float() / 64       # within 1.5
+        fine = torch.round((fine + u * softcap - border) * 64) / 64
+        keys = torch.zeros(L, 2, 128)
+        keys[:, :, 0] = border // 64            # (bf16 holds whole numbers up to 256)
+        keys[:, :, 1] = border % 64
+        keys[:, :, 2] = fine
+        values = torch.rand(L, 2, 128, generator=g) + 0.5
+        side = fine > u * softcap - border
+        values = torch.where(side[..., None], -values, values)
+        keys, values = keys.to(torch.bfloat16), values.to(torch.bfloat16)
+        tens.q.zero_()
+        tens.q[:, :, 0], tens.q[:, :, 1], tens.q[:, :, 2] = 64.0, 1.0, 1.0
+        tens.hist_k[0].copy_(keys[:700 - q])
+        tens.hist_v[0].copy_(values[:700 - q])
+        tens.k[:q], tens.v[:q] = keys[700 - q:].cuda(), values[700 - q:].cuda()
+        wl.place_history(spec, tens.hist_k, tens.k_cache)
+        wl.place_history(spec, tens.hist_v, tens.v_cache)
+        tens, meta = _setup(rb, spec, tens)
+        got = rb.paged_attention_scored(
+            dims_of(spec), 1, q, tens.q, tens.k_cache, tens.v_cache, i32(spec.block_table),
+            i32(meta["query_start_loc"][:2]), i32(meta["seq_lens"][:1]),
+            rb.ScoreRules(softcap=softcap), softmax_scale=1.0)
+        ks, vs = _full(spec, tens)
+        out, weight = oracle_scored(to64(tens.q), ks, vs, meta["query_start_loc"][:2],
+                                    meta["seq_lens"][:1], scale=1.0, softcap=softcap)
+        off = np.log(2.0) * (2.0 ** -11 + (2.0 ** -22 + 2.0 ** -23) * c)
+        tol = ((2.0 ** -8 + off) * (np.abs(out) + weight)) + 1e-30
+        worst = (np.abs(got.double().cpu().numpy() - out) / tol).max()
+        assert worst <= 1.0, (u, worst)
