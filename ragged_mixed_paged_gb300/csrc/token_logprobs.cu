@@ -183,7 +183,7 @@ struct Sums {
       w = 0.f;
     } else {
       const float d = fminf((to - ref) * kLog2e, -kFar), f = fast_exp2(-d);
-      w = (w - d * s) * f;
+      w = f == 0.f ? 0.f : (w - d * s) * f;  // (f = 0: d s may be past fp32's range)
       s *= f;
     }
     ref = to;

@@ -214,3 +214,22 @@ def test_zeros_of_either_sign_are_equal(rb, rows):
     x[::2, 39990] = -0.0
     for top in (3, 20):
         _check(rb, x.to(torch.bfloat16).cuda(), [104] * rows, top)
+
+
+def test_two_logits_far_above_a_large_sum(rb):
+    """A thread's sum of many terms near its reference, then two logits of 1e31: the sum
+    vanishes against them, and its weighted part with it."""
+    vocab = 24 << 20
+    logits = torch.full((1, vocab), 10.9, device="cuda")
+    for c in range(8):             # every thread's first batch, where its reference comes from
+        logits[0, c * (vocab // 8):c * (vocab // 8) + 4 * 4 * 256] = 0.0
+    at = [vocab // 2 - 5, vocab - 9]
+    logits[0, at] = 1e31
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tokens = torch.tensor(at[1:], dtype=torch.int32, device="cuda")
+    got = rb.token_logprobs(logits, tokens, 2, error_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    assert abs(float(got.logprobs) + np.log(2.0)) <= 4 * U
+    assert abs(float(got.entropy) - np.log(2.0)) <= 4 * U
+    assert int(got.ranks) == 1 and got.top_ids.tolist() == [at]
