@@ -40,7 +40,7 @@ struct DecCfg {
 // lanes.  Partials written by other SMs are read through L2 (ld.global.cg), kBatch splits' loads
 // in flight at a time: a merge of 20 splits is a chain of L2 round trips, 8 to 16 us of a small
 // decode call when each waited for its own.
-template <int HD, int kLanes>
+template <int HD, int kLanes, bool kScored>
 __device__ void combine_columns(const AttnArgs& a, int h, int first, int nsplit, int t0,
                                 int cols) {
   constexpr int kPer = HD / kLanes;         // values of one column per lane
@@ -61,10 +61,6 @@ __device__ void combine_columns(const AttnArgs& a, int h, int first, int nsplit,
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
   float lsum = 0.f;
-  // A scored split's partial may hold infinities and NaN of V that its columns see: a weight that
-  // rounds to 0 would make the infinities NaN, so it stays at the least number of all, 2^-149 (a
-  // split whose column saw no key is all zeros).
-  const float least = is_scored(a.rules) ? 1.401298464e-45f : 0.f;
 #pragma unroll 1
   for (int sp0 = 0; sp0 < nsplit; sp0 += kBatch) {
     float2 ml[kBatch];
@@ -82,7 +78,10 @@ __device__ void combine_columns(const AttnArgs& a, int h, int first, int nsplit,
     for (int k = 0; k < kBatch; ++k) {
       if (sp0 + k >= nsplit) break;
       float w = fast_exp2(ml[k].x - mx);
-      w = w < least ? least : w;
+      // A scored split's partial may hold infinities and NaN of V that its columns see: a weight of
+      // 0 would make the infinities NaN, so it is 2^-149 at least (a split whose column saw no key
+      // is all zeros).
+      if constexpr (kScored) w += 1.401298464e-45f;
       lsum += w * ml[k].y;
 #pragma unroll
       for (int v = 0; v < kVec; ++v) {
@@ -127,11 +126,11 @@ __device__ void combine_columns(const AttnArgs& a, int h, int first, int nsplit,
   }
 }
 
-template <int HD>
+template <int HD, bool kScored>
 __device__ void combine_splits(const AttnArgs& a, int h, int first, int nsplit, int t0,
                                int cols) {
-  if (cols <= 4) combine_columns<HD, 8>(a, h, first, nsplit, t0, cols);
-  else combine_columns<HD, 4>(a, h, first, nsplit, t0, cols);
+  if (cols <= 4) combine_columns<HD, 8, kScored>(a, h, first, nsplit, t0, cols);
+  else combine_columns<HD, 4, kScored>(a, h, first, nsplit, t0, cols);
 }
 
 // A warp adds the infinities and NaN in V of keys [k0, k1) to the results of the columns that see
@@ -501,7 +500,7 @@ __device__ void decode_warp(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p
       prev = __shfl_sync(0xffffffffu, prev, 0);
       if (prev == nsplit - 1) {
         __threadfence();
-        combine_splits<HD>(a, h, first, nsplit, t0, cols);
+        combine_splits<HD, kScored>(a, h, first, nsplit, t0, cols);
       }
     }
   }
