@@ -279,6 +279,8 @@ typedef struct rb_score_rules {
  * Pages before the first key that any query of the request sees are not read and their
  * page-table entries are not checked (a window's old pages may be gone), and what K and V hold
  * for keys that a query does not see, infinities and NaN too, does not reach its row.
+ * V of magnitudes up to 2^80 (1e24) gives finite rows: a weight is 2^20 at most before the sum
+ * divides it, and the sums over keys are fp32.
  */
 rb_status rb_paged_attention_scored(const rb_dims* dims, int32_t num_reqs, int32_t num_tokens,
                                     int32_t num_tokens_padded, const void* d_q,

@@ -12,7 +12,7 @@
 // two, which is exact in bf16.
 //
 // Measured on four chunks of 1-2 k tokens over up to 16 k cached ones (32 / 8 heads of 128; the
-// ordinary launch 646 us, 0.74 of the bf16 rate): no rule 710 us, soft cap 900, distance bias 859.
+// ordinary launch 646 us, 0.74 of the bf16 rate): no rule 710 us, soft cap 925, distance bias 854.
 // With all 128 scores kept in registers and the maximum taken once per tile: 695, 1102, 828; in
 // rounds of 16 columns 961, 1037, 1064; of 32 763, 949, 892; with the next columns' loads ahead of
 // the current ones' work (twice the code) 850, 992, 985 for 32.
@@ -26,11 +26,15 @@ namespace {
 
 // How far (log2 units) a score may lie above its row's reference.
 constexpr float kGrowth = 20.f;
-// Capped scores are at most cap_log2 (a bias that falls with distance only lowers them), so with
-// the fixed reference cap_log2 - kCapHeadroom every exponent is below 2^kCapHeadroom.  A row's
-// largest score is at least -cap_log2 (biased: its own key's, if it sees that one), so up to
-// kMaxBoundedCap its terms stay above 2^-100.  Such a row needs no maximum and never moves.
-constexpr float kMaxBoundedCap = 74.f, kCapHeadroom = 48.f;
+// Capped scores lie within +-cap_log2 (a bias that falls with distance only lowers them), so up to
+// kMaxBoundedCap a row needs no maximum.  Its reference starts where a score of -cap_log2, the least
+// that a row's largest can be (biased: its own key's, if it sees that one), weighs 2^-31 or more and
+// one of +cap_log2 at most 2^118, and rises by a power of two when a tile's 128 columns sum to more
+// than 2^kGrowth.  So the weights that O takes neither vanish nor, tile by tile, sum to more than
+// that, whichever end of the cap a row's scores lie at.  (A reference that never moved had V up to
+// 2^80 and down to 2^-26 at the ends of a cap of 50; the check costs 3 %, 900 -> 925 us below.)
+constexpr float kMaxBoundedCap = 74.f, kCapLow = 30.f;
+constexpr float kLargeSum = 1048576.f;  // 2^kGrowth
 constexpr int kCols = 64;  // columns taken at a time
 
 // Softmax and epilogue of tile x (0 = A, 1 = B); thread t = row t of the tile = TMEM lane t.
@@ -108,12 +112,15 @@ __device__ void softmax_scored(const AttnArgs& a, TcShared<true>& sh, uint32_t t
     // The side that reads the unit's K/V tiles last (B, or A when B is empty) hands the Q, K and
     // V slots back to the producers as its S tiles land.
     const bool releases = x == (un.n[1] > 0 ? 1 : 0);
-    // Running reference (log2 units, a whole number unless fixed) and sum.  A row that has seen
-    // no key is at -inf; one without a query stays at +inf, where no score moves it.  (Masking
-    // such rows' keys made every tile of a group like 6 or 7 a masked one: prompts of 300 to 1500
-    // tokens with 12 / 2 heads of 64 and a bias 97 us, so 83.)
+    // Running reference (log2 units, a whole number) and sum.  A row that has seen no key is at
+    // -inf (or where it starts); one without a query stays at +inf, where no score moves it.
+    // (Masking such rows' keys made every tile of a group like 6 or 7 a masked one: prompts of 300
+    // to 1500 tokens with 12 / 2 heads of 64 and a bias 97 us, so 83.)
     const float cap_s = valid ? a.cap_s : INFINITY;
-    float m_ref = !valid ? INFINITY : bounded ? a.cap_log2 - kCapHeadroom : -INFINITY, l = 0.f;
+    float m_ref = !valid    ? INFINITY
+                  : bounded ? ceilf(fminf(a.cap_log2, kCapLow - a.cap_log2))
+                            : -INFINITY;
+    float l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const uint32_t tj = tc_x + j;
@@ -165,13 +172,8 @@ __device__ void softmax_scored(const AttnArgs& a, TcShared<true>& sh, uint32_t t
       const unsigned seen0 = static_cast<unsigned>(kv_base - lo), n_seen = hi - lo;
       float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 
-      // Raises the reference above `top`, the largest of a row's scores in round c, for the rows
-      // of the warp that need it.
-      auto move_reference = [&](float top, int c) {
-        const bool need = top > m_ref + kGrowth;
-        const float m_new = need ? ceilf(top) : m_ref;
-        // (-inf before the first key: alpha 0; a row that does not move: 1)
-        const float alpha = need ? fast_exp2(m_ref - m_new) : 1.f;
+      // Multiplies what the warp's rows took before round c by alpha (1: a row that stays).
+      auto rescale = [&](float alpha, int c) {
         tc::wait_st();
 #pragma unroll 1
         for (int p = 0; p < c * (kCols / 32); ++p) {  // P of the rounds before
@@ -199,6 +201,14 @@ __device__ void softmax_scored(const AttnArgs& a, TcShared<true>& sh, uint32_t t
         l *= alpha;
         rs[0] = __fmul2_rn(rs[0], make_float2(alpha, alpha));
         rs[1] = __fmul2_rn(rs[1], make_float2(alpha, alpha));
+      };
+      // Raises the reference above `top`, the largest of a row's scores in round c, for the rows
+      // of the warp that need it.
+      auto move_reference = [&](float top, int c) {
+        const bool need = top > m_ref + kGrowth;
+        const float m_new = need ? ceilf(top) : m_ref;
+        // (-inf before the first key: alpha 0)
+        rescale(need ? fast_exp2(m_ref - m_new) : 1.f, c);
         m_ref = m_new;
       };
 #pragma unroll 1
@@ -280,7 +290,8 @@ __device__ void softmax_scored(const AttnArgs& a, TcShared<true>& sh, uint32_t t
 #pragma unroll
             for (int i = 2; i < kCols; i += 2) top = fmax3(top, s[i], s[i + 1]);
             if constexpr (kRules == kMasked) top *= a.scale_log2;
-            if (__any_sync(0xffffffffu, top > m_ref + kGrowth)) move_reference(top, c);
+            if (__builtin_expect(__any_sync(0xffffffffu, top > m_ref + kGrowth), 0))
+              move_reference(top, c);
           }
           const float mu = m_ref == -INFINITY ? 0.f : m_ref;
           const float2 nmu2 = make_float2(-mu, -mu);
@@ -302,11 +313,23 @@ __device__ void softmax_scored(const AttnArgs& a, TcShared<true>& sh, uint32_t t
         tc::st32(col_s + c * (kCols / 2), pk);
       }
       tc::wait_st();
+      float2 r = __fadd2_rn(rs[0], rs[1]);
+      if (kCap && bounded) {
+        const float sum = r.x + r.y;
+        const bool need = sum > kLargeSum;
+        if (__builtin_expect(__any_sync(0xffffffffu, need), 0)) {
+          // by the sum's power of two, at most 2^125
+          const int up = need ? (__float_as_int(sum) >> 23) - 127 : 0;
+          const float alpha = __int_as_float((127 - up) << 23);
+          rescale(alpha, C::kN / kCols);
+          r = __fmul2_rn(r, make_float2(alpha, alpha));
+          m_ref += static_cast<float>(up);
+        }
+      }
       // P_j overwrites the S columns P_{j-1} V_{j-1} read: that product is done, since S_j (the
       // MMA after it) has landed
       tc::fence_before_sync();
       arrive_warp(&sh.p_full[x]);
-      const float2 r = __fadd2_rn(rs[0], rs[1]);
       l += r.x + r.y;
     }
     if (!ok) break;

@@ -494,3 +494,24 @@ def test_soft_cap_keeps_its_precision(rb, softcap, q):
         tol = ((2.0 ** -8 + off) * (np.abs(out) + weight)) + 1e-30
         worst = (np.abs(got.double().cpu().numpy() - out) / tol).max()
         assert worst <= 1.0, (u, worst)
+
+
+@pytest.mark.parametrize("softcap", [3.0, 12.0, 20.0, 50.0, 51.0])
+def test_capped_scores_at_either_end_with_values_of_any_size(rb, softcap):
+    """Rows whose scores are all at +cap, all at -cap, and that go from one to the other either
+    way, with V about 2^80 and 2^-60."""
+    spec = wl.batch_from_lists([600, 0, 700, 900], [300, 400, 1, 150], num_q_heads=8,
+                               num_kv_heads=2, head_dim=128, seed=16)
+    everywhere = 40.0
+    for hot in ({(0, 2000): everywhere}, {(0, 2000): -everywhere},
+                {(0, 300): everywhere, (300, 2000): -everywhere},
+                {(0, 300): -everywhere, (300, 2000): everywhere}):
+        for size in (2.0 ** 80, 2.0 ** -60):
+            tens = jump_tensors(spec, hot)
+            for v in [tens.v] + tens.hist_v:
+                v.mul_(size)
+            wl.place_history(spec, tens.hist_v, tens.v_cache)
+            _check(rb, spec, tens=tens, softcap=softcap)
+            _check(rb, spec, tens=tens, softcap=softcap, slopes=_alibi(8))
+            _check(rb, spec, tens=tens, softcap=softcap, slopes=_alibi(8),
+                   prefix_lens=[700, 256, 701, 1050])
