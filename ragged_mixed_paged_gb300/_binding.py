@@ -362,6 +362,16 @@ def paged_attention_scored(dims: Dims, num_reqs: int, num_tokens: int, q, k_cach
                        ("prefix_lens", rules.prefix_lens, num_reqs)):
         if t is not None and t.numel() < n:
             raise ValueError(f"{name} must have {n} entries")
+    token = dims.num_q_heads * dims.head_dim
+    if q.dim() < 1 or q.numel() != q.shape[0] * token:
+        raise ValueError(f"q must be [tokens, {dims.num_q_heads}, {dims.head_dim}]")
+    cache = dims.num_blocks * dims.block_size * dims.num_kv_heads * dims.head_dim
+    for name, t, n in (("k_cache", k_cache, cache), ("v_cache", v_cache, cache),
+                       ("block_table", block_table, num_reqs * dims.max_blocks_per_req),
+                       ("query_start_loc", query_start_loc, num_reqs + 1),
+                       ("seq_lens", seq_lens, num_reqs), ("out", out, q.numel())):
+        if t is not None and t.numel() < n:
+            raise ValueError(f"{name} holds {t.numel()} values, the call needs {n}")
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("block_table", block_table),
                     ("query_start_loc", query_start_loc), ("seq_lens", seq_lens), ("out", out),
                     ("workspace", workspace), ("error_word", error_word),

@@ -139,3 +139,24 @@ def test_python_checks_come_first(lib):  # noqa: F811
     with pytest.raises(ValueError, match="prefix_lens must have 2 entries"):
         rb.paged_attention_scored(dims, 2, 4, q, kv, kv, kv, kv, kv,
                                   rb.ScoreRules(prefix_lens=torch.zeros(1, dtype=torch.int32)))
+
+
+@pytest.mark.parametrize("name,short", [
+    ("q", (4, 2, 32)), ("q", (4, 3, 64)), ("q", (4 * 2 * 64 + 1,)), ("k_cache", (159, 2, 64)),
+    ("v_cache", (160, 1, 64)), ("block_table", (2, 3)), ("query_start_loc", (2,)),
+    ("seq_lens", (1,)), ("out", (3, 2, 64))])
+def test_scored_attention_refuses_short_tensors(lib, name, short):  # noqa: F811
+    """A tensor that the kernel would read or write past its end is named and refused."""
+    import torch
+
+    import ragged_mixed_paged_gb300 as rb
+
+    dims = rb.Dims(16, 2, 2, 64, 4, 64, 4, 10)
+    bf, i32 = torch.bfloat16, torch.int32
+    args = dict(q=torch.zeros(4, 2, 64, dtype=bf), k_cache=torch.zeros(160, 2, 64, dtype=bf),
+                v_cache=torch.zeros(160, 2, 64, dtype=bf), block_table=torch.zeros(2, 4, dtype=i32),
+                query_start_loc=torch.zeros(3, dtype=i32), seq_lens=torch.zeros(2, dtype=i32),
+                out=torch.zeros(4, 2, 64, dtype=bf))
+    args[name] = torch.zeros(short, dtype=args[name].dtype)
+    with pytest.raises(ValueError, match="^%s " % name):
+        rb.paged_attention_scored(dims, 2, 4, rules=rb.ScoreRules(), **args)
