@@ -156,7 +156,8 @@ __device__ __forceinline__ TcUnit decode_unit(const AttnArgs& a, int u) {
   }
   // the planner lists the (request, pair) entries longest first; the kv heads of one entry
   // are consecutive units
-  const int entry = __ldg(a.pre_list + u / a.nkv);
+  // (a plain load: a scored launch is resident while the planner still writes the list)
+  const int entry = a.pre_list[u / a.nkv];
   const int r = entry >> 16, pair = entry & 0xffff;
   un.r = r;
   un.h = u % a.nkv;

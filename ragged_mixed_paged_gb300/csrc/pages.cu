@@ -15,7 +15,8 @@
 // Copies move whole 16-byte chunks and are bound by HBM (2 x page bytes); everything else is a
 // few dependent passes over the counts and is bound by latency, so each call is few launches: one
 // for copy and free, two (a plan by one CTA or one cluster, then the grid that copies) for fork
-// and compact.
+// and compact.  A launch may be resident while the one before it still writes what it reads, so
+// nothing here is read through the non-coherent path (__ldg).
 #include <cooperative_groups.h>
 
 #include "rb_internal.cuh"
@@ -155,8 +156,8 @@ __global__ void __launch_bounds__(kCopyThreads)
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
           const int i = base + k * kCopyThreads;
-          s[k] = i < n ? __ldg(src + i) : -1;
-          d[k] = i < n ? __ldg(dst + i) : -1;
+          s[k] = i < n ? src[i] : -1;
+          d[k] = i < n ? dst[i] : -1;
         }
         fn(s, d);
       }
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     return;
   }
   auto page = [&](const int32_t* list, long long i) {
-    const int id = __ldg(list + i);
+    const int id = list[i];
     return valid_page(a, id) ? id : -1;
   };
   copy_pages(
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kCheckThreads) __cluster_dims__(kClusterCtas, 
   int freed = 0, bits = 0;
   constexpr int kWarps = kCheckThreads / 32;
   for (int i = (threadIdx.x >> 5) * kClusterCtas + blockIdx.x; i < n; i += kWarps * kClusterCtas) {
-    const int r = __ldg(list + i);
+    const int r = list[i];
     if (r < 0 || r >= a.rows) {
       bits |= RB_EBIT_ROW;
       continue;
