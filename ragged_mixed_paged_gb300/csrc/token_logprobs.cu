@@ -43,6 +43,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // Differences to the reference are taken as at least kFar, so that masked (-inf) logits add
 // 2^t t = 0 rather than 0 * inf.
 constexpr float kFar = -1e30f;
+constexpr float kGone = 1e4f;  // log2 units over which a sum that moves vanishes
 constexpr float kLowest = -3.402823466e38f;  // the reference while a thread saw nothing finite
 // The reference moves when a logit exceeds it by kGrowth: s <= V e^11 stays far inside fp32.
 constexpr float kGrowth = 11.f;
@@ -182,8 +183,9 @@ struct Sums {
     if (s == 0.f) {
       w = 0.f;
     } else {
-      const float d = fminf((to - ref) * kLog2e, -kFar), f = fast_exp2(-d);
-      w = f == 0.f ? 0.f : (w - d * s) * f;  // (f = 0: d s may be past fp32's range)
+      // (beyond kGone f is 0; d itself would take d s past fp32's range)
+      const float d = fminf((to - ref) * kLog2e, kGone), f = fast_exp2(-d);
+      w = (w - d * s) * f;
       s *= f;
     }
     ref = to;
