@@ -63,11 +63,11 @@ FLUSH_BYTES = 512 << 20
 # its planner's code, comments left out): a figure is reported only while the code is the code
 # it was measured on.
 KNOWN_TRAFFIC = {
-    (2, "c8f9eb99a5b6211b"): 78987008 + 3487232,
-    (3, "c8f9eb99a5b6211b"): 4545612800 + 26181120,
+    (2, "243f94e4ec9aae15"): 78989568 + 3869184,
+    (3, "243f94e4ec9aae15"): 4545406720 + 26100736,
     # the stream: mean over the launches of stream steps 5..99 (the default timed steps)
-    (4, "c8f9eb99a5b6211b"): 9554043047 + 80905984,
-    (5, "c8f9eb99a5b6211b"): 7125457152 + 114908416,
+    (4, "243f94e4ec9aae15"): 9543039138 + 80848678,
+    (5, "243f94e4ec9aae15"): 6940740608 + 114152448,
 }
 
 WORKLOAD_NAMES = {1: "pages' worked example A/B/C", 2: "pages' padding example",
