@@ -402,7 +402,7 @@ def test_a_pool_made_on_a_busy_device(rb):
     scratch = torch.zeros(1 << 26, device="cuda")
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
-    for _ in range(200):               # some 20 ms of work on the current stream
+    for _ in range(1000):              # some 80 ms of work on the current stream
         scratch.add_(1.0)
     pool = rb.PagePool(s.dims, s.k, s.v, s.bt, s.nb, stream=side)
     pool.fork(*args, stream=side)
