@@ -25,6 +25,9 @@
  *                      page table (shared full pages, the partial page copied), freeing rows and
  *                      compacting the live pages
  *   rb_token_logprobs  log probability and rank of given tokens, entropy, top alternatives
+ *   rb_kv_append       queries and keys rotated by their positions, keys and values appended
+ *   rb_kv4_*           a paged cache held in 4 bits: appending to it (rotated), reading rows back
+ *   rb_add_rms_norm    the residual's addition and the root-mean-square norm, output in 8 bits
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -96,6 +99,8 @@ typedef enum rb_status {
 #define RB_EBIT_NO_PAGE 0x4000      /* rb_pages_fork: too few free pages */
 #define RB_EBIT_TOKEN_ID 0x8000     /* rb_token_logprobs: token id below -1 or >= vocab_size */
 #define RB_EBIT_LOGITS 0x10000      /* rb_token_logprobs: a row holds NaN or +inf */
+#define RB_EBIT_POSITION 0x20000    /* rb_kv_append, rb_kv4_append: position outside the table */
+#define RB_EBIT_NOT_FINITE 0x40000  /* rb_kv4_append: an appended key or value is NaN or infinite */
 
 /* Static sizes of the persistent batch and of one layer's paged KV pool. */
 typedef struct rb_dims {
@@ -701,8 +706,8 @@ rb_status rb_pages_compact(const rb_dims* dims, const rb_page_tables* tables,
                            void* d_v_cache, void* d_workspace, size_t workspace_bytes,
                            int32_t* d_error_word, void* stream);
 
-/* Element types of rb_token_logprobs's logits. */
-typedef enum rb_dtype { RB_BF16 = 0, RB_FP16 = 1, RB_FP32 = 2 } rb_dtype;
+/* Element types (rb_token_logprobs's logits, rb_add_rms_norm's rows; RB_E4M3: its 8-bit output). */
+typedef enum rb_dtype { RB_BF16 = 0, RB_FP16 = 1, RB_FP32 = 2, RB_E4M3 = 3 } rb_dtype;
 
 /*
  * rb_token_logprobs — for each of num_rows rows of logits: the log probability and the rank of
@@ -731,6 +736,115 @@ rb_status rb_token_logprobs(int32_t num_rows, int32_t vocab_size, int64_t row_st
                             const int32_t* d_token_ids, int32_t top_k, float* d_logprobs,
                             int32_t* d_ranks, float* d_entropy, int32_t* d_top_ids,
                             float* d_top_logprobs, int32_t* d_error_word, void* stream);
+
+/*
+ * Position rotation of rb_kv_append and rb_kv4_append: at position p, pair i of a head's first
+ * rotary_dim values, (x, y) = values (i, i + rotary_dim / 2), or (2i, 2i + 1) if interleaved, becomes
+ *   (x cos_i(p) - y sin_i(p),  y cos_i(p) + x sin_i(p))
+ * with cosine and sine from row p of d_cos_sin [max_position, rotary_dim] fp32 (rotary_dim / 2
+ * cosines, then as many sines; 16-byte aligned).  fp32, each product and sum rounded by itself, the
+ * result rounded to bf16.  The other values of a head stay as they are.  rotary_dim: a multiple of
+ * 16 up to head_dim.
+ */
+typedef struct rb_rotation {
+  int32_t rotary_dim;
+  int32_t interleaved;   /* 0 or 1 */
+  int32_t max_position;  /* rows of the table */
+  int32_t reserved;      /* 0 */
+  const float* d_cos_sin;
+} rb_rotation;
+
+/*
+ * rb_kv_append — rb_kv_write with the rotation on the way: q and k of each token are rotated by its
+ * position, q written to d_q_out and the step's K and V rows to their slots.
+ *
+ *   rotation         NULL: none (d_positions is ignored)
+ *   d_positions      [num_tokens_padded] int32, for example rb_prepare_inputs's
+ *   d_q              [num_tokens_padded, nh, hd] bf16, tokens q_stride values apart, heads adjacent
+ *                    (a slice of a fused projection's output); or NULL, with d_q_out, for none
+ *   d_k, d_v         [num_tokens_padded, nkv, hd] bf16, tokens k_stride / v_stride values apart
+ *   d_slot_mapping   [num_tokens_padded] int32; slot < 0: no K/V is written (q is rotated)
+ *   d_q_out          [num_tokens_padded, nh, hd] bf16, tokens q_out_stride values apart; d_q itself
+ *                    with q_stride rotates in place, no other overlap is allowed
+ *   d_k_cache, d_v_cache  [num_blocks * block_size, nkv, hd] bf16 (updated in place)
+ * head_dim a multiple of 16 up to 2048, strides multiples of 8 values and at least a token's
+ * row, base pointers 16-byte aligned.  Two real tokens must not share a slot.
+ * Errors: host -> RB_ERR_INVALID_ARG, RB_ERR_UNSUPPORTED; device -> SLOT (slot >= num_blocks *
+ * block_size: no K/V is written), POSITION (outside [0, max_position): nothing of the token is).
+ */
+rb_status rb_kv_append(const rb_dims* dims, int32_t num_tokens_padded,
+                       const rb_rotation* rotation, const int32_t* d_positions, const void* d_q,
+                       int64_t q_stride, const void* d_k, int64_t k_stride, const void* d_v,
+                       int64_t v_stride, const int32_t* d_slot_mapping, void* d_q_out,
+                       int64_t q_out_stride, void* d_k_cache, void* d_v_cache,
+                       int32_t* d_error_word, void* stream);
+
+/*
+ * A paged cache held in 4 bits (4.5 with its scales): K and V separate tensors [num_blocks, nkv,
+ * 9 * hd] of bytes, block_size 16, head_dim 64 or 128, 16-byte aligned.  The 9 hd bytes of one page
+ * and kv head are
+ *   codes   [16 tokens][hd / 2], value 2i of a token in the low half of byte i, 2i + 1 in the high
+ *   scales  K: [16 tokens][hd / 16]   V: [hd / 16][16 tokens], one for 16 neighbouring values
+ * A code c is a sign (bit 3) and a magnitude 0, 0.5, 1, 1.5, 2, 3, 4, 6 (bits 0-2); a scale byte s
+ * an unsigned number of four bits of exponent (bias 7) and three of mantissa (bit 7 ignored, 0x7f
+ * is 480).  The value is layer_scale * s * c, layer_scale being the call's k_scale or v_scale (one
+ * fp32 number of a layer, which puts its values into the scales' range; 1 where they are of the
+ * order of 0.01 to 1000).
+ * Whole pages of such a cache are moved by rb_pages_copy and rb_pages_compact with dims whose
+ * block_size is 1 and whose head_dim is 9 * hd / 2; after rb_pages_fork of another layer (its table,
+ * with block_size 16) a partial page follows by rb_pages_copy, as it does for further layers.
+ */
+
+/*
+ * rb_kv4_append — rb_kv_append into a 4-bit cache.  The rotated keys (rounded to bf16) and the
+ * values are held in blocks of 16: y = x / layer_scale, s = the scale nearest to max |y| / 6 (at most
+ * 448), c = the code nearest to y / s (0 where s is 0), ties to the even one, quotients in fp32.
+ * An infinity is held as the largest value, NaN as 0.
+ * Errors: as rb_kv_append, RB_ERR_UNSUPPORTED for another block_size or head_dim and for nkv * hd
+ * above 24576, RB_ERR_INVALID_ARG for a layer scale that is not positive and finite; device -> also
+ * NOT_FINITE.
+ */
+rb_status rb_kv4_append(const rb_dims* dims, int32_t num_tokens_padded,
+                        const rb_rotation* rotation, const int32_t* d_positions, const void* d_q,
+                        int64_t q_stride, const void* d_k, int64_t k_stride, const void* d_v,
+                        int64_t v_stride, const int32_t* d_slot_mapping, float k_scale,
+                        float v_scale, void* d_q_out, int64_t q_out_stride, void* d_k_cache,
+                        void* d_v_cache, int32_t* d_error_word, void* stream);
+
+/*
+ * rb_kv4_read — K and V of slots d_slots[i], i < num_rows, of a 4-bit cache, as bf16 rows d_k_out and
+ * d_v_out [num_rows, nkv, hd] (16-byte aligned).  A negative slot gives zeros.
+ * Errors: host -> as rb_kv4_append; device -> SLOT (slot >= num_blocks * 16: zeros).
+ */
+rb_status rb_kv4_read(const rb_dims* dims, int32_t num_rows, const int32_t* d_slots,
+                      const void* d_k_cache, const void* d_v_cache, float k_scale, float v_scale,
+                      void* d_k_out, void* d_v_out, int32_t* d_error_word, void* stream);
+
+/*
+ * rb_add_rms_norm — for each of num_rows rows of hidden states
+ *   r = x + residual (rounded to the rows' type; x without a residual)
+ *   y = r / sqrt(mean(r^2) + eps) * weight            (fp32)
+ * written as y in the rows' type (out_dtype = dtype, d_scales NULL) or in 8 bits (out_dtype
+ * RB_E4M3): s = max |y| / 448 over the row (group_size 0) or over each group_size neighbouring
+ * values, out = the e4m3 number nearest to y / s (0 where s is 0).
+ *
+ *   d_x, d_residual, d_residual_out  [num_rows, hidden_size] of dtype (RB_BF16, RB_FP16, RB_FP32),
+ *                rows *_stride values apart (at least hidden_size); residual and residual_out
+ *                are given together or not at all; residual_out (r) may be x or residual itself
+ *   d_weight     [hidden_size] of dtype
+ *   d_out        [num_rows, hidden_size], rows adjacent; may be x itself (of adjacent rows, in
+ *                dtype)
+ *   d_scales     [num_rows, hidden_size / group_size] fp32 ([num_rows, 1] for group_size 0)
+ * Any alignment of whole elements; rows of 16-byte alignment are read and written 16 bytes at a
+ * time.  hidden_size up to 32768; group_size 0, 16, 32, 64, 128 or 256, a divisor of hidden_size.
+ * A NaN makes its row NaN, an infinity becomes NaN and its row's other values 0.
+ * Errors: host -> RB_ERR_INVALID_ARG, RB_ERR_UNSUPPORTED.
+ */
+rb_status rb_add_rms_norm(int32_t num_rows, int32_t hidden_size, int32_t dtype, const void* d_x,
+                          int64_t x_stride, const void* d_residual, int64_t residual_stride,
+                          void* d_residual_out, int64_t residual_out_stride, const void* d_weight,
+                          float eps, int32_t out_dtype, int32_t group_size, void* d_out,
+                          float* d_scales, void* stream);
 
 #ifdef __cplusplus
 }

@@ -12,6 +12,11 @@
     PersistentBatch  device-resident rows of the resident requests; ``apply`` merges one
                      step's scheduler output (remove, append, install, condense) on the GPU
     PagePool         reference counts of the cache's pages: copy, fork, free, compact
+    kv_append        kv_write with the position rotation (Rotation) of queries and keys on the way
+    kv4_append       the same into a paged cache held in 4 bits (kv4_cache); kv4_read reads rows
+                     of it back
+    add_rms_norm     the residual's addition and the root-mean-square norm; add_rms_norm_fp8 with
+                     an output in 8 bits and scales
     token_logprobs   log probability and rank of given tokens, entropy, top alternatives
     pad_for_graph    smallest captured graph size >= the token count
 
@@ -24,8 +29,12 @@ from ._binding import (Dims, RbError, EBIT_ATTN_META, EBIT_BLOCK_ID, EBIT_NUM_CO
                        workspace_size, cascade_prefix_len, cascade_workspace_size,
                        paged_attention_cascade, ScoreRules, paged_attention_scored)
 from ._binding import (EBIT_BATCH_ID, EBIT_BATCH_SIZE, EBIT_LOGITS, EBIT_NO_PAGE,
-                       EBIT_PAGE_PAIR, EBIT_PAGE_REF, EBIT_ROW, EBIT_TOKEN_ID)
+                       EBIT_NOT_FINITE, EBIT_PAGE_PAIR, EBIT_PAGE_REF, EBIT_POSITION, EBIT_ROW,
+                       EBIT_TOKEN_ID)
+from .kv4 import (Rotation, kv4_append, kv4_cache, kv4_page_dims, kv4_pages, kv4_read,
+                  kv_append, rotary_table)
 from .logprobs import MAX_TOP_LOGPROBS, TokenLogprobs, token_logprobs
+from .norm import add_rms_norm, add_rms_norm_fp8
 from .pages import PagePool, pages_workspace_size
 from .persistent_batch import PersistentBatch, batch_workspace_size
 from .step import StepBuffers, run_step, run_step_fused, run_step_host, run_step_host_async
@@ -35,4 +44,6 @@ __all__ = ["Dims", "RbError", "gather_rows", "kv_write", "launch_count", "lib", 
            "run_step", "run_step_fused", "run_step_host", "run_step_host_async", "LIB_PATH", "PersistentBatch", "batch_workspace_size",
            "cascade_prefix_len", "cascade_workspace_size", "paged_attention_cascade", "ScoreRules",
            "paged_attention_scored", "PagePool",
-           "pages_workspace_size", "TokenLogprobs", "token_logprobs", "MAX_TOP_LOGPROBS"]
+           "pages_workspace_size", "TokenLogprobs", "token_logprobs", "MAX_TOP_LOGPROBS", "Rotation",
+           "rotary_table", "kv_append", "kv4_cache", "kv4_append", "kv4_read", "kv4_page_dims",
+           "kv4_pages", "add_rms_norm", "add_rms_norm_fp8"]

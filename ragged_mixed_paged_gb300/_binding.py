@@ -8,6 +8,7 @@ package raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -38,6 +39,8 @@ EBIT_PAGE_REF = 0x2000
 EBIT_NO_PAGE = 0x4000
 EBIT_TOKEN_ID = 0x8000
 EBIT_LOGITS = 0x10000
+EBIT_POSITION = 0x20000
+EBIT_NOT_FINITE = 0x40000
 
 
 class RbError(RuntimeError):
@@ -81,6 +84,11 @@ class rb_page_tables(ctypes.Structure):
         (n, ctypes.c_void_p) for n in ("d_block_table", "d_num_blocks", "d_ref_count")]
 
 
+class rb_rotation(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rotary_dim", "interleaved", "max_position",
+                                              "reserved")] + [("d_cos_sin", ctypes.c_void_p)]
+
+
 class rb_host_copy(ctypes.Structure):
     _fields_ = [("dst", ctypes.c_void_p), ("src", ctypes.c_void_p), ("bytes", ctypes.c_size_t)]
 
@@ -110,6 +118,8 @@ def _load():
     I32 = ctypes.c_int32
     PD = ctypes.POINTER(rb_dims)
     PT = ctypes.POINTER(rb_page_tables)
+    PR = ctypes.POINTER(rb_rotation)
+    I64, F32 = ctypes.c_int64, ctypes.c_float
     sig = {
         "rb_status_string": (ctypes.c_char_p, [I32]),
         "rb_kernel_launch_count": (ctypes.c_uint64, []),
@@ -148,6 +158,12 @@ def _load():
         "rb_pages_fork": (I32, [PD, PT, I32, P, P, P, P, P, P, ctypes.c_size_t, P, P]),
         "rb_pages_free": (I32, [PD, PT, I32, P, P, P, P]),
         "rb_pages_compact": (I32, [PD, PT, P, P, P, P, P, ctypes.c_size_t, P, P]),
+        "rb_kv_append": (I32, [PD, I32, PR, P, P, I64, P, I64, P, I64, P, P, I64, P, P, P, P]),
+        "rb_kv4_append": (I32, [PD, I32, PR, P, P, I64, P, I64, P, I64, P, F32, F32, P, I64, P, P,
+                                P, P]),
+        "rb_kv4_read": (I32, [PD, I32, P, P, P, F32, F32, P, P, P, P]),
+        "rb_add_rms_norm": (I32, [I32, I32, I32, P, I64, P, I64, P, I64, P, F32, I32, I32, P, P,
+                                  P]),
         "rb_token_logprobs": (I32, [I32, I32, ctypes.c_int64, I32, P, P, I32, P, P, P, P, P, P,
                                     P]),
     }
@@ -184,6 +200,12 @@ class Dims:
         return cls(d.block_size, d.num_q_heads, d.num_kv_heads, d.head_dim, d.max_num_reqs,
                    d.max_model_len, d.max_blocks_per_req, d.num_blocks, d.null_block,
                    getattr(d, "kernel_blocks_per_manager_block", 1))
+
+
+@functools.lru_cache(maxsize=64)
+def _dims_ref(dims: Dims):
+    """Pointer to the C form of ``dims``, made once for equal ones."""
+    return ctypes.byref(dims.c())
 
 
 def _check(fn: str, status: int) -> None:

@@ -1,0 +1,203 @@
+"""This step's queries, keys and values on their way into the paged cache: rotated by their
+positions (``rb_kv_append``), and a cache held in 4 bits (``rb_kv4_append``, ``rb_kv4_read``,
+``rb_paged_attention_kv4``).
+
+A cache in 4 bits is a pair of uint8 tensors [num_blocks, nkv, 9 * head_dim] (``kv4_cache``): 16 tokens
+a page, a sign, two bits of exponent and one of mantissa a value, and a scale for every 16 values.
+``k_scale`` and ``v_scale`` are the layer's own factors of all of them.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Any, Optional
+
+from . import _binding as rb
+
+
+class Rotation:
+    """How positions rotate heads: ``table`` [max_position, rotary_dim] fp32 holds the cosines and
+    then the sines of each position's rotary_dim / 2 angles (``rotary_table``); pair i is values
+    (i, i + rotary_dim / 2) of a head, or (2i, 2i + 1) if ``interleaved``.  The table stays as it is
+    (its values may change, its memory may not) while the rotation is in use."""
+
+    def __init__(self, table, interleaved: bool = False):
+        import torch
+
+        if table.dim() != 2:
+            raise ValueError("table must be [max_position, rotary_dim]")
+        pointer = rb._ptr(table, torch.float32, "table")
+        self.table, self.interleaved = table, bool(interleaved)
+        self._c = rb.rb_rotation(table.shape[1], int(self.interleaved), table.shape[0], 0, pointer)
+        self._ref = ctypes.byref(self._c)
+
+
+def rotary_table(max_position: int, rotary_dim: int, base: float = 10000.0, device="cuda"):
+    """The table of angles p * base^(-2 i / rotary_dim), taken in 64 bits and rounded once."""
+    import torch
+
+    half = torch.arange(rotary_dim // 2, dtype=torch.float64, device=device)
+    angle = torch.arange(max_position, dtype=torch.float64, device=device)[:, None] * \
+        base ** (-2.0 * half / rotary_dim)
+    return torch.cat((torch.cos(angle), torch.sin(angle)), 1).float()
+
+
+def _tokens(name: str, t, heads: int, hd: int, n: Optional[int] = None) -> int:
+    """The distance between tokens of ``t`` [n, heads, hd], whose heads and values are adjacent."""
+    import torch
+
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != hd or (n is not None and shape[0] != n):
+        raise ValueError(f"{name} must be [{'tokens' if n is None else n}, {heads}, {hd}], got "
+                         f"{list(shape)}")
+    if (hd > 1 and stride[2] != 1) or (heads > 1 and stride[1] != hd):
+        raise ValueError(f"the heads of a token of {name} must be adjacent")
+    return stride[0] if shape[0] > 1 else heads * hd
+
+
+def _int32(name: str, t, n: int, device) -> int:
+    import torch
+
+    if t.dtype != torch.int32 or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous int32")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the keys are on {device}")
+    return t.data_ptr()
+
+
+def _word(error_word, device) -> Optional[int]:
+    return None if error_word is None else _int32("error_word", error_word, 1, device)
+
+
+def _append(call: str, dims, q, k, v, slot_mapping, k_cache, v_cache, positions, rotation, scales,
+            q_out, error_word, stream, cache_pointer):
+    import torch
+
+    nkv, hd = dims.num_kv_heads, dims.head_dim
+    if not k.is_cuda:
+        raise ValueError("k must be a CUDA tensor")
+    device = k.device
+    k_stride = _tokens("k", k, nkv, hd)
+    n = k.shape[0]
+    v_stride = _tokens("v", v, nkv, hd, n)
+    on = rb._stream_on(device, stream)
+    q_at = q_out_at = None
+    q_stride = q_out_stride = 0
+    if q is not None:
+        q_stride = _tokens("q", q, dims.num_q_heads, hd, n)
+        if q_out is None:
+            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+                q_out = torch.empty((n, dims.num_q_heads, hd), dtype=q.dtype, device=device)
+        q_out_stride = _tokens("q_out", q_out, dims.num_q_heads, hd, n)
+        q_at, q_out_at = q.data_ptr(), q_out.data_ptr()
+        if q.device != device or q_out.device != device:
+            raise ValueError(f"q and q_out must be on {device}, as the keys are")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if v.device != device:
+        raise ValueError(f"v is on {v.device}, the keys are on {device}")
+    turn = position_at = None
+    if rotation is not None:
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        if rotation.table.device != device:
+            raise ValueError(f"the rotation's table is on {rotation.table.device}, the keys are on "
+                             f"{device}")
+        turn, position_at = rotation._ref, _int32("positions", positions, n, device)
+    rb._check(call, getattr(rb.lib, call)(
+        rb._dims_ref(dims), n, turn, position_at, q_at, q_stride, k.data_ptr(), k_stride,
+        v.data_ptr(), v_stride, _int32("slot_mapping", slot_mapping, n, device), *scales, q_out_at,
+        q_out_stride, cache_pointer("k_cache", k_cache, dims, device),
+        cache_pointer("v_cache", v_cache, dims, device), _word(error_word, device), on))
+    return q_out
+
+
+def _cache16(name: str, t, dims, device) -> int:
+    import torch
+
+    n = dims.num_blocks * dims.block_size * dims.num_kv_heads * dims.head_dim
+    if t.dtype != torch.bfloat16 or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous bf16 values")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the keys are on {device}")
+    return t.data_ptr()
+
+
+def _cache4(name: str, t, dims, device) -> int:
+    import torch
+
+    shape = (dims.num_blocks, dims.num_kv_heads, 9 * dims.head_dim)
+    if t.dtype != torch.uint8 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous uint8 {list(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t.data_ptr()
+
+
+def kv_append(dims: rb.Dims, q, k, v, slot_mapping, k_cache, v_cache, positions=None,
+              rotation: Optional[Rotation] = None, q_out=None, error_word=None, stream=None):
+    """Rotates ``q`` [tokens, nh, hd] and ``k`` [tokens, nkv, hd] by ``positions`` and appends k and
+    ``v`` to the caches at ``slot_mapping`` (a negative slot appends nothing).  q, k and v may be
+    slices of one projection's output (heads adjacent, tokens any distance apart); q may be None.
+    Returns the rotated queries: ``q_out`` (q itself to rotate in place) or a new tensor."""
+    return _append("rb_kv_append", dims, q, k, v, slot_mapping, k_cache, v_cache, positions,
+                   rotation, (), q_out, error_word, stream, _cache16)
+
+
+def kv4_cache(dims: rb.Dims, device="cuda") -> tuple:
+    """K and V of an empty cache in 4 bits (every value 0)."""
+    import torch
+
+    shape = (dims.num_blocks, dims.num_kv_heads, 9 * dims.head_dim)
+    return tuple(torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2))
+
+
+def kv4_page_dims(dims: rb.Dims) -> rb.Dims:
+    """``dims`` with which ``PagePool`` copies and compacts whole pages of a 4-bit cache (viewed as
+    ``kv4_pages``): a page is one token of 9 * head_dim / 2 values a head.  Not for ``fork``."""
+    return rb.Dims(1, dims.num_q_heads, dims.num_kv_heads, 9 * dims.head_dim // 2,
+                   dims.max_num_reqs, dims.max_model_len, dims.max_blocks_per_req,
+                   dims.num_blocks, dims.null_block, dims.kernel_blocks_per_manager_block)
+
+
+def kv4_pages(cache):
+    """A 4-bit cache as the bf16 tensor that ``PagePool`` moves pages of (the same memory)."""
+    import torch
+
+    return cache.view(torch.bfloat16)
+
+
+def kv4_append(dims: rb.Dims, q, k, v, slot_mapping, k_cache, v_cache, positions=None,
+               rotation: Optional[Rotation] = None, k_scale: float = 1.0, v_scale: float = 1.0,
+               q_out=None, error_word=None, stream=None):
+    """``kv_append`` into a cache held in 4 bits."""
+    return _append("rb_kv4_append", dims, q, k, v, slot_mapping, k_cache, v_cache, positions,
+                   rotation, (k_scale, v_scale), q_out, error_word, stream, _cache4)
+
+
+def kv4_read(dims: rb.Dims, slots, k_cache, v_cache, k_scale: float = 1.0, v_scale: float = 1.0,
+             out: Any = None, error_word=None, stream=None) -> tuple:
+    """K and V rows [len(slots), nkv, hd] in bf16 of a 4-bit cache's slots (a negative slot: zeros),
+    into the pair ``out`` where it is given."""
+    import torch
+
+    if slots.dim() != 1 or not slots.is_cuda:
+        raise ValueError("slots must be a one-dimensional CUDA tensor")
+    n, device = slots.shape[0], slots.device
+    on = rb._stream_on(device, stream)
+    if out is None:
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+            out = tuple(torch.empty((n, dims.num_kv_heads, dims.head_dim), dtype=torch.bfloat16,
+                                    device=device) for _ in range(2))
+    k, v = out
+    for name, t in (("out[0]", k), ("out[1]", v)):
+        _tokens(name, t, dims.num_kv_heads, dims.head_dim, n)
+        if t.device != device or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous, on {device}")
+    rb._check("rb_kv4_read", rb.lib.rb_kv4_read(
+        rb._dims_ref(dims), n, _int32("slots", slots, n, device),
+        _cache4("k_cache", k_cache, dims, device), _cache4("v_cache", v_cache, dims, device),
+        k_scale, v_scale, k.data_ptr(), v.data_ptr(), _word(error_word, device), on))
+    return k, v
