@@ -27,6 +27,7 @@
  *   rb_token_logprobs  log probability and rank of given tokens, entropy, top alternatives
  *   rb_kv_append       queries and keys rotated by their positions, keys and values appended
  *   rb_kv4_*           a paged cache held in 4 bits: appending to it (rotated), reading rows back
+ *   rb_paged_attention_kv4  the attention over such a cache
  *   rb_add_rms_norm    the residual's addition and the root-mean-square norm, output in 8 bits
  *
  * Conventions shared by every entry point
@@ -819,6 +820,23 @@ rb_status rb_kv4_append(const rb_dims* dims, int32_t num_tokens_padded,
 rb_status rb_kv4_read(const rb_dims* dims, int32_t num_rows, const int32_t* d_slots,
                       const void* d_k_cache, const void* d_v_cache, float k_scale, float v_scale,
                       void* d_k_out, void* d_v_out, int32_t* d_error_word, void* stream);
+
+/*
+ * rb_paged_attention_kv4 — rb_paged_attention over a 4-bit cache (rb_kv4_append's): softmax over
+ * each query's keys of softmax_scale * q . K, times V, with K and V the values that the cache
+ * stands for (k_scale and v_scale included); they enter the products unrounded.
+ * Arguments, layouts, workspace (rb_paged_attention_workspace_size), supported shapes and errors are
+ * those of rb_paged_attention, with caches [num_blocks, nkv, 9 * hd] of bytes; RB_ERR_INVALID_ARG
+ * also for a softmax_scale or layer scale that is not positive and finite.  What pages hold behind
+ * a request's last token does not reach its rows.
+ */
+rb_status rb_paged_attention_kv4(const rb_dims* dims, int32_t num_reqs, int32_t num_tokens,
+                                 int32_t num_tokens_padded, const void* d_q,
+                                 const void* d_k_cache, const void* d_v_cache,
+                                 const int32_t* d_block_table, const int32_t* d_query_start_loc,
+                                 const int32_t* d_seq_lens, float softmax_scale, float k_scale,
+                                 float v_scale, void* d_out, void* d_workspace,
+                                 size_t workspace_bytes, int32_t* d_error_word, void* stream);
 
 /*
  * rb_add_rms_norm — for each of num_rows rows of hidden states

@@ -15,6 +15,7 @@
     kv_append        kv_write with the position rotation (Rotation) of queries and keys on the way
     kv4_append       the same into a paged cache held in 4 bits (kv4_cache); kv4_read reads rows
                      of it back
+    paged_attention_kv4  the attention over a cache held in 4 bits
     add_rms_norm     the residual's addition and the root-mean-square norm; add_rms_norm_fp8 with
                      an output in 8 bits and scales
     token_logprobs   log probability and rank of given tokens, entropy, top alternatives
@@ -32,7 +33,7 @@ from ._binding import (EBIT_BATCH_ID, EBIT_BATCH_SIZE, EBIT_LOGITS, EBIT_NO_PAGE
                        EBIT_NOT_FINITE, EBIT_PAGE_PAIR, EBIT_PAGE_REF, EBIT_POSITION, EBIT_ROW,
                        EBIT_TOKEN_ID)
 from .kv4 import (Rotation, kv4_append, kv4_cache, kv4_page_dims, kv4_pages, kv4_read,
-                  kv_append, rotary_table)
+                  kv_append, paged_attention_kv4, rotary_table)
 from .logprobs import MAX_TOP_LOGPROBS, TokenLogprobs, token_logprobs
 from .norm import add_rms_norm, add_rms_norm_fp8
 from .pages import PagePool, pages_workspace_size
@@ -46,4 +47,4 @@ __all__ = ["Dims", "RbError", "gather_rows", "kv_write", "launch_count", "lib", 
            "paged_attention_scored", "PagePool",
            "pages_workspace_size", "TokenLogprobs", "token_logprobs", "MAX_TOP_LOGPROBS", "Rotation",
            "rotary_table", "kv_append", "kv4_cache", "kv4_append", "kv4_read", "kv4_page_dims",
-           "kv4_pages", "add_rms_norm", "add_rms_norm_fp8"]
+           "kv4_pages", "paged_attention_kv4", "add_rms_norm", "add_rms_norm_fp8"]

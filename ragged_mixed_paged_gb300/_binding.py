@@ -162,6 +162,8 @@ def _load():
         "rb_kv4_append": (I32, [PD, I32, PR, P, P, I64, P, I64, P, I64, P, F32, F32, P, I64, P, P,
                                 P, P]),
         "rb_kv4_read": (I32, [PD, I32, P, P, P, F32, F32, P, P, P, P]),
+        "rb_paged_attention_kv4": (I32, [PD, I32, I32, I32, P, P, P, P, P, P, F32, F32, F32, P, P,
+                                         ctypes.c_size_t, P, P]),
         "rb_add_rms_norm": (I32, [I32, I32, I32, P, I64, P, I64, P, I64, P, F32, I32, I32, P, P,
                                   P]),
         "rb_token_logprobs": (I32, [I32, I32, ctypes.c_int64, I32, P, P, I32, P, P, P, P, P, P,

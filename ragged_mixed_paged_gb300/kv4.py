@@ -63,7 +63,7 @@ def _int32(name: str, t, n: int, device) -> int:
     if t.dtype != torch.int32 or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{name} must be {n} contiguous int32")
     if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the keys are on {device}")
+        raise ValueError(f"{name} is on {t.device}, the call's tensors on {device}")
     return t.data_ptr()
 
 
@@ -201,3 +201,43 @@ def kv4_read(dims: rb.Dims, slots, k_cache, v_cache, k_scale: float = 1.0, v_sca
         _cache4("k_cache", k_cache, dims, device), _cache4("v_cache", v_cache, dims, device),
         k_scale, v_scale, k.data_ptr(), v.data_ptr(), _word(error_word, device), on))
     return k, v
+
+
+def paged_attention_kv4(dims: rb.Dims, num_reqs: int, num_tokens: int, q, k_cache, v_cache,
+                        block_table, query_start_loc, seq_lens, k_scale: float = 1.0,
+                        v_scale: float = 1.0, out=None, workspace=None,
+                        softmax_scale: Optional[float] = None, error_word=None, stream=None):
+    """``paged_attention`` over a cache held in 4 bits, which holds the step's own rows already
+    (``kv4_append``)."""
+    import torch
+
+    nh, hd = dims.num_q_heads, dims.head_dim
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    device = q.device
+    if q.dtype != torch.bfloat16 or not q.is_contiguous() or q.dim() < 1 or \
+            q.numel() != q.shape[0] * nh * hd:
+        raise ValueError(f"q must be contiguous bf16 [tokens, {nh}, {hd}]")
+    on = rb._stream_on(device, stream)
+    if out is None or workspace is None:
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+            if out is None:
+                out = torch.empty_like(q)
+            if workspace is None:
+                workspace = torch.empty(rb.workspace_size(dims, num_reqs, num_tokens),
+                                        dtype=torch.uint8, device=device)
+    if out.dtype != torch.bfloat16 or not out.is_contiguous() or out.numel() < q.numel() or \
+            out.device != device:
+        raise ValueError(f"out must be {q.numel()} contiguous bf16 values on {device}")
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
+            workspace.device != device:
+        raise ValueError(f"workspace must be contiguous uint8 on {device}")
+    scale = 1.0 / math.sqrt(hd) if softmax_scale is None else softmax_scale
+    rb._check("rb_paged_attention_kv4", rb.lib.rb_paged_attention_kv4(
+        rb._dims_ref(dims), num_reqs, num_tokens, q.shape[0], q.data_ptr(),
+        _cache4("k_cache", k_cache, dims, device), _cache4("v_cache", v_cache, dims, device),
+        _int32("block_table", block_table, num_reqs * dims.max_blocks_per_req, device),
+        _int32("query_start_loc", query_start_loc, num_reqs + 1, device),
+        _int32("seq_lens", seq_lens, num_reqs, device), scale, k_scale, v_scale, out.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _word(error_word, device), on))
+    return out
