@@ -7,13 +7,14 @@
 // attn_prefill_tc.cu): one persistent launch in which every CTA runs decode units
 // (attn_kv4_decode.cuh) and prefill units, the kind the planner gave it first.
 //
-// Prefill unit = (request, kv head, pair of 128-row query tiles); 12 warps:
-//   warp 1      takes units, loads Q (TMA), and turns the codes of each 128-key K tile into fp16 in
-//               the 128-byte-swizzled layout that tcgen05.mma reads;
-//   warp 2      does the same for V;
+// Decode units take all 16 warps.  Prefill unit = (request, kv head, pair of 128-row query tiles):
 //   warp 0      one thread issues the MMAs: S = Q K^T (both K-major in shared memory), O += P V (P
 //               from TMEM, V MN-major), kind::f16 with fp16 operands;
-//   warps 4-11  softmax and epilogue, a thread per query row.
+//   warp 1      takes units and loads Q (TMA);
+//   warp 2      copies the cache's bytes of each key tile to shared memory (bulk copies);
+//   warps 4, 5  turn the codes of each 128-key K tile into fp16 in the 128-byte-swizzled layout that
+//               tcgen05.mma reads; warps 6, 7 the same for V;
+//   warps 8-15  softmax and epilogue, a thread per query row.
 // fp16 holds every value of the cache exactly, so K and V enter the products unrounded, and P with 11
 // bits instead of bf16's 8.  Q comes as bf16: each softmax thread divides its own row by a power of
 // two, which makes it exact in fp16 (attn_kv4_decode.cuh), and keeps the factor for its scores.
@@ -36,12 +37,21 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(AttnArgs a, int 
   plan_body<false>(a, head_dim, ReqSrc{a.qsl, a.seq_lens, nullptr});
 }
 
+// Threads and registers: launched with 128 for each of 512 threads, which the decode phases use; a
+// prefill phase gives the softmax warps 184 and the others 72.
+constexpr int kThreads = 512, kWarps = 16;
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 184, kControlRegs = 72;
+static_assert(256 * kSoftmaxRegs + 256 * kControlRegs <= kThreads * kLaunchRegs,
+              "register split exceeds the launch allocation");
+constexpr int kTurnWarp = 4, kSoftmaxWarp = 8;  // the first ones
+constexpr int kRawSlots = 3;                    // half tiles of the cache's bytes on their way
+
 struct Kv4Shared {
   uint64_t unit_full[4], unit_empty[4];
   uint64_t q_full[2], q_ready[2], q_empty;  // Q landed (bf16), Q turned (fp16), per side
-  uint64_t k_full[TcCfg<128>::kStagesK], k_empty[TcCfg<128>::kStagesK];
-  uint64_t v_full[TcCfg<128>::kStagesV], v_empty[TcCfg<128>::kStagesV];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+  uint64_t raw_full[2][kRawSlots], raw_empty[2][kRawSlots];  // K and V
   uint64_t drain;
   TcUnit units[4];
   uint32_t tmem_base;
@@ -50,153 +60,201 @@ struct Kv4Shared {
   int role_rank;
 };
 
-// Largest sum of one tile's exponents (128 keys of a row): P stays below 2^15 in fp16.
-constexpr float kSumLimit = 32768.f;
-
 __host__ __device__ constexpr uint32_t make_idesc_f16(int M, int N, bool b_mn_major) {
   return tc::make_idesc(M, N, b_mn_major) & ~((1u << 7) | (1u << 10));  // A and B fp16, not bf16
 }
 
-// One lane's bytes of a page of one kv head: kRows runs of 32 codes with their two scales.
+// The warps that turn tiles read the cache's bytes from rings of pages in shared memory.  Loops are kept rolled: straight-line code of several roles runs at the rate of
+// instruction fetch (a tile's half unrolled took 8000 cycles, ten times its instructions).
 template <int HD>
-struct Codes {
-  static constexpr int kRows = HD / 64;
-  uint4 c[kRows];
-  uint32_t s[kRows];
+struct Kv4Cfg {
+  using C = TcCfg<HD>;
+  static constexpr int kStagesK = 2, kStagesV = 2;
+  static constexpr int kVOffset = kStagesK * C::kTileBytes;
+  static constexpr int kQOffset = kVOffset + kStagesV * C::kTileBytes;  // Q_A then Q_B
+  static constexpr int kRawOffset = kQOffset + 2 * C::kQBytes;
+  static constexpr int kRawBytes = C::kPagesPerTile / 2 * 9 * HD;  // K or V of half a tile
+  static constexpr int kUsed = kRawOffset + 2 * kRawSlots * kRawBytes;
+  static constexpr int kDecode = kWarps * kv4d::Ring<HD>::kWarpBytes;
+  static constexpr int kMost = kUsed > kDecode ? kUsed : kDecode;
+  // at least 120 KB keeps one CTA per SM (each CTA holds all 512 TMEM columns)
+  static constexpr int kSmemBytes = (kMost + 1024) > 120 * 1024 ? (kMost + 1024) : 120 * 1024;
 };
 
-// Lane's run of 32 values: token and place in the head, of run i of a page.
-template <int HD>
-__device__ __forceinline__ int run_token(int lane, int i) {
-  return HD == 128 ? i * 8 + (lane >> 2) : lane >> 1;
-}
-template <int HD>
-__device__ __forceinline__ int run_part(int lane) {
-  return HD == 128 ? lane & 3 : lane & 1;
-}
-
+// Two pages' codes to fp16 rows of a tile (128 keys x 128 bytes, 128-byte swizzle, one such block per
+// 64 values).  A lane takes 32 values of a token: four 16-byte stores.  A head of 128 has its
+// quarters in two blocks of the same banks: the upper two take their pieces in the order 2, 3,
+// 0, 1.
 template <int HD, bool kValues>
-__device__ __forceinline__ void load_codes(Codes<HD>& b, const uint8_t* page, int lane) {
-  const int part = run_part<HD>(lane);
-#pragma unroll
-  for (int i = 0; i < Codes<HD>::kRows; ++i) {
-    const int tok = run_token<HD>(lane, i);
-    b.c[i] = __ldg(reinterpret_cast<const uint4*>(page + tok * (HD / 2) + part * 16));
-    const uint8_t* s = page + 8 * HD;
-    if constexpr (kValues)
-      b.s[i] = __ldg(s + 2 * part * kPage + tok) |
-               static_cast<uint32_t>(__ldg(s + (2 * part + 1) * kPage + tok)) << 8;
-    else
-      b.s[i] = __ldg(reinterpret_cast<const uint16_t*>(s + tok * (HD / 16) + 2 * part));
-  }
-}
-
-// Turns the runs into fp16 rows of a tile (128 keys x 128 bytes, 128-byte swizzle, one such block per
-// 64 values): four 16-byte stores a run.  A head of 128 has its runs in two blocks of the same
-// banks: the upper two parts take their pieces in the order 2, 3, 0, 1.
-template <int HD>
-__device__ __forceinline__ void store_codes(const Codes<HD>& b, uint8_t* tile, int page, int lane) {
+__device__ __forceinline__ void turn_pages(const uint8_t* page, uint8_t* tile, int first_row,
+                                           int lane) {
   using C = TcCfg<HD>;
-  const int part = run_part<HD>(lane);
-  const bool upper = HD == 128 && part >= 2;
-#pragma unroll
-  for (int i = 0; i < Codes<HD>::kRows; ++i) {
-    const int row = page * kPage + run_token<HD>(lane, i);
-    const uint4 c = b.c[i];
+  constexpr int kParts = HD / 32;  // lanes of a token
+  const int part = lane % kParts;
+  const bool upper = part >= 2;
+#pragma unroll 1
+  for (int i = 0; i < kParts; ++i) {
+    if (i == kParts / 2) {
+      page += 9 * HD;
+      first_row += kPage;
+    }
+    const int tok = lane / kParts + i % (kParts / 2) * (32 / kParts);
+    const uint4 c = *reinterpret_cast<const uint4*>(page + tok * (HD / 2) + part * 16);
+    const uint8_t* sp = page + 8 * HD;
+    uint32_t sb;
+    if constexpr (kValues)
+      sb = sp[2 * part * kPage + tok] | static_cast<uint32_t>(sp[(2 * part + 1) * kPage + tok]) << 8;
+    else
+      sb = *reinterpret_cast<const uint16_t*>(sp + tok * (HD / 16) + 2 * part);
+    const uint32_t s2 = kv4d::scales2(sb);
+    const int row = first_row + tok;
+    uint8_t* dst = tile + (part >> 1) * (HD == 128 ? C::kHalfBytes : 0) + row * 128;
     const uint32_t w[4] = {upper ? c.z : c.x, upper ? c.w : c.y, upper ? c.x : c.z,
                            upper ? c.y : c.w};
-    const uint32_t s2 = kv4d::scales2(b.s[i]);
-    const uint32_t first = upper ? kv4d::high2(s2) : kv4d::low2(s2);
-    const uint32_t second = upper ? kv4d::low2(s2) : kv4d::high2(s2);
-    uint8_t* dst = tile + (part >> 1) * (HD == 128 ? C::kHalfBytes : 0) + row * 128;
-    const int chunk = (part & 1) * 4 + (upper ? 2 : 0);
+    const uint32_t lo = kv4d::low2(s2), hi = kv4d::high2(s2);
+    const int chunk = ((part & 1) * 4 + (upper ? 2 : 0)) ^ (row & 7);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       uint32_t h[4];
       kv4::values8(w[k], h);
-      const uint32_t m = k < 2 ? first : second;
-      *reinterpret_cast<uint4*>(dst + (((chunk ^ k) ^ (row & 7)) << 4)) =
+      const uint32_t m = (k < 2) != upper ? lo : hi;
+      *reinterpret_cast<uint4*>(dst + ((chunk ^ k) << 4)) =
           make_uint4(hmul2(h[0], m), hmul2(h[1], m), hmul2(h[2], m), hmul2(h[3], m));
     }
   }
 }
 
-// Turns a unit's tiles one after the other into a ring of `kStages` tiles; false: gave up.  The
-// codes of kAhead pages are on their way in registers, across the tiles.
-template <int HD, bool kValues, int kStages>
-__device__ __forceinline__ bool produce_tiles(const Kv4Args& g4, const TcUnit& un, uint8_t* ring,
-                                              uint64_t* full, uint64_t* empty, uint32_t it,
-                                              volatile int* abort, int lane) {
-  using C = TcCfg<HD>;
-  const AttnArgs& a = g4.a;
-  constexpr int kAhead = 4;
-  const uint8_t* cache = kValues ? g4.v : g4.k;
-  PageWindow pw(a, un, lane);
-  auto at = [&](int id, int page) {
-    return cache + (static_cast<size_t>(__shfl_sync(0xffffffffu, id, page)) * a.nkv + un.h) *
-                       kv4::page_bytes(HD);
-  };
-  int id = pw.tile_page(0, !kValues);
-  Codes<HD> buf[kAhead];
-#pragma unroll
-  for (int p = 0; p < kAhead; ++p) load_codes<HD, kValues>(buf[p], at(id, p), lane);
-  for (int j = 0; j < un.n_kt; ++j) {
-    const uint32_t tile = it + j, st = tile % kStages;
-    const int next = j + 1 < un.n_kt ? pw.tile_page(j + 1, !kValues) : id;
-    int ok = 1;
-    if (lane == 0) ok = tc_wait(&empty[st], ((tile / kStages) & 1) ^ 1, abort, a) ? 1 : 0;
-    if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
-    uint8_t* dst = ring + st * C::kTileBytes;
-#pragma unroll
-    for (int p = 0; p < C::kPagesPerTile; ++p) {
-      store_codes<HD>(buf[p % kAhead], dst, p, lane);
-      const int n = p + kAhead;
-      load_codes<HD, kValues>(buf[p % kAhead],
-                              n < C::kPagesPerTile ? at(id, n) : at(next, n - C::kPagesPerTile),
-                              lane);
-    }
-    id = next;
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&full[st]);
-  }
-  return true;
+// One contiguous copy into shared memory, its bytes counted on `bar`.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const uint8_t* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
 }
 
-// Warp 1: units, Q and K.
+// Warp 2: the cache's bytes of each half tile (four pages) of each unit, K and V, into a ring of
+// kRawSlots half tiles.  A bulk copy a page: 16-byte cp.async starves beside the MMAs, which read
+// shared memory at its full rate (pages five ahead came 6000 cycles late).
 template <int HD>
-__device__ void producer_qk4(const Kv4Args& g4, Kv4Shared& sh, uint32_t smem_base,
-                             uint8_t* smem_ptr, const CUtensorMap* qmap) {
+__device__ __forceinline__ void producer_raw(const Kv4Args& g4, Kv4Shared& sh, uint32_t raw_at) {
   using C = TcCfg<HD>;
+  using K4 = Kv4Cfg<HD>;
   const AttnArgs& a = g4.a;
+  volatile int* abort = &sh.abort;
+  constexpr int kHalf = C::kPagesPerTile / 2, kBytes = 9 * HD;
+  const int lane = threadIdx.x & 31;
+  const int kv = lane >> 2 & 1;  // lanes 0-3 copy K, 4-7 V
+  const uint8_t* cache = kv ? g4.v : g4.k;
+  uint32_t count = 0;  // half tiles so far
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    const int slot = k % C::kRing;
+    int go = 1;
+    if (lane == 0) go = tc_wait(&sh.unit_full[slot], (k / C::kRing) & 1, abort, a) ? 1 : 0;
+    if (!__shfl_sync(0xffffffffu, go, 0)) break;
+    const TcUnit un = sh.units[slot];
+    if (!un.valid) break;
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&sh.unit_empty[slot]);  // the descriptor is in registers
+    PageWindow pw(a, un, lane);
+    int id = 0;
+#pragma unroll 1
+    for (int i = 0; i < 2 * un.n_kt; ++i, ++count) {
+      if ((i & 1) == 0) id = pw.tile_page(i >> 1, true);
+      const int mine = __shfl_sync(0xffffffffu, id, (i & 1) * kHalf + (lane & 3));
+      const uint32_t st = count % kRawSlots;
+      if ((lane & 3) == 0 && lane < 8) {
+        go = tc_wait(&sh.raw_empty[kv][st], ((count / kRawSlots) & 1) ^ 1, abort, a) ? 1 : 0;
+        if (go) mbar_arrive_expect_tx(&sh.raw_full[kv][st], kHalf * kBytes);
+      }
+      const bool armed_k = __shfl_sync(0xffffffffu, go, 0), armed_v = __shfl_sync(0xffffffffu, go, 4);
+      // (what is armed is copied, so that its barrier completes whatever happens)
+      if (lane < 8 && (kv ? armed_v : armed_k))
+        bulk_copy(raw_at + (2 * st + kv) * K4::kRawBytes + (lane & 3) * kBytes,
+                  cache + (static_cast<size_t>(mine) * a.nkv + un.h) * kBytes, kBytes,
+                  &sh.raw_full[kv][st]);
+      if (!(armed_k && armed_v)) { ok = false; break; }
+    }
+  }
+  if (lane == 0 && *abort)  // let the copies already issued land before the CTA can exit
+#pragma unroll 1
+    for (uint32_t i = 0; i < kRawSlots && i < count + 1; ++i) {
+      const uint32_t c = count - i;  // (the one after the last may be armed in part)
+      for (int w = 0; w < 2; ++w)
+        mbar_wait_bounded(&sh.raw_full[w][c % kRawSlots], (c / kRawSlots) & 1, 1000000ull);
+    }
+  __syncwarp();
+}
+
+// A warp of the two that turn K (V): two pages of each half tile, into a ring of kStages tiles.
+template <int HD, bool kValues, int kStages>
+__device__ __forceinline__ void turn_tiles(const AttnArgs& a, Kv4Shared& sh, uint8_t* ring,
+                                           const uint8_t* raw, uint64_t* full, uint64_t* empty) {
+  using C = TcCfg<HD>;
+  using K4 = Kv4Cfg<HD>;
+  volatile int* abort = &sh.abort;
+  constexpr int kBytes = 9 * HD, kHalf = C::kPagesPerTile / 2;
+  const int lane = threadIdx.x & 31, page = (threadIdx.x >> 5 & 1) * (kHalf / 2);
+  uint32_t it = 0, count = 0;
+  auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {
+    const bool done = tc_wait(bar, phase, abort, a);
+    return !__any_sync(0xffffffffu, !done);
+  };
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    const int slot = k % C::kRing;
+    if (!wait(&sh.unit_full[slot], (k / C::kRing) & 1)) break;
+    const int tiles = sh.units[slot].n_kt, valid = sh.units[slot].valid;
+    if (!valid) break;
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&sh.unit_empty[slot]);
+#pragma unroll 1
+    for (int i = 0; i < 2 * tiles; ++i, ++count) {
+      const uint32_t tile = it + (i >> 1), st = tile % kStages, from = count % kRawSlots;
+      if (!wait(&sh.raw_full[kValues][from], (count / kRawSlots) & 1) ||
+          ((i & 1) == 0 && !wait(&empty[st], ((tile / kStages) & 1) ^ 1))) {
+        ok = false;
+        break;
+      }
+      const uint8_t* src = raw + (2 * from + kValues) * K4::kRawBytes;
+      turn_pages<HD, kValues>(src + page * kBytes, ring + st * C::kTileBytes,
+                              ((i & 1) * kHalf + page) * kPage, lane);
+      if (i & 1) fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&sh.raw_empty[kValues][from]);
+        if (i & 1) tc::mbar_arrive(&full[st]);
+      }
+    }
+    it += tiles;
+  }
+}
+
+// Warp 1: units and Q.
+template <int HD>
+__device__ void producer_q4(const AttnArgs& a, Kv4Shared& sh, uint32_t smem_base,
+                            const CUtensorMap* qmap) {
+  using C = TcCfg<HD>;
+  using K4 = Kv4Cfg<HD>;
   volatile int* abort = &sh.abort;
   const int lane = threadIdx.x & 31;
   const int n_units = a.header[kHNumPrefillUnits];
-  uint32_t it = 0, q_armed[2] = {0, 0};
-  auto lane0_wait = [&](uint64_t* bar, uint32_t phase) -> bool {
-    int ok = 1;
-    if (lane == 0) ok = tc_wait(bar, phase, abort, a) ? 1 : 0;
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
-  };
-  for (int k = 0;; ++k) {
-    const int slot = k % C::kRing;
-    if (!lane0_wait(&sh.unit_empty[slot], ((k / C::kRing) & 1) ^ 1)) break;
-    int withhold = 0;
-    if (lane == 0) {
+  uint32_t q_armed[2] = {0, 0};
+  if (lane == 0) {
+    for (int k = 0;; ++k) {
+      const int slot = k % C::kRing;
+      if (!tc_wait(&sh.unit_empty[slot], ((k / C::kRing) & 1) ^ 1, abort, a)) break;
       const int u = atomicAdd(a.header + kHPrefillNext, 1);
       TcUnit un{};
       if (u < n_units) un = decode_unit(a, u);
       sh.units[slot] = un;
       // test hook: CTA 0 stops before its first unit reaches the other roles
-      withhold = a.withhold_first_unit && blockIdx.x == 0 && k == 0 && un.valid;
-      if (!withhold) tc::mbar_arrive(&sh.unit_full[slot]);
-    }
-    if (__shfl_sync(0xffffffffu, withhold, 0)) break;
-    __syncwarp();
-    const TcUnit un = sh.units[slot];
-    if (!un.valid) break;
-    if (!lane0_wait(&sh.q_empty, (k & 1) ^ 1)) break;
-    if (lane == 0) {
+      if (a.withhold_first_unit && blockIdx.x == 0 && k == 0 && un.valid) break;
+      tc::mbar_arrive(&sh.unit_full[slot]);
+      if (!un.valid) break;
+      if (!tc_wait(&sh.q_empty, (k & 1) ^ 1, abort, a)) break;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (un.n[x] == 0) continue;
@@ -204,64 +262,39 @@ __device__ void producer_qk4(const Kv4Args& g4, Kv4Shared& sh, uint32_t smem_bas
         ++q_armed[x];
 #pragma unroll
         for (int hf = 0; hf < C::kHalves; ++hf)
-          tma_load_3d(smem_base + C::kQOffset + x * C::kQBytes + hf * C::kQHalfBytes, qmap,
+          tma_load_3d(smem_base + K4::kQOffset + x * C::kQBytes + hf * C::kQHalfBytes, qmap,
                       &sh.q_full[x], hf * 64, un.h * a.group, un.t0 + un.tok0 + a.tile_tokens * x);
       }
     }
-    __syncwarp();
-    if (!produce_tiles<HD, false, C::kStagesK>(g4, un, smem_ptr, sh.k_full, sh.k_empty, it, abort,
-                                               lane))
-      break;
-    it += un.n_kt;
+    if (*abort)  // let the copies already issued land before the CTA can exit
+      for (int x = 0; x < 2; ++x)
+        if (q_armed[x]) mbar_wait_bounded(&sh.q_full[x], (q_armed[x] - 1) & 1, 100000000ull);
   }
-  if (lane == 0 && *abort) {  // let the copies already issued land before the CTA can exit
-    for (int x = 0; x < 2; ++x)
-      if (q_armed[x]) mbar_wait_bounded(&sh.q_full[x], (q_armed[x] - 1) & 1, 100000000ull);
-  }
+  __syncwarp();
 }
 
-// Warp 2: V.
-template <int HD>
-__device__ void producer_v4(const Kv4Args& g4, Kv4Shared& sh, uint8_t* smem_ptr) {
-  using C = TcCfg<HD>;
-  volatile int* abort = &sh.abort;
-  const int lane = threadIdx.x & 31;
-  uint32_t it = 0;
-  for (int k = 0;; ++k) {
-    const int slot = k % C::kRing;
-    int ok = 1;
-    if (lane == 0) ok = tc_wait(&sh.unit_full[slot], (k / C::kRing) & 1, abort, g4.a) ? 1 : 0;
-    if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-    const TcUnit un = sh.units[slot];
-    if (!un.valid) break;
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&sh.unit_empty[slot]);  // the descriptor is in registers
-    if (!produce_tiles<HD, true, C::kStagesV>(g4, un, smem_ptr + C::kVOffset, sh.v_full,
-                                              sh.v_empty, it, abort, lane))
-      break;
-    it += un.n_kt;
-  }
-}
-
-// The MMA issuer (one thread).  K and V are written by ordinary stores of other warps, which fence
-// them for the tensor core before they arrive; the waits for them acquire.  P, O and S are tensor
-// memory, ordered by tcgen05 fences, and their waits are relaxed (an acquiring wait behind queued
-// MMAs idles the tensor pipe).
+// The MMA issuer (one thread).  What its waits guard is read by tcgen05.mma alone: P and O in tensor
+// memory, and K and V, whose writers make their stores visible to the tensor core (a proxy fence)
+// before they arrive.  Each wait is followed by tcgen05.fence::after_thread_sync, and so they are
+// relaxed (an acquiring wait behind queued MMAs idles the tensor pipe).
 template <int HD>
 __device__ void mma_issuer4(const AttnArgs& a, Kv4Shared& sh, uint32_t tmem, uint32_t smem_base) {
   using C = TcCfg<HD>;
+  using K4 = Kv4Cfg<HD>;
   volatile int* abort = &sh.abort;
   constexpr uint32_t idesc_s = make_idesc_f16(128, 128, false);
   constexpr uint32_t idesc_o = make_idesc_f16(128, HD, true);
   uint32_t itk = 0, tcount[2] = {0, 0}, ucount[2] = {0, 0};
   bool issued = false;
-  auto relaxed = [&](uint64_t* bar, uint32_t phase) {
-    return mbar_test_relaxed(bar, phase) || tc_wait<true>(bar, phase, abort, a);
-  };
+  // A wait whose result decides a branch costs a few hundred cycles even when the phase is long
+  // complete, so the barriers of one step are tested together and waited for one by one only if one
+  // of them is not complete.
+  auto test = [](uint64_t* bar, uint32_t phase) { return mbar_test_relaxed(bar, phase); };
+  auto relaxed = [&](uint64_t* bar, uint32_t phase) { return tc_wait<true>(bar, phase, abort, a); };
   auto acquire = [&](uint64_t* bar, uint32_t phase) { return tc_wait(bar, phase, abort, a); };
-  const uint64_t q_desc0 = tc::sdesc_sw128(smem_base + C::kQOffset, 16, 1024);
+  const uint64_t q_desc0 = tc::sdesc_sw128(smem_base + K4::kQOffset, 16, 1024);
   const uint64_t k_desc0 = tc::sdesc_sw128(smem_base, 16, 1024);
-  const uint64_t v_desc0 = tc::sdesc_sw128(smem_base + C::kVOffset, C::kHalfBytes, 1024);
+  const uint64_t v_desc0 = tc::sdesc_sw128(smem_base + K4::kVOffset, C::kHalfBytes, 1024);
   const uint32_t q_lo = static_cast<uint32_t>(q_desc0), k_lo = static_cast<uint32_t>(k_desc0),
                  v_lo = static_cast<uint32_t>(v_desc0);
   const uint32_t q_hi = static_cast<uint32_t>(q_desc0 >> 32),
@@ -271,7 +304,7 @@ __device__ void mma_issuer4(const AttnArgs& a, Kv4Shared& sh, uint32_t tmem, uin
     return ((ks >> 2) * half_bytes + (ks & 3) * 32) >> 4;
   };
   auto issue_s = [&](int x, uint32_t kt) {  // S_x = Q_x K^T
-    const uint32_t kd = k_lo + (((kt % C::kStagesK) * C::kTileBytes) >> 4);
+    const uint32_t kd = k_lo + (((kt % K4::kStagesK) * C::kTileBytes) >> 4);
     const uint32_t qd = q_lo + ((x * C::kQBytes) >> 4);
     const uint32_t d = tmem + C::col_s(x);
     tc::mma_ss_lh(d, qd, q_hi, kd, k_hi, idesc_s, 0u);
@@ -283,7 +316,7 @@ __device__ void mma_issuer4(const AttnArgs& a, Kv4Shared& sh, uint32_t tmem, uin
     issued = true;
   };
   auto issue_pv = [&](int x, uint32_t kt, bool first, bool last) {  // O_x (+)= P_x V
-    const uint32_t vd = v_lo + (((kt % C::kStagesV) * C::kTileBytes) >> 4);
+    const uint32_t vd = v_lo + (((kt % K4::kStagesV) * C::kTileBytes) >> 4);
     const uint32_t d = tmem + C::col_o(x), p = tmem + C::col_s(x);
     tc::mma_ts_lh(d, p, vd, v_hi, idesc_o, first ? 0u : 1u);
 #pragma unroll
@@ -296,7 +329,7 @@ __device__ void mma_issuer4(const AttnArgs& a, Kv4Shared& sh, uint32_t tmem, uin
     if (!acquire(&sh.unit_full[slot], (k / C::kRing) & 1)) break;
     const TcUnit un = sh.units[slot];
     if (!un.valid) break;
-    if (!acquire(&sh.k_full[itk % C::kStagesK], (itk / C::kStagesK) & 1)) break;
+    if (!acquire(&sh.k_full[itk % K4::kStagesK], (itk / K4::kStagesK) & 1)) break;
     bool ok = true;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -313,12 +346,15 @@ __device__ void mma_issuer4(const AttnArgs& a, Kv4Shared& sh, uint32_t tmem, uin
         if (j >= un.n[x]) continue;
         const bool next_s = j + 1 < un.n[x];
         const bool need_v = !v_ready, need_o = j == 0 && ucount[x] > 0, need_k = next_s && !k_ready;
-        uint64_t* bar_v = &sh.v_full[kt % C::kStagesV];
-        uint64_t* bar_k = &sh.k_full[(kt + 1) % C::kStagesK];
-        const uint32_t ph_v = (kt / C::kStagesV) & 1, ph_k = ((kt + 1) / C::kStagesK) & 1;
-        if ((need_v && !acquire(bar_v, ph_v)) || (need_k && !acquire(bar_k, ph_k)) ||
-            (need_o && !relaxed(&sh.o_free[x], (ucount[x] - 1) & 1)) ||
-            !relaxed(&sh.p_full[x], (tcount[x] + j) & 1)) {
+        uint64_t* bar_v = &sh.v_full[kt % K4::kStagesV];
+        uint64_t* bar_k = &sh.k_full[(kt + 1) % K4::kStagesK];
+        const uint32_t ph_v = (kt / K4::kStagesV) & 1, ph_k = ((kt + 1) / K4::kStagesK) & 1;
+        const uint32_t ph_p = (tcount[x] + j) & 1, ph_o = (ucount[x] - 1) & 1;
+        const bool ready = test(&sh.p_full[x], ph_p) & (!need_v || test(bar_v, ph_v)) &
+                           (!need_o || test(&sh.o_free[x], ph_o)) & (!need_k || test(bar_k, ph_k));
+        if (!ready && (!relaxed(&sh.p_full[x], ph_p) || (need_v && !relaxed(bar_v, ph_v)) ||
+                       (need_o && !relaxed(&sh.o_free[x], ph_o)) ||
+                       (need_k && !relaxed(bar_k, ph_k)))) {
           ok = false;
           break;
         }
@@ -344,12 +380,81 @@ __device__ void mma_issuer4(const AttnArgs& a, Kv4Shared& sh, uint32_t tmem, uin
   }
 }
 
-// Softmax and epilogue of tile x (0 = A, 1 = B); thread t = row t of the tile = TMEM lane t.  The
-// reference and its rescaling are those of the ordinary launch (attn_prefill_tc.cu).
+// Columns of a tile that a softmax thread takes at a time.
+constexpr int kCols = 32;
+// Largest sum of their exponents: P stays below 2^15 in fp16.
+constexpr float kSumLimit = 32768.f;
+
+__device__ __forceinline__ void load_scores(uint32_t at, float (&s)[kCols]) {
+#pragma unroll
+  for (int c = 0; c < kCols / 32; ++c)
+    tc::ld32(at + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
+  tc::wait_ld();
+}
+__device__ __forceinline__ void store_weights(uint32_t at, const uint32_t (&p)[kCols / 2]) {
+#pragma unroll
+  for (int c = 0; c < kCols / 32; ++c)
+    tc::st16(at + 16 * c, *reinterpret_cast<const uint32_t(*)[16]>(p + 16 * c));
+}
+
+// A warp's rows take a new reference where their scores of columns [c0, c0 + kCols) exceed the old
+// one: O (if it holds anything), the sum and the row's P of the columns before move by a power of
+// two.  Out of line: rare, but for a row's first columns.
+template <int HD>
+__device__ __noinline__ void move_reference(uint32_t col_s, uint32_t col_o, int c0, int seen,
+                                            float scale, bool has_o, float* m_ref, float* l) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < kCols; c += 16) {
+    uint32_t r[16];
+    tc::ld16(col_s + c0 + c, r);
+    tc::wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float v = __uint_as_float(r[i]);
+      top = c0 + c + i < seen ? fmaxf(top, v) : top;
+    }
+  }
+  const float old = *m_ref, next = fmaxf(old, ceilf(top * scale));
+  const float alpha = next > old ? fast_exp2(old - next) : 1.f;
+  if (has_o) {  // O holds the tiles before: S of this one, issued after them, has landed
+#pragma unroll 1
+    for (int c = 0; c < HD; c += 16) {
+      uint32_t r[16];
+      tc::ld16(col_o + c, r);
+      tc::wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+      tc::st16(col_o + c, r);
+    }
+  }
+#pragma unroll 1
+  for (int c = 0; c < c0 / 2; c += 16) {
+    uint32_t r[16];
+    tc::wait_st();
+    tc::ld16(col_s + c, r);
+    tc::wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {  // (fp32: alpha itself may be below fp16's range)
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
+      r[i] = kv4d::pack_f16x2(v.x * alpha, v.y * alpha);
+    }
+    tc::st16(col_s + c, r);
+  }
+  tc::wait_st();
+  *l *= alpha;
+  *m_ref = next;
+}
+
+// Softmax and epilogue of tile x (0 = A, 1 = B); thread t = row t of the tile = TMEM lane t.
+// Exponents are taken against a reference that lags the row's maximum, as in the ordinary launch
+// (attn_prefill_tc.cu), but kCols columns at a time in a rolled loop, P going over columns that are
+// read already.
 template <int HD>
 __device__ void softmax_kv4(const Kv4Args& g4, Kv4Shared& sh, uint32_t tmem, uint8_t* smem_ptr,
                             int x) {
   using C = TcCfg<HD>;
+  using K4 = Kv4Cfg<HD>;
   const AttnArgs& a = g4.a;
   volatile int* abort = &sh.abort;
   const int t = threadIdx.x & 127;
@@ -387,7 +492,7 @@ __device__ void softmax_kv4(const Kv4Args& g4, Kv4Shared& sh, uint32_t tmem, uin
     float scale = a.scale_log2;
     if (n > 0) {  // this row of Q to fp16, in place
       if (!wait_all(&sh.q_full[x], uc_x & 1)) break;
-      uint8_t* row = smem_ptr + C::kQOffset + x * C::kQBytes + t * 128;
+      uint8_t* row = smem_ptr + K4::kQOffset + x * C::kQBytes + t * 128;
       uint4 w[HD / 8];
       float top = 0.f;
 #pragma unroll
@@ -416,129 +521,83 @@ __device__ void softmax_kv4(const Kv4Args& g4, Kv4Shared& sh, uint32_t tmem, uin
       fence_proxy_async_smem();
       arrive_warp(&sh.q_ready[x]);
     }
-    // running reference (log2 domain) and sum; a row without a query starts at 0
+    // running reference (log2 units, a whole number) and sum; a row without a query starts at 0
     float m_ref = valid ? -INFINITY : 0.f, l = 0.f;
     for (int j = 0; j < n; ++j) {
       const uint32_t tj = tc_x + j;
       if (!wait_all(&sh.s_full[x], tj & 1)) { ok = false; break; }
       if (releases && t == 0) {
         const uint32_t kt = itk + j;
-        tc::mbar_arrive(&sh.k_empty[kt % C::kStagesK]);
-        if (j > 0) tc::mbar_arrive(&sh.v_empty[(kt - 1) % C::kStagesV]);
+        tc::mbar_arrive(&sh.k_empty[kt % K4::kStagesK]);
+        if (j > 0) tc::mbar_arrive(&sh.v_empty[(kt - 1) % K4::kStagesV]);
         if (j + 1 == n) tc::mbar_arrive(&sh.q_empty);
       }
       tc::fence_after_sync();
-      float s[128];
-      {
-        uint32_t r0[32], r1[32], r2[32], r3[32];
-        tc::ld32(col_s + 0, r0);
-        tc::ld32(col_s + 32, r1);
-        tc::ld32(col_s + 64, r2);
-        tc::ld32(col_s + 96, r3);
-        tc::wait_ld();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          s[i] = __uint_as_float(r0[i]);
-          s[32 + i] = __uint_as_float(r1[i]);
-          s[64 + i] = __uint_as_float(r2[i]);
-          s[96 + i] = __uint_as_float(r3[i]);
-        }
-      }
       const int kv_base = j * C::kN;
-      if (partial || kv_base + C::kN - 1 > lim_min) {
+      const bool masked = partial || kv_base + C::kN - 1 > lim_min;
+      // keys of the tile that this row sees
+      const int seen = masked ? lim + 1 - kv_base : C::kN;
+      const float2 sc2 = make_float2(scale, scale);
+#pragma unroll 1
+      for (int c0 = 0; c0 < C::kN; c0 += kCols) {
+        float s[kCols];
+        load_scores(col_s + c0, s);
+        if (masked) {
 #pragma unroll
-        for (int i = 0; i < 128; ++i) s[i] = (kv_base + i <= lim) ? s[i] : -INFINITY;
-      }
-      auto take_tile_max = [&]() {
-        float mx[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mx[i] = fmax3(s[i], s[8 + i], s[16 + i]);
-#pragma unroll
-        for (int g = 3; g + 1 < 16; g += 2)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) mx[i] = fmax3(mx[i], s[8 * g + i], s[8 * g + 8 + i]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mx[i] = fmaxf(mx[i], s[120 + i]);
-        const float m_tile = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
-                                   fmaxf(mx[6], mx[7])) *
-                             scale;
-        const bool need = m_tile > m_ref;
-        if (__any_sync(0xffffffffu, need)) {
-          const float m_new = need ? m_tile : m_ref;
-          const float alpha = fast_exp2(m_ref - m_new);
-          if (j > 0) {  // O holds P_{j-1} V_{j-1}: S_j, issued after it, has landed
-            uint32_t r[32];
-#pragma unroll
-            for (int c = 0; c < HD / 32; ++c) {
-              tc::ld32(col_o + c * 32, r);
-              tc::wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-              tc::st32(col_o + c * 32, r);
-            }
-            tc::wait_st();
-          }
-          l *= alpha;
-          m_ref = m_new;
+          for (int i = 0; i < kCols; ++i) s[i] = c0 + i < seen ? s[i] : -INFINITY;
         }
-      };
-      if (__any_sync(0xffffffffu, m_ref == -INFINITY)) take_tile_max();
-      // exponents and the row sum two columns at a time; P (fp16) goes over the S columns
-      auto exponents = [&]() -> float {
-        const float mu = m_ref == -INFINITY ? 0.f : m_ref - kPShift;
-        const float2 sc2 = make_float2(scale, scale), nmu2 = make_float2(-mu, -mu);
-        float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                        make_float2(0.f, 0.f)};
+        uint32_t pk[kCols / 2];
+        auto exponents = [&]() -> float {
+          const float mu = m_ref == -INFINITY ? 0.f : m_ref - kPShift;
+          const float2 nmu2 = make_float2(-mu, -mu);
+          float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 e = __ffma2_rn(make_float2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]),
-                                        sc2, nmu2);
+          for (int i = 0; i < kCols / 2; ++i) {
+            const float2 e = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), sc2, nmu2);
             const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-            rs[i & 3] = __fadd2_rn(rs[i & 3], p);
+            rs[i & 1] = __fadd2_rn(rs[i & 1], p);
             pk[i] = kv4d::pack_f16x2(p.x, p.y);
           }
-          tc::st16(col_s + c * 16, pk);
+          const float2 r = __fadd2_rn(rs[0], rs[1]);
+          return r.x + r.y;
+        };
+        float sum = exponents();
+        // the row's first columns, and any that exceed the reference by too much
+        if (__any_sync(0xffffffffu, !(sum <= kSumLimit) || m_ref == -INFINITY)) {
+          move_reference<HD>(col_s, col_o, c0, seen, scale, j > 0, &m_ref, &l);
+          sum = exponents();
         }
-        const float2 rs01 = __fadd2_rn(rs[0], rs[1]), rs23 = __fadd2_rn(rs[2], rs[3]);
-        const float2 rsum = __fadd2_rn(rs01, rs23);
-        return rsum.x + rsum.y;
-      };
-      float rsum = exponents();
-      if (__any_sync(0xffffffffu, !(rsum <= kSumLimit))) {  // rare: re-reference this tile
-        tc::wait_st();
-        take_tile_max();
-        rsum = exponents();
+        l += sum;
+        store_weights(col_s + c0 / 2, pk);
       }
       tc::wait_st();
       tc::fence_before_sync();
       arrive_warp(&sh.p_full[x]);
-      l += rsum;
     }
     if (!ok) break;
     const uint32_t kt_last = itk + un.n_kt - 1;
     itk += un.n_kt;
     if (n > 0) {
       if (!wait_all(&sh.o_done[x], uc_x & 1)) break;  // the unit's last P V is in O
-      if (releases && t == 0) tc::mbar_arrive(&sh.v_empty[kt_last % C::kStagesV]);
+      if (releases && t == 0) tc::mbar_arrive(&sh.v_empty[kt_last % K4::kStagesV]);
       ++uc_x;
       tc_x += n;
       tc::fence_after_sync();
-      uint32_t o[HD];
+      const float wa = l > 0.f ? g4.v_scale / l : l * 0.f;  // (NaN stays NaN)
+      uint32_t pk[HD / 2];
 #pragma unroll
-      for (int c = 0; c < HD / 32; ++c)
-        tc::ld32(col_o + c * 32, *reinterpret_cast<uint32_t(*)[32]>(o + c * 32));
-      tc::wait_ld();
+      for (int c = 0; c < HD / 32; ++c) {
+        uint32_t o[32];
+        tc::ld32(col_o + c * 32, o);
+        tc::wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          pk[16 * c + i] =
+              pack_bf16x2(__uint_as_float(o[2 * i]) * wa, __uint_as_float(o[2 * i + 1]) * wa);
+      }
       tc::fence_before_sync();
       arrive_warp(&sh.o_free[x]);
       if (valid) {
-        const float wa = l > 0.f ? g4.v_scale / l : l * 0.f;  // (NaN stays NaN)
-        uint32_t pk[HD / 2];
-#pragma unroll
-        for (int i = 0; i < HD / 2; ++i)
-          pk[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * wa, __uint_as_float(o[2 * i + 1]) * wa);
         __nv_bfloat16* dst =
             a.out + (static_cast<size_t>(un.t0 + jt) * a.nh + un.h * a.group + hh) * HD;
         if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
@@ -557,10 +616,20 @@ __device__ void softmax_kv4(const Kv4Args& g4, Kv4Shared& sh, uint32_t tmem, uin
   }
 }
 
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <int HD>
-__global__ void __launch_bounds__(TcCfg<HD>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     attn_kv4_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ Kv4Args g4) {
   using C = TcCfg<HD>;
+  using K4 = Kv4Cfg<HD>;
   const AttnArgs& a = g4.a;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Kv4Shared sh;
@@ -572,15 +641,15 @@ __global__ void __launch_bounds__(TcCfg<HD>::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < C::kRing; ++i) {
       mbar_init(&sh.unit_full[i], 1);
-      mbar_init(&sh.unit_empty[i], 1 + 8 + 1);  // issuer, one lane of each softmax warp, V
+      mbar_init(&sh.unit_empty[i], 1 + 8 + 4 + 1);  // issuer; softmax, turning, copying warps
     }
     mbar_init(&sh.q_empty, 1);
-    for (int i = 0; i < C::kStagesK; ++i) {
-      mbar_init(&sh.k_full[i], 1);
+    for (int i = 0; i < K4::kStagesK; ++i) {
+      mbar_init(&sh.k_full[i], 2);
       mbar_init(&sh.k_empty[i], 1);
     }
-    for (int i = 0; i < C::kStagesV; ++i) {
-      mbar_init(&sh.v_full[i], 1);
+    for (int i = 0; i < K4::kStagesV; ++i) {
+      mbar_init(&sh.v_full[i], 2);
       mbar_init(&sh.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -591,6 +660,11 @@ __global__ void __launch_bounds__(TcCfg<HD>::kThreads, 1)
       mbar_init(&sh.o_done[i], 1);
       mbar_init(&sh.o_free[i], 4);
     }
+    for (int w = 0; w < 2; ++w)
+      for (int i = 0; i < kRawSlots; ++i) {
+        mbar_init(&sh.raw_full[w][i], 1);
+        mbar_init(&sh.raw_empty[w][i], 2);
+      }
     mbar_init(&sh.drain, 1);
     sh.abort = 0;
     sh.role_rank = atomicAdd(a.header + kHRoleNext, 1);
@@ -606,36 +680,47 @@ __global__ void __launch_bounds__(TcCfg<HD>::kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = sh.tmem_base;
 
-  // the planner's kind of work first, then the other; each register class in a loop of its own
+  // A CTA that the planner gave decode units first takes those until there are none; every CTA
+  // then takes prefill units, and decode units again while there are any.
   const bool decode_first = sh.decode_first != 0;
-  auto phase_end = [] {
+#pragma unroll 1
+  for (int phase = 0; phase < 2; ++phase) {
+    if (phase == 1 || decode_first)
+      decode_warp_kv4<HD>(g4, base_ptr + warp * kv4d::Ring<HD>::kWarpBytes,
+                          phase == 0 ? sh.role_rank * a.decode_warps_per_cta + warp : -1);
+    if (phase == 1) break;
+    fence_proxy_async_smem();  // the rings' ordinary accesses before the tiles' asynchronous ones
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-  };
-  if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kControlRegs));
-    for (int phase = 0; phase < 2; ++phase) {
-      if ((phase == 0) != decode_first) {
-        if (warp == C::kProducerWarp) {
-          producer_qk4<HD>(g4, sh, base, base_ptr, &qmap);
-        } else if (warp == C::kProducerVWarp) {
-          producer_v4<HD>(g4, sh, base_ptr);
-        } else if (warp == C::kMmaWarp) {
-          if ((tid & 31) == 0) mma_issuer4<HD>(a, sh, tmem, base);
-        }
+    if (warp < kSoftmaxWarp) {
+      fewer_registers<kControlRegs>();
+      if (warp == C::kMmaWarp) {
+        if ((tid & 31) == 0) mma_issuer4<HD>(a, sh, tmem, base);
+        __syncwarp();
+      } else if (warp == 1) {
+        producer_q4<HD>(a, sh, base, &qmap);
+      } else if (warp == 2) {
+        producer_raw<HD>(g4, sh, base + K4::kRawOffset);
+      } else if (warp == kTurnWarp || warp == kTurnWarp + 1) {
+        turn_tiles<HD, false, K4::kStagesK>(a, sh, base_ptr, base_ptr + K4::kRawOffset, sh.k_full,
+                                            sh.k_empty);
+      } else if (warp > kTurnWarp) {
+        turn_tiles<HD, true, K4::kStagesV>(a, sh, base_ptr + K4::kVOffset,
+                                           base_ptr + K4::kRawOffset, sh.v_full, sh.v_empty);
       }
-      phase_end();
-    }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
-    for (int phase = 0; phase < 2; ++phase) {
-      if ((phase == 0) == decode_first)
-        decode_warp_kv4<HD>(g4, decode_first ? sh.role_rank * a.decode_warps_per_cta + warp - 4
-                                             : -1);
-      else
-        softmax_kv4<HD>(g4, sh, tmem, base_ptr, (warp >> 2) - 1);
-      phase_end();
+      __syncwarp();
+      tc::fence_before_sync();
+      __syncthreads();
+      tc::fence_after_sync();
+      more_registers<kLaunchRegs>();
+    } else {
+      more_registers<kSoftmaxRegs>();
+      softmax_kv4<HD>(g4, sh, tmem, base_ptr, (warp - kSoftmaxWarp) >> 2);
+      fewer_registers<kLaunchRegs>();
+      tc::fence_before_sync();
+      __syncthreads();
+      tc::fence_after_sync();
     }
   }
   if (warp == C::kMmaWarp) {
@@ -647,16 +732,17 @@ __global__ void __launch_bounds__(TcCfg<HD>::kThreads, 1)
 template <int HD>
 rb_status launch_kv4(const Kv4Args& g4, const CUtensorMap& qmap, cudaStream_t s) {
   using C = TcCfg<HD>;
+  using K4 = Kv4Cfg<HD>;
   static bool configured[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return RB_ERR_CUDA;
   if (!configured[dev]) {
     if (cudaFuncSetAttribute(attn_kv4_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::kSmemBytes) != cudaSuccess)
+                             K4::kSmemBytes) != cudaSuccess)
       return RB_ERR_CUDA;
     configured[dev] = true;
   }
-  attn_kv4_kernel<HD><<<max(1, device_sm_count()), C::kThreads, C::kSmemBytes, s>>>(qmap, g4);
+  attn_kv4_kernel<HD><<<max(1, device_sm_count()), kThreads, K4::kSmemBytes, s>>>(qmap, g4);
   if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
   note_launches(1);
   return RB_OK;
@@ -687,6 +773,7 @@ extern "C" rb_status rb_paged_attention_kv4(
       !(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(scale) || !(scale > 0.f))
     return RB_ERR_INVALID_ARG;
   a.scale_log2 = scale;
+  a.decode_warps_per_cta = kWarps;
   if (a.N_pad > 0 &&
       !encode_q_tensor_map(&su.qmap, a.q, su.head_dim, a.nh, a.N_pad, a.group))
     return RB_ERR_CUDA;

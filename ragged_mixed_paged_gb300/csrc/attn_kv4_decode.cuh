@@ -8,10 +8,11 @@
 // exact in fp16 (two bits of a code times four of a scale, between 2^-10 and 2880), so K and V enter
 // the MMAs unrounded; Q is divided by a power of two per column, which keeps its 8 bits.
 //
-// A page of one kv head is 9 hd contiguous bytes of K and as many of V.  They go from memory to
-// the registers of the lane whose MMA operand they are, without shared memory: the MMA does not
-// mind which 16 values of head_dim (K) or which dims and keys (V) a step takes, as long as both operands
-// agree, so the order is chosen to make a lane's bytes neighbours.  With g = lane / 4, t = lane % 4:
+// A page of one kv head is 9 hd contiguous bytes of K and as many of V.  A warp copies them to its
+// own ring in shared memory with 16-byte cp.async, kStages pages ahead, and each lane then reads the
+// bytes that are its MMA operands.  The MMA does not mind which 16 values of head_dim (K) or
+// which dims and keys (V) a step takes, as long as both operands agree, so the order is chosen to
+// make a lane's bytes neighbours.  With g = lane / 4, t = lane % 4:
 //   K  rows g and g + 8 of the MMA are keys kg = 4 (g / 2) + g % 2 and kg + 2; lane (g, t) holds
 //      values [t hd / 4, (t + 1) hd / 4) of both, and step s takes its s-th four values;
 //   V  row g of step s is dim (hd / 8) g + 2 s and row g + 8 the next one; the lane holds the hd / 8
@@ -19,7 +20,9 @@
 //      shifts and masks for a word of eight: neighbouring codes then belong to neighbouring keys.
 // A lane so ends up with hd / 8 neighbouring values of two columns of the output.
 //
-// Two pages a step, the next two steps' bytes on their way in registers (kDepth).
+// What bounds it: the codes' conversions.  A page costs 64 of them per lane (hd 128), two cycles
+// each on the pipe that also takes masks, shifts and comparisons, about 285 cycles a page of
+// 2304 bytes in all, where HBM delivers one to a quarter SM in 390.
 #pragma once
 
 #include "attn_decode_warp.cuh"
@@ -76,60 +79,78 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One lane's bytes of a page of one kv head.
+// Geometry of a warp's ring: pages as they lie in the cache, but for the order of rows (and, in
+// rows of 64 bytes, of 16-byte chunks), which keeps the lanes' reads free of bank conflicts.
+//   K: the lanes' first rows, in order of g, then their second ones: lane's bytes at lane x hd / 8
+//   V: row 4t + i at t + 4i; chunk c of it at c ^ 2 for t >= 2 (hd 128)
 template <int HD>
-struct Page {
-  static constexpr int kWords = HD / 32;  // words of eight codes per K row; V words per key: half
-  uint32_t k[2][kWords];
-  uint32_t v[4][kWords / 2];
-  uint32_t ks[2], vs;
+struct Ring {
+  static constexpr int kStages = 4;              // pages
+  static constexpr int kBytes = 9 * HD;          // K or V of a page
+  static constexpr int kStageBytes = 2 * kBytes;
+  static constexpr int kWarpBytes = kStages * kStageBytes;
+  static constexpr int kRow = HD / 2;            // bytes of codes of a row
+  static constexpr int kCopies = (kBytes / 16 + 31) / 32;
 };
 
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&r)[N], const uint8_t* p) {
+__device__ __forceinline__ void copies_wait() {  // all but the last N groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Where chunk i of a page of K (V) goes in its stage.
+template <int HD, bool kValues>
+__device__ __forceinline__ int chunk_at(int i) {
+  constexpr int kPerRow = HD / 32;  // chunks of codes of a row
+  if (i >= 8 * HD / 16) return i * 16;  // scales stay where they are
+  const int r = i / kPerRow, c = i % kPerRow;
+  if (kValues) return ((r >> 2) + 4 * (r & 3)) * (HD / 2) + ((HD == 128 ? c ^ ((r >> 3) * 2) : c) << 4);
+  return (((r >> 2) * 2 + (r & 1)) + 8 * ((r >> 1) & 1)) * (HD / 2) + (c << 4);
+}
+
+template <int N>
+__device__ __forceinline__ void read_words(uint32_t (&r)[N], const uint8_t* p) {
   if constexpr (N == 4) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
     r[0] = w.x; r[1] = w.y; r[2] = w.z; r[3] = w.w;
   } else if constexpr (N == 2) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
     r[0] = w.x; r[1] = w.y;
   } else {
-    r[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    r[0] = *reinterpret_cast<const uint32_t*>(p);
   }
 }
 
-// `k` and `v`: this lane's first bytes (codes of its first K row; codes of its first V key).
+// S^T of the page whose K is at `k`: two chains of MMAs.
 template <int HD>
-__device__ __forceinline__ void load_page(Page<HD>& p, const uint8_t* k, const uint8_t* v,
-                                          int k_scale_at, int v_scale_at) {
-  load_words(p.k[0], k);
-  load_words(p.k[1], k + 2 * (HD / 2));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) load_words(p.v[i], v + i * (HD / 2));
-  if constexpr (HD == 128) {
-    p.ks[0] = __ldg(reinterpret_cast<const uint16_t*>(k + k_scale_at));
-    p.ks[1] = __ldg(reinterpret_cast<const uint16_t*>(k + k_scale_at + 2 * (HD / 16)));
-  } else {
-    p.ks[0] = __ldg(k + k_scale_at);
-    p.ks[1] = __ldg(k + k_scale_at + 2 * (HD / 16));
-  }
-  p.vs = __ldg(reinterpret_cast<const uint32_t*>(v + v_scale_at));
-}
-
-// S^T of a page: two chains of MMAs.
-template <int HD>
-__device__ __forceinline__ void scores(const Page<HD>& p, const uint32_t (&bq)[HD / 16][2],
+__device__ __forceinline__ void scores(const uint8_t* k, int lane, const uint32_t (&bq)[HD / 16][2],
                                        float (&s)[4]) {
+  const int g = lane >> 2, t = lane & 3, key_g = 4 * (g >> 1) + (g & 1);
   float s2[4] = {0.f, 0.f, 0.f, 0.f};
   s[0] = s[1] = s[2] = s[3] = 0.f;
-  const uint32_t sc0 = scales2(p.ks[0]), sc1 = scales2(p.ks[1]);
+  uint32_t c0[HD / 32], c1[HD / 32];
+  read_words(c0, k + lane * (HD / 8));
+  read_words(c1, k + 4 * HD + lane * (HD / 8));
+  const uint8_t* sp = k + 8 * HD + key_g * (HD / 16) + t * (HD / 64);
+  uint32_t sc0, sc1;
+  if constexpr (HD == 128) {
+    sc0 = scales2(*reinterpret_cast<const uint16_t*>(sp));
+    sc1 = scales2(*reinterpret_cast<const uint16_t*>(sp + 2 * (HD / 16)));
+  } else {
+    sc0 = scales2(*sp);
+    sc1 = scales2(*(sp + 2 * (HD / 16)));
+  }
 #pragma unroll
   for (int w = 0; w < HD / 32; ++w) {
     // (a lane's HD / 4 values are one block of 16 for HD 64, two for 128)
     const uint32_t m0 = w < 2 ? low2(sc0) : high2(sc0), m1 = w < 2 ? low2(sc1) : high2(sc1);
     uint32_t x[4], y[4];
-    kv4::values8(p.k[0][w], x);
-    kv4::values8(p.k[1][w], y);
+    kv4::values8(c0[w], x);
+    kv4::values8(c1[w], y);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[i] = hmul2(x[i], m0);
@@ -142,21 +163,29 @@ __device__ __forceinline__ void scores(const Page<HD>& p, const uint32_t (&bq)[H
   for (int i = 0; i < 4; ++i) s[i] += s2[i];
 }
 
-// O^T += V^T P^T of a page.
+// O^T += V^T P^T of the page whose V is at `v`.
 template <int HD>
-__device__ __forceinline__ void add_values(const Page<HD>& p, uint32_t pb0, uint32_t pb1,
+__device__ __forceinline__ void add_values(const uint8_t* v, int lane, uint32_t pb0, uint32_t pb1,
                                            float (&acc)[HD / 16][4]) {
-  const uint32_t s01 = scales2(p.vs), s23 = scales2(p.vs >> 16);
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t sv = *reinterpret_cast<const uint32_t*>(
+      v + 8 * HD + (g * (HD / 8) / 16) * 16 + 4 * t);
+  const uint32_t s01 = scales2(sv), s23 = scales2(sv >> 16);
+  uint32_t c[4][HD / 64];
+  const int chunk = g * (HD / 16) / 16, in = g * (HD / 16) % 16;
+  const uint8_t* p = v + t * (HD / 2) + ((HD == 128 ? chunk ^ ((t >> 1) * 2) : chunk) << 4) + in;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) read_words(c[i], p + 4 * i * (HD / 2));
 #pragma unroll
   for (int w = 0; w < HD / 64; ++w) {
     // even and odd dims of a word, the first key of a pair in the low half of each byte
     auto even = [](uint32_t x, uint32_t y) { return (x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u); };
     auto odd = [](uint32_t x, uint32_t y) { return ((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u); };
     uint32_t e01[4], o01[4], e23[4], o23[4];
-    kv4::values8(even(p.v[0][w], p.v[1][w]), e01);
-    kv4::values8(odd(p.v[0][w], p.v[1][w]), o01);
-    kv4::values8(even(p.v[2][w], p.v[3][w]), e23);
-    kv4::values8(odd(p.v[2][w], p.v[3][w]), o23);
+    kv4::values8(even(c[0][w], c[1][w]), e01);
+    kv4::values8(odd(c[0][w], c[1][w]), o01);
+    kv4::values8(even(c[2][w], c[3][w]), e23);
+    kv4::values8(odd(c[2][w], c[3][w]), o23);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       mma_f16(acc[4 * w + i], hmul2(e01[i], s01), hmul2(o01[i], s01), hmul2(e23[i], s23),
@@ -167,23 +196,25 @@ __device__ __forceinline__ void add_values(const Page<HD>& p, uint32_t pb0, uint
 }  // namespace kv4d
 
 // One decode warp: pulls (request, kv head, split) units from the shared counter until none
-// are left; `first_unit` >= 0: its first unit, handed out statically.
+// are left; `ring` is its kv4d::Ring in shared memory, `first_unit` >= 0 its first unit, handed out
+// statically.
 template <int HD>
-__device__ void decode_warp_kv4(const Kv4Args& g4, int first_unit) {
+__device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int first_unit) {
   using namespace kv4d;
   const AttnArgs& a = g4.a;
   constexpr int kKS = HD / 16, kPer = HD / 8;  // MMA steps; output values of a lane and column
-  constexpr int kPages = 2;                    // pages a step
-  constexpr int kDepth = 2;                    // steps in registers
+  using R = Ring<HD>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int n_units = a.header[kHNumDecodeUnits];
   const int sp = a.header[kHSplitPages];
   const int key_g = 4 * (g >> 1) + (g & 1);  // key of the lane's first K row
-  // byte offsets of the lane in a page: K codes and scales, V codes and scales
-  const int k_at = key_g * (HD / 2) + t * (HD / 8);
-  const int k_scale_at = 8 * HD + key_g * (HD / 16) + t * (HD / 64) - k_at;
-  const int v_at = 4 * t * (HD / 2) + g * (HD / 16);
-  const int v_scale_at = 8 * HD + (g * (HD / 8) / 16) * 16 + 4 * t - v_at;
+  const uint32_t ring_at = smem_u32(ring);
+  int k_to[R::kCopies], v_to[R::kCopies];  // where this lane's chunks go in a stage
+#pragma unroll
+  for (int i = 0; i < R::kCopies; ++i) {
+    k_to[i] = chunk_at<HD, false>(lane + 32 * i);
+    v_to[i] = R::kBytes + chunk_at<HD, true>(lane + 32 * i);
+  }
   int next_static = first_unit;
   while (true) {
     int u = next_static;
@@ -213,22 +244,28 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, int first_unit) {
       return id < 0 ? a.null_block : id;
     };
     int bid = page(lane), bid_next = page(32 + lane);
-    Page<HD> buf[kDepth][kPages] = {};  // (a step's missing second page: any finite values)
-    auto load = [&](Page<HD>& dst, int i) {  // pages in order; past the last one nothing
-      if (i >= n_pages) return;
-      if (i - win >= 32) {
-        win += 32;
-        bid = bid_next;
-        bid_next = page(win + 32 + lane);
+    auto load = [&](int i) {  // pages in order; past the last one an empty group
+      if (i < n_pages) {
+        if (i - win >= 32) {
+          win += 32;
+          bid = bid_next;
+          bid_next = page(win + 32 + lane);
+        }
+        const int id = __shfl_sync(0xffffffffu, bid, i - win);
+        const size_t at = (static_cast<size_t>(id) * a.nkv + h) * kv4::page_bytes(HD) + lane * 16;
+        const uint32_t to = ring_at + (i % R::kStages) * R::kStageBytes;
+#pragma unroll
+        for (int c = 0; c < R::kCopies; ++c) {
+          if ((c + 1) * 32 <= R::kBytes / 16 || lane < R::kBytes / 16 - c * 32) {
+            copy16(to + k_to[c], g4.k + at + c * 512);
+            copy16(to + v_to[c], g4.v + at + c * 512);
+          }
+        }
       }
-      const int id = __shfl_sync(0xffffffffu, bid, i - win);
-      const size_t at = (static_cast<size_t>(id) * a.nkv + h) * kv4::page_bytes(HD);
-      load_page<HD>(dst, g4.k + at + k_at, g4.v + at + v_at, k_scale_at, v_scale_at);
+      copies_commit();
     };
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d)
-#pragma unroll
-      for (int p = 0; p < kPages; ++p) load(buf[d][p], d * kPages + p);
+    for (int i = 0; i < R::kStages - 1; ++i) load(i);
 
     // Q^T fragments: column g, values [t hd / 4, (t + 1) hd / 4) over 2^e
     uint32_t bq[kKS][2];
@@ -271,21 +308,25 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, int first_unit) {
 #pragma unroll
     for (int mt = 0; mt < kKS; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
 
-    auto step = [&](Page<HD> (&pg)[kPages], int i0) {
-      float x[kPages][4];
-      float g0 = -INFINITY, g1 = -INFINITY;
-#pragma unroll
-      for (int p = 0; p < kPages; ++p) {
-        scores<HD>(pg[p], bq, x[p]);
-        // keys past the end of the unit's pages (an odd last step) and of the column
-        const int key = i0 + p < n_pages ? (p_begin + i0 + p) * kPage + key_g : 0x7ffffff0;
-        x[p][0] = key <= lim0 ? x[p][0] * sc0 : -INFINITY;
-        x[p][1] = key <= lim1 ? x[p][1] * sc1 : -INFINITY;
-        x[p][2] = key + 2 <= lim0 ? x[p][2] * sc0 : -INFINITY;
-        x[p][3] = key + 2 <= lim1 ? x[p][3] * sc1 : -INFINITY;
-        g0 = fmax3(g0, x[p][0], x[p][2]);
-        g1 = fmax3(g1, x[p][1], x[p][3]);
+    for (int i = 0; i < n_pages; ++i) {
+      copies_wait<R::kStages - 2>();
+      __syncwarp();  // page i has landed for every lane, and every lane is done with page i - 1
+      load(i + R::kStages - 1);
+      const uint8_t* stage = ring + (i % R::kStages) * R::kStageBytes;
+      float x[4];
+      scores<HD>(stage, lane, bq, x);
+      const int key = (p_begin + i) * kPage + key_g;
+      x[0] *= sc0;
+      x[1] *= sc1;
+      x[2] *= sc0;
+      x[3] *= sc1;
+      if ((p_begin + i) * kPage + kPage - 1 > c) {  // (the columns' last keys are c and more)
+        x[0] = key <= lim0 ? x[0] : -INFINITY;
+        x[1] = key <= lim1 ? x[1] : -INFINITY;
+        x[2] = key + 2 <= lim0 ? x[2] : -INFINITY;
+        x[3] = key + 2 <= lim1 ? x[3] : -INFINITY;
       }
+      float g0 = fmaxf(x[0], x[2]), g1 = fmaxf(x[1], x[3]);
       // exponents against a reference that moves only when a score exceeds it by more than
       // kGrowth (log2 units), so that P stays below 2^(kPShift + kGrowth)
       constexpr float kGrowth = 8.f;
@@ -309,26 +350,15 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, int first_unit) {
       }
       const float ms0 = m0 == -INFINITY ? 0.f : m0 - kPShift;
       const float ms1 = m1 == -INFINITY ? 0.f : m1 - kPShift;
-#pragma unroll
-      for (int p = 0; p < kPages; ++p) {
-        const float e0 = fast_exp2(x[p][0] - ms0), e1 = fast_exp2(x[p][1] - ms1);
-        const float e2 = fast_exp2(x[p][2] - ms0), e3 = fast_exp2(x[p][3] - ms1);
-        l0 += e0 + e2;
-        l1 += e1 + e3;
-        add_values<HD>(pg[p], movmatrix_trans(pack_f16x2(e0, e1)),
-                       movmatrix_trans(pack_f16x2(e2, e3)), acc);
-      }
-    };
-    for (int i = 0; i < n_pages; i += kDepth * kPages) {
-#pragma unroll
-      for (int d = 0; d < kDepth; ++d) {
-        const int i0 = i + d * kPages;
-        if (i0 >= n_pages) break;
-        step(buf[d], i0);
-#pragma unroll
-        for (int p = 0; p < kPages; ++p) load(buf[d][p], i0 + kDepth * kPages + p);
-      }
+      const float e0 = fast_exp2(x[0] - ms0), e1 = fast_exp2(x[1] - ms1);
+      const float e2 = fast_exp2(x[2] - ms0), e3 = fast_exp2(x[3] - ms1);
+      l0 += e0 + e2;
+      l1 += e1 + e3;
+      add_values<HD>(stage + R::kBytes, lane, movmatrix_trans(pack_f16x2(e0, e1)),
+                     movmatrix_trans(pack_f16x2(e2, e3)), acc);
     }
+    copies_wait<0>();
+    __syncwarp();  // every lane is done with the ring
     if (bad) raise_error(a.err, RB_EBIT_BLOCK_ID);
 
 #pragma unroll
