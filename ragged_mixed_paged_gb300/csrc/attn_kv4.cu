@@ -3,11 +3,9 @@
 //
 //   o = softmax(scale * q . K) . V,  K = k_scale * s * c,  V = v_scale * s * c  (rb.h's format)
 //
-// The planner and the shape of the launch are the 16-bit cache's (attention.cu,
-// attn_prefill_tc.cu): one persistent launch in which every CTA runs decode units
-// (attn_kv4_decode.cuh) and prefill units, the kind the planner gave it first.
-//
-// Decode units take all 16 warps.  Prefill unit = (request, kv head, pair of 128-row query tiles):
+// A planner (attn_kv4_plan.cuh) and one persistent launch: the CTAs that the planner gives the decode
+// requests take their pages with all 16 warps (attn_kv4_decode.cuh), and every CTA takes prefill
+// units.  Prefill unit = (request, kv head, pair of 128-row query tiles):
 //   warp 0      one thread issues the MMAs: S = Q K^T (both K-major in shared memory), O += P V (P
 //               from TMEM, V MN-major), kind::f16 with fp16 operands;
 //   warp 1      takes units and loads Q (TMA);
@@ -22,7 +20,7 @@
 // memory traffic, against 512 multiply-adds of the tensor core.
 // Values behind the sequence's end are finite whatever a page holds, so their zero weights suffice.
 #include "attn_kv4_decode.cuh"
-#include "attn_plan.cuh"
+#include "attn_kv4_plan.cuh"
 #include "attn_prefill_tc.cuh"
 
 namespace rb {
@@ -33,10 +31,6 @@ using kv4d::hmul2;
 
 constexpr int kPlanThreads = 1024;
 
-__global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(AttnArgs a, int head_dim) {
-  plan_body<false>(a, head_dim, ReqSrc{a.qsl, a.seq_lens, nullptr});
-}
-
 // Threads and registers: launched with 128 for each of 512 threads, which the decode phases use; a
 // prefill phase gives the softmax warps 184 and the others 72.
 constexpr int kThreads = 512, kWarps = 16;
@@ -45,6 +39,11 @@ static_assert(256 * kSoftmaxRegs + 256 * kControlRegs <= kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr int kTurnWarp = 4, kSoftmaxWarp = 8;  // the first ones
 constexpr int kRawSlots = 3;                    // half tiles of the cache's bytes on their way
+
+__global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(AttnArgs a, int head_dim) {
+  grid_release();  // the attention launch sets itself up meanwhile
+  kv4_plan_body(a, head_dim, kWarps);
+}
 
 struct Kv4Shared {
   uint64_t unit_full[4], unit_empty[4];
@@ -56,8 +55,7 @@ struct Kv4Shared {
   TcUnit units[4];
   uint32_t tmem_base;
   int abort;
-  int decode_first;
-  int role_rank;
+  int role_rank;  // order in which the CTAs came: the first ones decode
 };
 
 __host__ __device__ constexpr uint32_t make_idesc_f16(int M, int N, bool b_mn_major) {
@@ -667,29 +665,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     mbar_init(&sh.drain, 1);
     sh.abort = 0;
-    sh.role_rank = atomicAdd(a.header + kHRoleNext, 1);
-    sh.decode_first = sh.role_rank < a.header[kHDecodeCtas];
     fence_barrier_init();
   }
   if (warp == C::kMmaWarp) {
     tc::tmem_alloc(&sh.tmem_base, C::kTmemCols);
     tc::tmem_relinquish();
   }
+  grid_wait();  // the planner's results
+  if (tid == 0) sh.role_rank = atomicAdd(a.header + kHRoleNext, 1);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = sh.tmem_base;
 
-  // A CTA that the planner gave decode units first takes those until there are none; every CTA
-  // then takes prefill units, and decode units again while there are any.
-  const bool decode_first = sh.decode_first != 0;
-#pragma unroll 1
-  for (int phase = 0; phase < 2; ++phase) {
-    if (phase == 1 || decode_first)
-      decode_warp_kv4<HD>(g4, base_ptr + warp * kv4d::Ring<HD>::kWarpBytes,
-                          phase == 0 ? sh.role_rank * a.decode_warps_per_cta + warp : -1);
-    if (phase == 1) break;
+  // The first CTAs take the decode requests' pages (the stream's warps spread over them); every CTA
+  // then takes prefill units.
+  const int decode_ctas = a.header[kHDecodeCtas];
+  if (sh.role_rank < decode_ctas) {
+    decode_warp_kv4<HD>(g4, base_ptr + warp * kv4d::Ring<HD>::kWarpBytes,
+                        warp * decode_ctas + sh.role_rank);
     fence_proxy_async_smem();  // the rings' ordinary accesses before the tiles' asynchronous ones
+  }
+  if (a.header[kHNumPrefillUnits] > 0) {
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -710,21 +707,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            base_ptr + K4::kRawOffset, sh.v_full, sh.v_empty);
       }
       __syncwarp();
-      tc::fence_before_sync();
-      __syncthreads();
-      tc::fence_after_sync();
-      more_registers<kLaunchRegs>();
     } else {
       more_registers<kSoftmaxRegs>();
       softmax_kv4<HD>(g4, sh, tmem, base_ptr, (warp - kSoftmaxWarp) >> 2);
-      fewer_registers<kLaunchRegs>();
-      tc::fence_before_sync();
-      __syncthreads();
-      tc::fence_after_sync();
     }
   }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
   if (warp == C::kMmaWarp) {
-    __syncwarp();
     tc::tmem_dealloc(tmem, C::kTmemCols);
   }
 }
@@ -742,10 +733,8 @@ rb_status launch_kv4(const Kv4Args& g4, const CUtensorMap& qmap, cudaStream_t s)
       return RB_ERR_CUDA;
     configured[dev] = true;
   }
-  attn_kv4_kernel<HD><<<max(1, device_sm_count()), kThreads, K4::kSmemBytes, s>>>(qmap, g4);
-  if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
-  note_launches(1);
-  return RB_OK;
+  return launch_overlapped(attn_kv4_kernel<HD>, max(1, device_sm_count()), kThreads,
+                           K4::kSmemBytes, s, qmap, g4);
 }
 
 }  // namespace
@@ -773,7 +762,6 @@ extern "C" rb_status rb_paged_attention_kv4(
       !(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(scale) || !(scale > 0.f))
     return RB_ERR_INVALID_ARG;
   a.scale_log2 = scale;
-  a.decode_warps_per_cta = kWarps;
   if (a.N_pad > 0 &&
       !encode_q_tensor_map(&su.qmap, a.q, su.head_dim, a.nh, a.N_pad, a.group))
     return RB_ERR_CUDA;

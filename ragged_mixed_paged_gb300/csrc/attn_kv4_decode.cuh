@@ -1,7 +1,8 @@
 // Split-KV decode warp of the attention over a 4-bit cache.  Not part of the C ABI.
 //
-// Work unit = (request, kv head, split of pages), one warp per unit, as in the 16-bit cache's
-// decode; the contraction runs transposed, a 16-token page per MMA tile:
+// All decode requests' pages form one stream, of which every warp takes an equal part (Stream); a
+// (request, kv head) whose pages end up with several warps is merged by the last one to finish.
+// The contraction runs transposed, a 16-token page per MMA tile:
 //   S^T[16 keys, 8 cols] = K[16, hd] . Q^T[hd, 8]     cols = (query token, head of the group)
 //   O^T[hd, 8 cols]     += V^T[hd, 16] . P^T[16, 8]
 // with mma.sync m16n8k16, fp16 in and fp32 accumulated.  Every value that the cache can hold is
@@ -195,78 +196,186 @@ __device__ __forceinline__ void add_values(const uint8_t* v, int lane, uint32_t 
 
 }  // namespace kv4d
 
-// One decode warp: pulls (request, kv head, split) units from the shared counter until none
-// are left; `ring` is its kv4d::Ring in shared memory, `first_unit` >= 0 its first unit, handed out
-// statically.
+// Log-sum-exp merge of the pieces of one (request, kv head) by one warp, kLanes lanes per column,
+// each lane owning that part of head_dim.  Piece 0 is the last one of its warp, the others are the
+// first of theirs.  Partials of other SMs are read through L2, 16 loads in flight.
+template <int HD, int kLanes>
+__device__ __forceinline__ void merge_pieces(const AttnArgs& a, int w0, int n, int h, int t0,
+                                             int cols) {
+  constexpr int kPer = HD / kLanes, kVec = kPer / 4, kBatch = 16 / kVec;
+  const int lane = threadIdx.x & 31;
+  const int col = lane / kLanes, part = lane % kLanes;
+  const bool active = col < cols;
+  const int c = active ? col : 0;
+  auto slot = [&](int i) { return static_cast<size_t>(i == 0 ? 2 * w0 + 1 : 2 * (w0 + i)); };
+  float mx = -INFINITY;
+#pragma unroll 2
+  for (int i = part; i < n; i += kLanes)
+    mx = fmaxf(mx, __ldcg(&a.part_ml[slot(i) * kMaxCols + c].x));
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (mx == -INFINITY) mx = 0.f;
+  float acc[kPer], sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += kBatch) {
+    float2 ml[kBatch];
+    float4 x[kBatch][kVec];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const size_t u = slot(min(i0 + k, n - 1)) * kMaxCols + c;
+      ml[k] = __ldcg(a.part_ml + u);
+#pragma unroll
+      for (int v = 0; v < kVec; ++v)
+        x[k][v] = __ldcg(reinterpret_cast<const float4*>(a.part_o + u * HD + part * kPer) + v);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (i0 + k >= n) break;
+      const float w = fast_exp2(ml[k].x - mx);
+      sum += w * ml[k].y;
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) {
+        acc[4 * v + 0] += w * x[k][v].x;
+        acc[4 * v + 1] += w * x[k][v].y;
+        acc[4 * v + 2] += w * x[k][v].z;
+        acc[4 * v + 3] += w * x[k][v].w;
+      }
+    }
+  }
+  if (!active) return;
+  const int j = col / a.group, hh = col - j * a.group;
+  const float inv = sum > 0.f ? 1.f / sum : sum * 0.f;  // (NaN stays NaN)
+  uint2* dst = reinterpret_cast<uint2*>(
+      a.out + (static_cast<size_t>(t0 + j) * a.nh + h * a.group + hh) * HD + part * kPer);
+#pragma unroll
+  for (int v = 0; v < kVec; ++v)
+    dst[v] = make_uint2(pack_bf16x2(acc[4 * v + 0] * inv, acc[4 * v + 1] * inv),
+                        pack_bf16x2(acc[4 * v + 2] * inv, acc[4 * v + 3] * inv));
+}
+
+// What the decode phase reads, as one stream of pages: requests in order, of each the kv heads, of
+// each the pages.  a.dec_off[r] counts the pages of one head of the decode requests before r.  Warp w
+// of W takes pages [T w / W, T (w + 1) / W) of the T, so all end together, and a warp's copies go
+// on across the ends of heads and requests.
+struct Stream {
+  long long total;
+  int warps;
+  __device__ Stream(const AttnArgs& a)
+      : total(static_cast<long long>(a.dec_off[a.R]) * a.nkv), warps(a.header[kHNumDecodeUnits]) {}
+  __device__ long long begin(int w) const { return total * w / warps; }
+  __device__ int warp_of(long long x) const {
+    return static_cast<int>(((x + 1) * warps - 1) / total);
+  }
+};
+// A place in the stream.
+struct Place {
+  int r, h, page, pages;
+  __device__ Place(const AttnArgs& a, long long x) {
+    r = warp_upper_bound_i32(a.dec_off, a.R + 1, static_cast<int>(x / a.nkv)) - 1;
+    const int off = a.dec_off[r];
+    pages = a.dec_off[r + 1] - off;
+    const long long local = x - static_cast<long long>(off) * a.nkv;
+    h = static_cast<int>(local / pages);
+    page = static_cast<int>(local - static_cast<long long>(h) * pages);
+  }
+  __device__ void head_end(const AttnArgs& a, bool more) {  // after the head's last page
+    page = 0;
+    if (++h < a.nkv || !more) return;
+    h = 0;
+    int off = a.dec_off[r + 1], next;
+    do {  // (more: there is a request with pages)
+      ++r;
+      next = a.dec_off[r + 1];
+    } while (next == off);
+    pages = next - off;
+  }
+};
+
+// One decode warp, w of the stream's; `ring` is its kv4d::Ring in shared memory.
 template <int HD>
-__device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int first_unit) {
+__device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int w) {
   using namespace kv4d;
+  using R = Ring<HD>;
   const AttnArgs& a = g4.a;
   constexpr int kKS = HD / 16, kPer = HD / 8;  // MMA steps; output values of a lane and column
-  using R = Ring<HD>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int n_units = a.header[kHNumDecodeUnits];
-  const int sp = a.header[kHSplitPages];
-  const int key_g = 4 * (g >> 1) + (g & 1);  // key of the lane's first K row
+  const Stream stream(a);
+  if (w >= stream.warps) return;
+  const long long x0 = stream.begin(w);
+  const int n = static_cast<int>(stream.begin(w + 1) - x0);
+  Place at(a, x0);  // of the next page to compute
+
+  // Copies: page ids of up to 32 pages of one head a window, one per lane, the next one prefetched.
+  Place from = at;  // of the first page after the prefetched window
+  int left = n;
+  bool bad = false;
+  struct Window {
+    int id, n, h;
+  };
+  auto window = [&]() {
+    Window x{0, min(32, min(from.pages - from.page, left)), from.h};
+    if (lane < x.n) {
+      x.id = kernel_page(a.block_table + static_cast<size_t>(from.r) * a.MB, from.page + lane,
+                         a.ratio, a.num_blocks, a.null_block);
+      if (x.id < 0) {
+        bad = true;
+        x.id = a.null_block;
+      }
+    }
+    left -= x.n;
+    from.page += x.n;
+    if (from.page == from.pages) from.head_end(a, left > 0);
+    return x;
+  };
+  Window now = window(), next = window();
+  int pos = 0, to_copy = n, copy_slot = 0;
   const uint32_t ring_at = smem_u32(ring);
+  const uint8_t* const k_src = g4.k + lane * 16;
+  const uint8_t* const v_src = g4.v + lane * 16;
+  const uint32_t page_stride = static_cast<uint32_t>(a.nkv) * kv4::page_bytes(HD);
   int k_to[R::kCopies], v_to[R::kCopies];  // where this lane's chunks go in a stage
 #pragma unroll
   for (int i = 0; i < R::kCopies; ++i) {
     k_to[i] = chunk_at<HD, false>(lane + 32 * i);
     v_to[i] = R::kBytes + chunk_at<HD, true>(lane + 32 * i);
   }
-  int next_static = first_unit;
-  while (true) {
-    int u = next_static;
-    if (u < 0) {
-      if (lane == 0) u = atomicAdd(a.header + kHDecodeNext, 1);
-      u = __shfl_sync(0xffffffffu, u, 0);
-    }
-    next_static = -1;
-    if (u >= n_units) break;
-    const int r = warp_upper_bound_i32(a.dec_off, a.R + 1, u) - 1;
-    const int first = a.dec_off[r];
-    const int nsplit = (a.dec_off[r + 1] - first) / a.nkv;
-    const int local = u - first;
-    const int split = local / a.nkv, h = local - split * a.nkv;
-    const int t0 = a.qsl[r], q = a.qsl[r + 1] - t0, L = a.seq_lens[r];
-    const int c = L - q, cols = q * a.group, pages = (L + kPage - 1) / kPage;
-    const int p_begin = split * sp, n_pages = min(p_begin + sp, pages) - p_begin;
-
-    // page ids of pages [win, win + 32) held one per lane, the next window prefetched
-    const int32_t* bt_row = a.block_table + static_cast<size_t>(r) * a.MB;
-    int win = 0;
-    bool bad = false;
-    auto page = [&](int i) {
-      if (i >= n_pages) return a.null_block;
-      const int id = kernel_page(bt_row, p_begin + i, a.ratio, a.num_blocks, a.null_block);
-      bad |= id < 0;
-      return id < 0 ? a.null_block : id;
-    };
-    int bid = page(lane), bid_next = page(32 + lane);
-    auto load = [&](int i) {  // pages in order; past the last one an empty group
-      if (i < n_pages) {
-        if (i - win >= 32) {
-          win += 32;
-          bid = bid_next;
-          bid_next = page(win + 32 + lane);
-        }
-        const int id = __shfl_sync(0xffffffffu, bid, i - win);
-        const size_t at = (static_cast<size_t>(id) * a.nkv + h) * kv4::page_bytes(HD) + lane * 16;
-        const uint32_t to = ring_at + (i % R::kStages) * R::kStageBytes;
+  auto copy = [&]() {  // the next page; past the last one an empty group
+    if (to_copy > 0) {
+      --to_copy;
+      if (pos == now.n) {
+        now = next;
+        pos = 0;
+        next = window();
+      }
+      const uint32_t id = __shfl_sync(0xffffffffu, now.id, pos++);
+      const size_t off = static_cast<size_t>(id) * page_stride + now.h * kv4::page_bytes(HD);
+      const uint32_t to = ring_at + copy_slot * R::kStageBytes;
+      const uint8_t *ks = k_src + off, *vs = v_src + off;
 #pragma unroll
-        for (int c = 0; c < R::kCopies; ++c) {
-          if ((c + 1) * 32 <= R::kBytes / 16 || lane < R::kBytes / 16 - c * 32) {
-            copy16(to + k_to[c], g4.k + at + c * 512);
-            copy16(to + v_to[c], g4.v + at + c * 512);
-          }
+      for (int c = 0; c < R::kCopies; ++c) {
+        if ((c + 1) * 32 <= R::kBytes / 16 || lane < R::kBytes / 16 - c * 32) {
+          copy16(to + k_to[c], ks + c * 512);
+          copy16(to + v_to[c], vs + c * 512);
         }
       }
-      copies_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < R::kStages - 1; ++i) load(i);
+      copy_slot = copy_slot + 1 == R::kStages ? 0 : copy_slot + 1;
+    }
+    copies_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < R::kStages - 1; ++i) copy();
 
+  const int key_g = 4 * (g >> 1) + (g & 1);  // key of the lane's first K row
+  int slot = 0;
+  for (int done = 0; done < n;) {  // segments: pages of one (request, kv head)
+    const int r = at.r, h = at.h, first = at.page, pages = at.pages;
+    const int seg = min(pages - first, n - done);
+    done += seg;
+    at.page += seg;
+    if (at.page == pages) at.head_end(a, done < n);
+    const int t0 = a.qsl[r], q = a.qsl[r + 1] - t0, c = a.seq_lens[r] - q, cols = q * a.group;
     // Q^T fragments: column g, values [t hd / 4, (t + 1) hd / 4) over 2^e
     uint32_t bq[kKS][2];
     float up;
@@ -276,26 +385,23 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int first_unit
       const int hh = valid ? g - j * a.group : 0;
       const uint4* qp = reinterpret_cast<const uint4*>(
           a.q + (static_cast<size_t>(t0 + j) * a.nh + h * a.group + hh) * HD + t * (HD / 4));
-      uint4 w[HD / 32];
+      uint4 word[HD / 32];
 #pragma unroll
-      for (int i = 0; i < HD / 32; ++i) w[i] = valid ? __ldg(qp + i) : make_uint4(0u, 0u, 0u, 0u);
-      float f[HD / 4], top = 0.f;
+      for (int i = 0; i < HD / 32; ++i) word[i] = valid ? __ldg(qp + i) : make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t* qw = reinterpret_cast<const uint32_t*>(word);
+      float top = 0.f;
 #pragma unroll
-      for (int i = 0; i < HD / 8; ++i) {
-        const uint32_t x = reinterpret_cast<const uint32_t*>(w)[i];
-        f[2 * i] = __uint_as_float(x << 16);
-        f[2 * i + 1] = __uint_as_float(x & 0xffff0000u);
-        top = fmax3(top, fabsf(f[2 * i]), fabsf(f[2 * i + 1]));
-      }
+      for (int i = 0; i < HD / 8; ++i)
+        top = fmax3(top, fabsf(__uint_as_float(qw[i] << 16)),
+                    fabsf(__uint_as_float(qw[i] & 0xffff0000u)));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       float down;
       power_of(top, &down, &up);
 #pragma unroll
-      for (int s = 0; s < kKS; ++s)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          bq[s][i] = pack_f16x2(f[4 * s + 2 * i] * down, f[4 * s + 2 * i + 1] * down);
+      for (int i = 0; i < HD / 8; ++i)
+        bq[i / 2][i % 2] = pack_f16x2(__uint_as_float(qw[i] << 16) * down,
+                                      __uint_as_float(qw[i] & 0xffff0000u) * down);
     }
     // the lane's columns of S^T: their scales and their last visible key
     const int c0 = 2 * t, c1 = c0 + 1;
@@ -307,29 +413,26 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int first_unit
     float acc[kKS][4];
 #pragma unroll
     for (int mt = 0; mt < kKS; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
-
-    for (int i = 0; i < n_pages; ++i) {
+#pragma unroll 1
+    for (int page = first; page < first + seg; ++page) {
       copies_wait<R::kStages - 2>();
-      __syncwarp();  // page i has landed for every lane, and every lane is done with page i - 1
-      load(i + R::kStages - 1);
-      const uint8_t* stage = ring + (i % R::kStages) * R::kStageBytes;
-      float x[4];
-      scores<HD>(stage, lane, bq, x);
-      const int key = (p_begin + i) * kPage + key_g;
-      x[0] *= sc0;
-      x[1] *= sc1;
-      x[2] *= sc0;
-      x[3] *= sc1;
-      if ((p_begin + i) * kPage + kPage - 1 > c) {  // (the columns' last keys are c and more)
-        x[0] = key <= lim0 ? x[0] : -INFINITY;
-        x[1] = key <= lim1 ? x[1] : -INFINITY;
-        x[2] = key + 2 <= lim0 ? x[2] : -INFINITY;
-        x[3] = key + 2 <= lim1 ? x[3] : -INFINITY;
+      __syncwarp();  // the page has landed for every lane, and every lane is done with the one before
+      copy();
+      const uint8_t* stage = ring + slot * R::kStageBytes;
+      slot = slot + 1 == R::kStages ? 0 : slot + 1;
+      float s[4];
+      scores<HD>(stage, lane, bq, s);
+      if (page * kPage + kPage - 1 > c) {  // (the columns' last keys are c and more)
+        const int key = page * kPage + key_g;
+        s[0] = key <= lim0 ? s[0] : -INFINITY;
+        s[1] = key <= lim1 ? s[1] : -INFINITY;
+        s[2] = key + 2 <= lim0 ? s[2] : -INFINITY;
+        s[3] = key + 2 <= lim1 ? s[3] : -INFINITY;
       }
-      float g0 = fmaxf(x[0], x[2]), g1 = fmaxf(x[1], x[3]);
       // exponents against a reference that moves only when a score exceeds it by more than
       // kGrowth (log2 units), so that P stays below 2^(kPShift + kGrowth)
       constexpr float kGrowth = 8.f;
+      float g0 = fmaxf(s[0], s[2]) * sc0, g1 = fmaxf(s[1], s[3]) * sc1;
       if (__any_sync(0xffffffffu, g0 > m0 + kGrowth || g1 > m1 + kGrowth)) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
@@ -348,31 +451,27 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int first_unit
         m0 = mn0;
         m1 = mn1;
       }
-      const float ms0 = m0 == -INFINITY ? 0.f : m0 - kPShift;
-      const float ms1 = m1 == -INFINITY ? 0.f : m1 - kPShift;
-      const float e0 = fast_exp2(x[0] - ms0), e1 = fast_exp2(x[1] - ms1);
-      const float e2 = fast_exp2(x[2] - ms0), e3 = fast_exp2(x[3] - ms1);
+      const float ms0 = m0 == -INFINITY ? 0.f : kPShift - m0;
+      const float ms1 = m1 == -INFINITY ? 0.f : kPShift - m1;
+      const float e0 = fast_exp2(fmaf(s[0], sc0, ms0)), e1 = fast_exp2(fmaf(s[1], sc1, ms1));
+      const float e2 = fast_exp2(fmaf(s[2], sc0, ms0)), e3 = fast_exp2(fmaf(s[3], sc1, ms1));
       l0 += e0 + e2;
       l1 += e1 + e3;
       add_values<HD>(stage + R::kBytes, lane, movmatrix_trans(pack_f16x2(e0, e1)),
                      movmatrix_trans(pack_f16x2(e2, e3)), acc);
     }
-    copies_wait<0>();
-    __syncwarp();  // every lane is done with the ring
-    if (bad) raise_error(a.err, RB_EBIT_BLOCK_ID);
 
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, o);
       l1 += __shfl_xor_sync(0xffffffffu, l1, o);
     }
-    if (nsplit == 1) {
-      const float inv0 = l0 > 0.f ? g4.v_scale / l0 : 0.f, inv1 = l1 > 0.f ? g4.v_scale / l1 : 0.f;
+    if (seg == pages) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int col = k == 0 ? c0 : c1;
         if (col >= cols) continue;
-        const float inv = k == 0 ? inv0 : inv1;
+        const float l = k == 0 ? l0 : l1, inv = l > 0.f ? g4.v_scale / l : l * 0.f;
         const int j = col / a.group, hh = col - j * a.group;
         uint4* o = reinterpret_cast<uint4*>(
             a.out + (static_cast<size_t>(t0 + j) * a.nh + h * a.group + hh) * HD + g * kPer);
@@ -383,31 +482,38 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int first_unit
         }
       }
     } else {
+      const size_t piece = static_cast<size_t>(first == 0 ? 2 * w + 1 : 2 * w);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float4* o = reinterpret_cast<float4*>(
-            a.part_o + (static_cast<size_t>(u) * kMaxCols + (k == 0 ? c0 : c1)) * HD + g * kPer);
+        const int col = k == 0 ? c0 : c1;
+        if (col >= cols) continue;
+        float4* o = reinterpret_cast<float4*>(a.part_o + (piece * kMaxCols + col) * HD + g * kPer);
 #pragma unroll
         for (int v = 0; v < kPer / 4; ++v)
           o[v] = make_float4(acc[2 * v][k] * g4.v_scale, acc[2 * v][k + 2] * g4.v_scale,
                              acc[2 * v + 1][k] * g4.v_scale, acc[2 * v + 1][k + 2] * g4.v_scale);
+        if (g == 0)
+          a.part_ml[piece * kMaxCols + col] = k == 0 ? make_float2(m0, l0) : make_float2(m1, l1);
       }
-      if (lane < 4) {
-        a.part_ml[static_cast<size_t>(u) * kMaxCols + c0] = make_float2(m0, l0);
-        a.part_ml[static_cast<size_t>(u) * kMaxCols + c1] = make_float2(m1, l1);
-      }
-      // the last split of this (request, kv head) to finish merges all partials
+      // the last piece of this (request, kv head) to finish merges all of them
+      const long long begin = static_cast<long long>(a.dec_off[r]) * a.nkv +
+                              static_cast<long long>(h) * pages;
+      const int w0 = stream.warp_of(begin), pieces = stream.warp_of(begin + pages - 1) - w0 + 1;
       __threadfence();
       __syncwarp();
       int prev = 0;
       if (lane == 0) prev = atomicAdd(a.done + r * a.nkv + h, 1);
       prev = __shfl_sync(0xffffffffu, prev, 0);
-      if (prev == nsplit - 1) {
+      if (prev == pieces - 1) {
         __threadfence();
-        combine_splits<HD, false>(a, h, first, nsplit, t0, cols);
+        if (cols <= 4) merge_pieces<HD, 8>(a, w0, pieces, h, t0, cols);
+        else merge_pieces<HD, 4>(a, w0, pieces, h, t0, cols);
       }
     }
   }
+  copies_wait<0>();
+  __syncwarp();
+  if (bad) raise_error(a.err, RB_EBIT_BLOCK_ID);
 }
 
 }  // namespace attn
