@@ -855,7 +855,8 @@ rb_status rb_paged_attention_kv4(const rb_dims* dims, int32_t num_reqs, int32_t 
  *   d_scales     [num_rows, hidden_size / group_size] fp32 ([num_rows, 1] for group_size 0)
  * Any alignment of whole elements; rows of 16-byte alignment are read and written 16 bytes at a
  * time.  hidden_size up to 32768; group_size 0, 16, 32, 64, 128 or 256, a divisor of hidden_size.
- * A NaN makes its row NaN, an infinity becomes NaN and its row's other values 0.
+ * A NaN makes its row NaN; an infinity becomes NaN (in 8 bits, with the values that share its scale)
+ * and the rest of its row 0.
  * Errors: host -> RB_ERR_INVALID_ARG, RB_ERR_UNSUPPORTED.
  */
 rb_status rb_add_rms_norm(int32_t num_rows, int32_t hidden_size, int32_t dtype, const void* d_x,

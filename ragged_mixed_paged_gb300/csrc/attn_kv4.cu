@@ -79,48 +79,52 @@ struct Kv4Cfg {
   static constexpr int kSmemBytes = (kMost + 1024) > 120 * 1024 ? (kMost + 1024) : 120 * 1024;
 };
 
-// Two pages' codes to fp16 rows of a tile (128 keys x 128 bytes, 128-byte swizzle, one such block per
-// 64 values).  A lane takes 32 values of a token: four 16-byte stores.  A head of 128 has its
-// quarters in two blocks of the same banks: the upper two take their pieces in the order 2, 3,
-// 0, 1.
+// A lane's part in turning pages into fp16 rows of a tile (128 keys x 128 bytes, 128-byte swizzle, one
+// such block per 64 values): it takes runs of 32 values, a quarter (half, for heads of 64) of a
+// token, four 16-byte stores each, of token `tok` and for heads of 128 of tok + 8.  A head of 128 has
+// its quarters in two blocks of the same banks: the upper two take their pieces in the order 2, 3,
+// 0, 1.  The places do not change, so they are worked out once.
 template <int HD, bool kValues>
-__device__ __forceinline__ void turn_pages(const uint8_t* page, uint8_t* tile, int first_row,
-                                           int lane) {
-  using C = TcCfg<HD>;
-  constexpr int kParts = HD / 32;  // lanes of a token
-  const int part = lane % kParts;
-  const bool upper = part >= 2;
-#pragma unroll 1
-  for (int i = 0; i < kParts; ++i) {
-    if (i == kParts / 2) {
-      page += 9 * HD;
-      first_row += kPage;
-    }
-    const int tok = lane / kParts + i % (kParts / 2) * (32 / kParts);
-    const uint4 c = *reinterpret_cast<const uint4*>(page + tok * (HD / 2) + part * 16);
-    const uint8_t* sp = page + 8 * HD;
-    uint32_t sb;
-    if constexpr (kValues)
-      sb = sp[2 * part * kPage + tok] | static_cast<uint32_t>(sp[(2 * part + 1) * kPage + tok]) << 8;
-    else
-      sb = *reinterpret_cast<const uint16_t*>(sp + tok * (HD / 16) + 2 * part);
-    const uint32_t s2 = kv4d::scales2(sb);
-    const int row = first_row + tok;
-    uint8_t* dst = tile + (part >> 1) * (HD == 128 ? C::kHalfBytes : 0) + row * 128;
-    const uint32_t w[4] = {upper ? c.z : c.x, upper ? c.w : c.y, upper ? c.x : c.z,
-                           upper ? c.y : c.w};
-    const uint32_t lo = kv4d::low2(s2), hi = kv4d::high2(s2);
-    const int chunk = ((part & 1) * 4 + (upper ? 2 : 0)) ^ (row & 7);
+struct Turner {
+  static constexpr int kParts = HD / 32, kTokens = 32 / kParts;
+  int code, scale, row, piece[4];  // bytes from the page; from the tile's row and in it
+  uint32_t first, second;          // which of a run's two scales a piece takes (byte selectors)
+  bool upper;
+  __device__ explicit Turner(int lane) {
+    const int part = lane % kParts, tok = lane / kParts;
+    upper = part >= 2;
+    code = tok * (HD / 2) + part * 16;
+    scale = 8 * HD + (kValues ? 2 * part * kPage + tok : tok * (HD / 16) + 2 * part);
+    row = (part >> 1) * (HD == 128 ? TcCfg<HD>::kHalfBytes : 0) + tok * 128;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint32_t h[4];
-      kv4::values8(w[k], h);
-      const uint32_t m = (k < 2) != upper ? lo : hi;
-      *reinterpret_cast<uint4*>(dst + ((chunk ^ k) << 4)) =
-          make_uint4(hmul2(h[0], m), hmul2(h[1], m), hmul2(h[2], m), hmul2(h[3], m));
+    for (int k = 0; k < 4; ++k)
+      piece[k] = row + ((((part & 1) * 4 + (upper ? k ^ 2 : k)) ^ (tok & 7)) << 4);
+    first = upper ? 0x3232 : 0x1010;
+    second = upper ? 0x1010 : 0x3232;
+  }
+  // One page, whose first row of the tile is at `rows`.
+  __device__ __forceinline__ void page(const uint8_t* from, uint8_t* rows) const {
+#pragma unroll
+    for (int i = 0; i < kPage / kTokens; ++i) {  // (rows 8 apart have the same swizzle)
+      const uint4 c = *reinterpret_cast<const uint4*>(from + code + i * kTokens * (HD / 2));
+      const uint8_t* sp = from + scale + i * kTokens * (kValues ? 1 : HD / 16);
+      const uint32_t s2 = kv4d::scales2(
+          kValues ? sp[0] | static_cast<uint32_t>(sp[kPage]) << 8
+                  : static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(sp)));
+      const uint32_t w[4] = {upper ? c.z : c.x, upper ? c.w : c.y, upper ? c.x : c.z,
+                             upper ? c.y : c.w};
+      const uint32_t m0 = __byte_perm(s2, 0, first), m1 = __byte_perm(s2, 0, second);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t h[4];
+        kv4::values8(w[k], h);
+        const uint32_t m = k < 2 ? m0 : m1;
+        *reinterpret_cast<uint4*>(rows + piece[k] + i * kTokens * 128) =
+            make_uint4(hmul2(h[0], m), hmul2(h[1], m), hmul2(h[2], m), hmul2(h[3], m));
+      }
     }
   }
-}
+};
 
 // One contiguous copy into shared memory, its bytes counted on `bar`.
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const uint8_t* src, uint32_t bytes,
@@ -195,6 +199,7 @@ __device__ __forceinline__ void turn_tiles(const AttnArgs& a, Kv4Shared& sh, uin
   volatile int* abort = &sh.abort;
   constexpr int kBytes = 9 * HD, kHalf = C::kPagesPerTile / 2;
   const int lane = threadIdx.x & 31, page = (threadIdx.x >> 5 & 1) * (kHalf / 2);
+  const Turner<HD, kValues> turner(lane);
   uint32_t it = 0, count = 0;
   auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {
     const bool done = tc_wait(bar, phase, abort, a);
@@ -217,8 +222,10 @@ __device__ __forceinline__ void turn_tiles(const AttnArgs& a, Kv4Shared& sh, uin
         break;
       }
       const uint8_t* src = raw + (2 * from + kValues) * K4::kRawBytes;
-      turn_pages<HD, kValues>(src + page * kBytes, ring + st * C::kTileBytes,
-                              ((i & 1) * kHalf + page) * kPage, lane);
+#pragma unroll 1
+      for (int p = page; p < page + kHalf / 2; ++p)
+        turner.page(src + p * kBytes,
+                    ring + st * C::kTileBytes + ((i & 1) * kHalf + p) * (kPage * 128));
       if (i & 1) fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -282,100 +289,98 @@ __device__ void mma_issuer4(const AttnArgs& a, Kv4Shared& sh, uint32_t tmem, uin
   volatile int* abort = &sh.abort;
   constexpr uint32_t idesc_s = make_idesc_f16(128, 128, false);
   constexpr uint32_t idesc_o = make_idesc_f16(128, HD, true);
-  uint32_t itk = 0, tcount[2] = {0, 0}, ucount[2] = {0, 0};
-  bool issued = false;
-  // A wait whose result decides a branch costs a few hundred cycles even when the phase is long
-  // complete, so the barriers of one step are tested together and waited for one by one only if one
-  // of them is not complete.
+  static_assert(K4::kStagesK == 2 && K4::kStagesV == 2, "stages are taken by parity");
+  uint32_t itk = 0;               // K/V tiles so far
+  uint32_t ph_s = 0, ph_u = 0;    // bit x: parity of side x's S tiles and units so far
+  uint32_t used = 0;              // bit x: side x had a unit
+  // Loops stay rolled: this thread's code runs once a step beside the loops of other roles, and
+  // straight-line it waits for its instructions.  A wait whose result decides a branch costs a few
+  // hundred cycles even when the phase is long complete, so the barriers of one step are tested
+  // together and waited for one by one only if one of them is not complete.
   auto test = [](uint64_t* bar, uint32_t phase) { return mbar_test_relaxed(bar, phase); };
   auto relaxed = [&](uint64_t* bar, uint32_t phase) { return tc_wait<true>(bar, phase, abort, a); };
   auto acquire = [&](uint64_t* bar, uint32_t phase) { return tc_wait(bar, phase, abort, a); };
-  const uint64_t q_desc0 = tc::sdesc_sw128(smem_base + K4::kQOffset, 16, 1024);
-  const uint64_t k_desc0 = tc::sdesc_sw128(smem_base, 16, 1024);
-  const uint64_t v_desc0 = tc::sdesc_sw128(smem_base + K4::kVOffset, C::kHalfBytes, 1024);
-  const uint32_t q_lo = static_cast<uint32_t>(q_desc0), k_lo = static_cast<uint32_t>(k_desc0),
-                 v_lo = static_cast<uint32_t>(v_desc0);
-  const uint32_t q_hi = static_cast<uint32_t>(q_desc0 >> 32),
-                 k_hi = static_cast<uint32_t>(k_desc0 >> 32),
-                 v_hi = static_cast<uint32_t>(v_desc0 >> 32);
-  auto step = [](int ks, uint32_t half_bytes) -> uint32_t {
-    return ((ks >> 2) * half_bytes + (ks & 3) * 32) >> 4;
-  };
+  const uint64_t q_desc = tc::sdesc_sw128(smem_base + K4::kQOffset, 16, 1024);
+  const uint64_t v_desc = tc::sdesc_sw128(smem_base + K4::kVOffset, C::kHalfBytes, 1024);
+  const uint32_t q_lo = static_cast<uint32_t>(q_desc), v_lo = static_cast<uint32_t>(v_desc);
+  const uint32_t k_lo = static_cast<uint32_t>(tc::sdesc_sw128(smem_base, 16, 1024));
+  const uint32_t hi = static_cast<uint32_t>(q_desc >> 32);  // the same for all
   auto issue_s = [&](int x, uint32_t kt) {  // S_x = Q_x K^T
-    const uint32_t kd = k_lo + (((kt % K4::kStagesK) * C::kTileBytes) >> 4);
-    const uint32_t qd = q_lo + ((x * C::kQBytes) >> 4);
+    uint32_t kd = k_lo + (((kt & 1) * C::kTileBytes) >> 4), qd = q_lo + ((x * C::kQBytes) >> 4);
     const uint32_t d = tmem + C::col_s(x);
-    tc::mma_ss_lh(d, qd, q_hi, kd, k_hi, idesc_s, 0u);
+#pragma unroll 1
+    for (int half = 0; half < C::kHalves; ++half) {
 #pragma unroll
-    for (int ks = 1; ks < HD / 16; ++ks)
-      tc::mma_ss_lh_acc(d, qd + step(ks, C::kQHalfBytes), q_hi, kd + step(ks, C::kHalfBytes),
-                        k_hi, idesc_s);
+      for (int ks = 0; ks < 4; ++ks)
+        tc::mma_ss_lh(d, qd + ks * 2, hi, kd + ks * 2, hi, idesc_s, half + ks > 0 ? 1u : 0u);
+      qd += C::kQHalfBytes >> 4;
+      kd += C::kHalfBytes >> 4;
+    }
     tc::commit(&sh.s_full[x]);
-    issued = true;
   };
   auto issue_pv = [&](int x, uint32_t kt, bool first, bool last) {  // O_x (+)= P_x V
-    const uint32_t vd = v_lo + (((kt % K4::kStagesV) * C::kTileBytes) >> 4);
-    const uint32_t d = tmem + C::col_o(x), p = tmem + C::col_s(x);
-    tc::mma_ts_lh(d, p, vd, v_hi, idesc_o, first ? 0u : 1u);
+    uint32_t vd = v_lo + (((kt & 1) * C::kTileBytes) >> 4), p = tmem + C::col_s(x);
+    const uint32_t d = tmem + C::col_o(x);
+#pragma unroll 1
+    for (int kk = 0; kk < C::kN / 64; ++kk) {
 #pragma unroll
-    for (int kk = 1; kk < C::kN / 16; ++kk)
-      tc::mma_ts_lh_acc(d, p + kk * 8, vd + ((kk * 16 * 128) >> 4), v_hi, idesc_o);
+      for (int ks = 0; ks < 4; ++ks)
+        tc::mma_ts_lh(d, p + ks * 8, vd + ((ks * 16 * 128) >> 4), hi, idesc_o,
+                      first && kk + ks == 0 ? 0u : 1u);
+      p += 32;
+      vd += (64 * 128) >> 4;
+    }
     if (last) tc::commit(&sh.o_done[x]);
   };
   for (int k = 0;; ++k) {
     const int slot = k % C::kRing;
     if (!acquire(&sh.unit_full[slot], (k / C::kRing) & 1)) break;
-    const TcUnit un = sh.units[slot];
-    if (!un.valid) break;
-    if (!acquire(&sh.k_full[itk % K4::kStagesK], (itk / K4::kStagesK) & 1)) break;
+    const int n0 = sh.units[slot].n[0], n1 = sh.units[slot].n[1];
+    if (!sh.units[slot].valid) break;
+    const int steps = max(n0, n1);
+    if (!relaxed(&sh.k_full[itk & 1], (itk >> 1) & 1)) break;
     bool ok = true;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      if (!ok || un.n[x] == 0) continue;
-      if (!acquire(&sh.q_ready[x], ucount[x] & 1)) { ok = false; continue; }
+#pragma unroll 1
+    for (int x = 0; x < (n1 > 0 ? 2 : 1) && ok; ++x) {
+      ok = relaxed(&sh.q_ready[x], ph_u >> x & 1);
+      if (!ok) break;
       tc::fence_after_sync();
       issue_s(x, itk);
     }
-    for (int j = 0; j < un.n_kt && ok; ++j) {
+    for (int j = 0; j < steps && ok; ++j) {
       const uint32_t kt = itk + j;
-      bool k_ready = false, v_ready = false;
-#pragma unroll
+#pragma unroll 1
       for (int x = 0; x < 2; ++x) {
-        if (j >= un.n[x]) continue;
-        const bool next_s = j + 1 < un.n[x];
-        const bool need_v = !v_ready, need_o = j == 0 && ucount[x] > 0, need_k = next_s && !k_ready;
-        uint64_t* bar_v = &sh.v_full[kt % K4::kStagesV];
-        uint64_t* bar_k = &sh.k_full[(kt + 1) % K4::kStagesK];
-        const uint32_t ph_v = (kt / K4::kStagesV) & 1, ph_k = ((kt + 1) / K4::kStagesK) & 1;
-        const uint32_t ph_p = (tcount[x] + j) & 1, ph_o = (ucount[x] - 1) & 1;
-        const bool ready = test(&sh.p_full[x], ph_p) & (!need_v || test(bar_v, ph_v)) &
-                           (!need_o || test(&sh.o_free[x], ph_o)) & (!need_k || test(bar_k, ph_k));
-        if (!ready && (!relaxed(&sh.p_full[x], ph_p) || (need_v && !relaxed(bar_v, ph_v)) ||
+        const int n = x ? n1 : n0;
+        if (j >= n) continue;
+        const bool next_s = j + 1 < n, need_o = j == 0 && (used >> x & 1);
+        uint64_t* bar_v = &sh.v_full[kt & 1];
+        uint64_t* bar_k = &sh.k_full[(kt + 1) & 1];
+        const uint32_t ph_v = (kt >> 1) & 1, ph_k = ((kt + 1) >> 1) & 1;
+        const uint32_t ph_p = ph_s >> x & 1, ph_o = (ph_u >> x & 1) ^ 1;
+        const bool ready = test(&sh.p_full[x], ph_p) & test(bar_v, ph_v) &
+                           (!need_o || test(&sh.o_free[x], ph_o)) & (!next_s || test(bar_k, ph_k));
+        if (!ready && (!relaxed(&sh.p_full[x], ph_p) || !relaxed(bar_v, ph_v) ||
                        (need_o && !relaxed(&sh.o_free[x], ph_o)) ||
-                       (need_k && !relaxed(bar_k, ph_k)))) {
+                       (next_s && !relaxed(bar_k, ph_k)))) {
           ok = false;
           break;
         }
-        k_ready = k_ready || next_s;
-        v_ready = true;
         tc::fence_after_sync();
         issue_pv(x, kt, j == 0, !next_s);
         if (next_s) issue_s(x, kt + 1);
+        ph_s ^= 1u << x;
       }
     }
     if (!ok) break;
     tc::mbar_arrive(&sh.unit_empty[slot]);
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      tcount[x] += un.n[x];
-      if (un.n[x] > 0) ++ucount[x];
-    }
-    itk += un.n_kt;
+    ph_u ^= n1 > 0 ? 3u : 1u;
+    used |= n1 > 0 ? 3u : 1u;
+    itk += steps;
   }
-  if (issued) {  // every MMA and every commit-arrival lands before TMEM and smem are released
-    tc::commit(&sh.drain);
-    mbar_wait_bounded(&sh.drain, 0, 100000000ull);
-  }
+  // every MMA and every commit-arrival lands before TMEM and smem are released
+  tc::commit(&sh.drain);
+  mbar_wait_bounded(&sh.drain, 0, 100000000ull);
 }
 
 // Columns of a tile that a softmax thread takes at a time.

@@ -15,8 +15,10 @@ namespace rb {
 namespace {
 
 constexpr int kRun = 8;        // values of one run
-constexpr int kRuns = 4;       // runs a thread may hold
+constexpr int kMostRuns = 4096;  // of a row
 constexpr float kMax8 = 448.f; // largest e4m3 value
+
+enum Out : int { kPlain, kRowScales, kGroupScales };
 
 struct NormArgs {
   const void *x, *residual, *weight;
@@ -47,39 +49,41 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float f) {
   return __float2bfloat16_rn(f);
 }
 
-// Run `run` of a row of n values: eight values, zeros past the end.
+// Eight values of a row as they lie in memory.
 template <class T>
-__device__ __forceinline__ void load_run(const T* row, int run, int n, bool wide, float (&f)[kRun]) {
+struct alignas(16) Run {
+  T v[kRun];
+};
+
+// Run `run` of a row of n values, zeros past the end.
+template <class T>
+__device__ __forceinline__ Run<T> load_run(const T* row, int run, int n, bool wide) {
   const T* p = row + run * kRun;
+  Run<T> r;
   if (wide && (run + 1) * kRun <= n) {
     constexpr int kVec = static_cast<int>(sizeof(T)) * kRun / 16;
-    uint4 w[kVec];
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
-    const T* v = reinterpret_cast<const T*>(w);
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) f[i] = to_float(v[i]);
+    for (int i = 0; i < kVec; ++i)
+      reinterpret_cast<uint4*>(r.v)[i] = reinterpret_cast<const uint4*>(p)[i];
   } else {
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) f[i] = run * kRun + i < n ? to_float(p[i]) : 0.f;
+    for (int i = 0; i < kRun; ++i) r.v[i] = run * kRun + i < n ? p[i] : from_float<T>(0.f);
   }
+  return r;
 }
 
 template <class T>
-__device__ __forceinline__ void store_run(T* row, int run, int n, bool wide, const float (&f)[kRun]) {
+__device__ __forceinline__ void store_run(T* row, int run, int n, bool wide, const Run<T>& r) {
   T* p = row + run * kRun;
   if (wide && (run + 1) * kRun <= n) {
     constexpr int kVec = static_cast<int>(sizeof(T)) * kRun / 16;
-    uint4 w[kVec];
-    T* v = reinterpret_cast<T*>(w);
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) v[i] = from_float<T>(f[i]);
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
+    for (int i = 0; i < kVec; ++i)
+      reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(r.v)[i];
   } else {
 #pragma unroll
     for (int i = 0; i < kRun; ++i)
-      if (run * kRun + i < n) p[i] = from_float<T>(f[i]);
+      if (run * kRun + i < n) p[i] = r.v[i];
   }
 }
 
@@ -93,106 +97,144 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[kRun]) {
                     h[2] | static_cast<uint32_t>(h[3]) << 16);
 }
 
-// Reduction over the `kWarps` warps of a row; every thread gets the result.
-template <int kWarps, class Op>
-__device__ __forceinline__ float row_reduce(float v, float* shared, const Op& op) {
+// Sum and maximum over the warps of a row (kWarps of them; 0: the CTA's); every thread gets both.
+template <int kWarps, bool kMax>
+__device__ __forceinline__ float2 row_reduce(float sum, float top, float2* shared) {
+  auto over_lanes = [&](int first) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-  if constexpr (kWarps > 1) {
+    for (int o = first; o > 0; o >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (kMax) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
+  };
+  over_lanes(16);
+  if constexpr (kWarps != 1) {
     const int lane = threadIdx.x & 31;
-    if (lane == 0) shared[threadIdx.x >> 5] = v;
+    if (lane == 0) shared[threadIdx.x >> 5] = make_float2(sum, top);
     __syncthreads();
-    v = shared[lane % kWarps];
-#pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+    float2 v = make_float2(0.f, 0.f);
+    if (kWarps > 0) v = shared[lane % (kWarps > 0 ? kWarps : 1)];
+    else if (lane < blockDim.x / 32) v = shared[lane];
+    sum = v.x;
+    top = v.y;
+    over_lanes(kWarps > 0 ? kWarps / 2 : 16);
   }
-  return v;
+  return make_float2(sum, top);
 }
 
-template <class T, int kWarps, bool k8bit>
-__global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) norm_kernel(const NormArgs a) {
-  __shared__ float s_sum[32], s_max[32];
-  const int tid = kWarps == 1 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
+// a / b, correctly rounded for ordinary values: a product with the rounded reciprocal and one
+// correction by its exact remainder (Markstein 1990), three instructions once r = 1 / b is there.
+__device__ __forceinline__ float quotient(float a, float b, float r) {
+  const float q = a * r;
+  return fmaf(fmaf(-q, b, a), r, q);
+}
+
+// The 8-bit codes need no norm: y / (max |y| / 448) is 448 z / max |z| with z = r weight, which is
+// exact in fp32 for 16-bit types.  So ties are ties, and one reduction gives sum and maximum.
+// A row is a CTA's: of kWarps warps, or (0) of as many as it has, kMost threads at most; with one warp a
+// row, a CTA has four rows.
+template <class T, int kWarps, int kMost, int kRuns, int kOut>
+__global__ void __launch_bounds__(kMost, kMost == 1024 ? 1 : 1536 / kMost)
+    norm_kernel(const NormArgs a) {
+  constexpr bool k8bit = kOut != kPlain, kRowScale = kOut == kRowScales;
+  __shared__ float2 s_row[32];
+  const int tid = kWarps == 1 ? threadIdx.x & 31 : threadIdx.x;
   const int row = kWarps == 1 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
   if (row >= a.rows) return;  // (a whole warp, when a CTA has several rows)
-  constexpr int kThreads = kWarps * 32;
+  const int threads = kWarps > 0 ? kWarps * 32 : blockDim.x;
   const int n = a.hidden;
   const bool wide = a.wide != 0;
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-  float y[kRuns][kRun];
+  const T* weight = static_cast<const T*>(a.weight);
+  const bool weight_wide = aligned16(a.weight);
+  Run<T> y[kRuns];
 #pragma unroll
-  for (int i = 0; i < kRuns; ++i) {
-    const int run = tid + i * kThreads;
-    if (run * kRun < n) load_run(x, run, n, wide, y[i]);
-    else
-#pragma unroll
-      for (int k = 0; k < kRun; ++k) y[i][k] = 0.f;
-  }
+  for (int i = 0; i < kRuns; ++i)
+    if ((tid + i * threads) * kRun < n) y[i] = load_run(x, tid + i * threads, n, wide);
   if (a.residual != nullptr) {
     const T* res = static_cast<const T*>(a.residual) + row * a.residual_stride;
     T* after = static_cast<T*>(a.residual_out) + row * a.residual_out_stride;
-    float z[kRuns][kRun];
+    Run<T> r[kRuns];
 #pragma unroll
     for (int i = 0; i < kRuns; ++i)
-      if ((tid + i * kThreads) * kRun < n) load_run(res, tid + i * kThreads, n, wide, z[i]);
+      if ((tid + i * threads) * kRun < n) r[i] = load_run(res, tid + i * threads, n, wide);
 #pragma unroll
     for (int i = 0; i < kRuns; ++i) {
-      const int run = tid + i * kThreads;
+      const int run = tid + i * threads;
       if (run * kRun >= n) break;
 #pragma unroll
-      for (int k = 0; k < kRun; ++k) y[i][k] = to_float(from_float<T>(y[i][k] + z[i][k]));
+      for (int k = 0; k < kRun; ++k)
+        y[i].v[k] = from_float<T>(to_float(y[i].v[k]) + to_float(r[i].v[k]));
       store_run(after, run, n, wide, y[i]);
     }
   }
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < kRuns; ++i)
-#pragma unroll
-    for (int k = 0; k < kRun; ++k) sum = fmaf(y[i][k], y[i][k], sum);
-  sum = row_reduce<kWarps>(sum, s_sum, [](float p, float q) { return p + q; });
-  const float inv = rsqrtf(sum / static_cast<float>(n) + a.eps);
-  const T* weight = static_cast<const T*>(a.weight);
-  const bool weight_wide = aligned16(a.weight);
-  float top = 0.f;
+  float sum = 0.f, top = 0.f;
+  float z[kRuns][kRun];
 #pragma unroll
   for (int i = 0; i < kRuns; ++i) {
-    const int run = tid + i * kThreads;
+    const int run = tid + i * threads;
     if (run * kRun >= n) break;
-    float w[kRun];
-    load_run(weight, run, n, weight_wide, w);
 #pragma unroll
     for (int k = 0; k < kRun; ++k) {
-      y[i][k] = y[i][k] * inv * w[k];
-      if constexpr (k8bit) top = fmaxf(top, fabsf(y[i][k]));
+      const float v = to_float(y[i].v[k]);
+      sum = fmaf(v, v, sum);
     }
-    if constexpr (!k8bit) {
-      T* out = static_cast<T*>(a.out) + static_cast<size_t>(row) * n;
-      store_run(out, run, n, aligned16(out), y[i]);
+    if constexpr (kRowScale) {
+      const Run<T> w = load_run(weight, run, n, weight_wide);
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) {
+        z[i][k] = to_float(y[i].v[k]) * to_float(w.v[k]);
+        top = fmaxf(top, fabsf(z[i][k]));
+      }
     }
   }
-  if constexpr (k8bit) {
-    uint8_t* out = static_cast<uint8_t*>(a.out) + static_cast<size_t>(row) * n;
-    const bool out_wide = (reinterpret_cast<uintptr_t>(out) & 7u) == 0;
-    if (a.group == 0)
-      top = row_reduce<kWarps>(top, s_max, [](float p, float q) { return fmaxf(p, q); });
-    const int lanes = a.group / kRun;  // of one group
+  const float2 both = row_reduce<kWarps, kRowScale>(sum, top, s_row);
+  const float inv = rsqrtf(both.x / static_cast<float>(n) + a.eps);
+  if constexpr (!k8bit) {
+    T* out = static_cast<T*>(a.out) + static_cast<size_t>(row) * n;
+    const bool out_wide = aligned16(out);
 #pragma unroll
     for (int i = 0; i < kRuns; ++i) {
-      const int run = tid + i * kThreads;
-      if (a.group != 0) {  // (every lane of the warp is here: a group ends with the row)
-        top = 0.f;
+      const int run = tid + i * threads;
+      if (run * kRun >= n) break;
+      const Run<T> w = load_run(weight, run, n, weight_wide);
 #pragma unroll
-        for (int k = 0; k < kRun; ++k) top = fmaxf(top, fabsf(y[i][k]));
+      for (int k = 0; k < kRun; ++k)
+        y[i].v[k] = from_float<T>(to_float(y[i].v[k]) * inv * to_float(w.v[k]));
+      store_run(out, run, n, out_wide, y[i]);
+    }
+  } else {
+    uint8_t* out = static_cast<uint8_t*>(a.out) + static_cast<size_t>(row) * n;
+    const bool out_wide = (reinterpret_cast<uintptr_t>(out) & 7u) == 0;
+    const int lanes = a.group / kRun;  // of one group
+    top = both.y;
+    float r = __frcp_rn(top);
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) {
+      const int run = tid + i * threads;
+      const bool here = run * kRun < n;
+      if constexpr (!kRowScale) {
+        top = 0.f;
+        if (here) {
+          const Run<T> w = load_run(weight, run, n, weight_wide);
+#pragma unroll
+          for (int k = 0; k < kRun; ++k) {
+            z[i][k] = to_float(y[i].v[k]) * to_float(w.v[k]);
+            top = fmaxf(top, fabsf(z[i][k]));
+          }
+        }
+        // (every lane of the warp is here: a group ends with the row)
         for (int o = lanes / 2; o > 0; o >>= 1)
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        r = __frcp_rn(top);
       }
-      if (run * kRun >= n) continue;
-      const float s = top / kMax8;
-      float t[kRun];
+      if (!here) continue;
+      const float s = top * inv * (1.f / kMax8);
+      const bool ordinary = s > 0.f && top < INFINITY && r < INFINITY;
 #pragma unroll
       for (int k = 0; k < kRun; ++k)  // (0 where s is 0, but NaN stays NaN)
-        t[k] = s > 0.f ? __fdiv_rn(y[i][k], s) : y[i][k] * 0.f;
-      const uint2 c = codes8(t);
+        z[i][k] = ordinary ? quotient(z[i][k] * kMax8, top, r) : z[i][k] * inv * 0.f;
+      const uint2 c = codes8(z[i]);
       if (out_wide && (run + 1) * kRun <= n) {
         *reinterpret_cast<uint2*>(out + run * kRun) = c;
       } else {
@@ -200,7 +242,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) norm_kernel(c
         for (int k = 0; k < kRun; ++k)
           if (run * kRun + k < n) out[run * kRun + k] = b[k];
       }
-      if (a.group == 0) {
+      if constexpr (kRowScale) {
         if (run == 0) a.scales[row] = s;
       } else if (run % lanes == 0) {
         a.scales[static_cast<size_t>(row) * (n / a.group) + run / lanes] = s;
@@ -209,23 +251,30 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32) norm_kernel(c
   }
 }
 
-template <class T, bool k8bit>
-void launch_norm(const NormArgs& a, cudaStream_t s) {
+template <class T, int kOut>
+rb_status run_norm(const NormArgs& a, cudaStream_t s) {
+  // Two runs a thread, in whole warps, up to a CTA of 1024 (four beyond).  A count of warps that is
+  // a power of two is compiled in (8192 x 4096 bf16 into 8 bits: 44 us against 49).  Four runs on
+  // half the threads take 54 there; persistent CTAs that load the next row ahead 65.
   const int runs = (a.hidden + kRun - 1) / kRun;
-  if (runs <= 32 * kRuns) norm_kernel<T, 1, k8bit><<<(a.rows + 3) / 4, 128, 0, s>>>(a);
-  else if (runs <= 128 * kRuns) norm_kernel<T, 4, k8bit><<<a.rows, 128, 0, s>>>(a);
-  else if (runs <= 256 * kRuns) norm_kernel<T, 8, k8bit><<<a.rows, 256, 0, s>>>(a);
-  else if (runs <= 512 * kRuns) norm_kernel<T, 16, k8bit><<<a.rows, 512, 0, s>>>(a);
-  else norm_kernel<T, 32, k8bit><<<a.rows, 1024, 0, s>>>(a);
+  const int warps = (runs + 63) / 64;
+  if (warps == 1) norm_kernel<T, 1, 128, 2, kOut><<<(a.rows + 3) / 4, 128, 0, s>>>(a);
+  else if (warps == 2) norm_kernel<T, 2, 64, 2, kOut><<<a.rows, 64, 0, s>>>(a);
+  else if (warps == 4) norm_kernel<T, 4, 128, 2, kOut><<<a.rows, 128, 0, s>>>(a);
+  else if (warps == 8) norm_kernel<T, 8, 256, 2, kOut><<<a.rows, 256, 0, s>>>(a);
+  else if (warps == 16) norm_kernel<T, 16, 512, 2, kOut><<<a.rows, 512, 0, s>>>(a);
+  else if (warps < 16) norm_kernel<T, 0, 512, 2, kOut><<<a.rows, warps * 32, 0, s>>>(a);
+  else if (warps <= 32) norm_kernel<T, 0, 1024, 2, kOut><<<a.rows, warps * 32, 0, s>>>(a);
+  else norm_kernel<T, 0, 1024, 4, kOut><<<a.rows, (warps + 1) / 2 * 32, 0, s>>>(a);
+  if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
+  note_launches(1);
+  return RB_OK;
 }
 
 template <class T>
 rb_status run_norm(const NormArgs& a, bool eight, cudaStream_t s) {
-  if (eight) launch_norm<T, true>(a, s);
-  else launch_norm<T, false>(a, s);
-  if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
-  note_launches(1);
-  return RB_OK;
+  if (!eight) return run_norm<T, kPlain>(a, s);
+  return a.group == 0 ? run_norm<T, kRowScales>(a, s) : run_norm<T, kGroupScales>(a, s);
 }
 
 }  // namespace
@@ -242,7 +291,7 @@ extern "C" rb_status rb_add_rms_norm(int32_t num_rows, int32_t hidden_size, int3
   if (num_rows < 0 || hidden_size < 1 || !std::isfinite(eps) || eps < 0.f) return RB_ERR_INVALID_ARG;
   if (dtype != RB_BF16 && dtype != RB_FP16 && dtype != RB_FP32) return RB_ERR_UNSUPPORTED;
   const bool eight = out_dtype == RB_E4M3;
-  if ((!eight && out_dtype != dtype) || hidden_size > 1024 * kRuns * kRun) return RB_ERR_UNSUPPORTED;
+  if ((!eight && out_dtype != dtype) || hidden_size > kMostRuns * kRun) return RB_ERR_UNSUPPORTED;
   if (group_size != 0) {
     if (!eight || group_size < 0) return RB_ERR_INVALID_ARG;
     if (group_size != 16 && group_size != 32 && group_size != 64 && group_size != 128 &&
