@@ -56,6 +56,13 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   return r;
 }
 
+// a / b, correctly rounded for ordinary values: a product with the rounded reciprocal and one
+// correction by its exact remainder (Markstein 1990), three instructions once r = 1 / b is there.
+__device__ __forceinline__ float quotient(float a, float b, float r) {
+  const float q = a * r;
+  return fmaf(fmaf(-q, b, a), r, q);
+}
+
 // The eight values of four bytes of codes as half2 (value 2i in the low half), exact.
 __device__ __forceinline__ void values8(uint32_t codes, uint32_t (&h)[4]) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"

@@ -5,12 +5,18 @@
 // Rotation: a pair (x, y) of a head becomes (x cos - y sin, y cos + x sin), the angles' cosines and
 // sines taken from the caller's fp32 table; products and sums are rounded to fp32 one by one (no
 // fused multiply-add), so that the result is the same whatever evaluates the formula.
+#include <cfloat>
+
 #include "kv4.cuh"
 
 namespace rb {
 namespace {
 
 constexpr int kThreads = 128;
+
+struct LayerScale {
+  float scale, inverse;
+};
 
 struct AppendArgs {
   const __nv_bfloat16 *q, *k, *v;
@@ -22,7 +28,7 @@ struct AppendArgs {
   int32_t* err;
   long long num_slots;
   int tokens, nh, nkv, hd, rotary, max_position, interleaved;
-  float k_scale, v_scale;
+  LayerScale k_scale, v_scale;
 };
 
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
@@ -59,7 +65,7 @@ __device__ __forceinline__ void turn16(uint4& a, uint4& b, const float (&c)[8], 
 // Codes and scale of sixteen bf16 values, written to their place; returns whether one of them was
 // not finite (an infinity is held as the largest value, NaN as 0).
 template <bool kValues>
-__device__ __forceinline__ bool put_block(const uint4& a, const uint4& b, float scale,
+__device__ __forceinline__ bool put_block(const uint4& a, const uint4& b, const LayerScale& by,
                                           uint8_t* cache, int slot, int head, int block, int nkv,
                                           int hd) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -74,13 +80,15 @@ __device__ __forceinline__ bool put_block(const uint4& a, const uint4& b, float 
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    odd |= !isfinite(y[i]);
-    if (y[i] != y[i]) y[i] = 0.f;
-    if (scale != 1.f) y[i] = __fdiv_rn(y[i], scale);
+    const bool nan = y[i] != y[i];
+    odd |= nan || fabsf(y[i]) > FLT_MAX;
+    if (nan) y[i] = 0.f;
+    if (by.scale != 1.f) y[i] = kv4::quotient(y[i], by.scale, by.inverse);
+    if (!(fabsf(y[i]) <= FLT_MAX)) y[i] = copysignf(FLT_MAX, y[i]);
     top = fmaxf(top, fabsf(y[i]));
   }
   const uint32_t sb = kv4::scale_byte(__fdiv_rn(top, 6.f));
-  const float s = kv4::scale_value(sb);
+  const float s = kv4::scale_value(sb), r = __frcp_rn(s);
   uint32_t code[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -88,7 +96,7 @@ __device__ __forceinline__ bool put_block(const uint4& a, const uint4& b, float 
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float x = y[4 * i + j];
-      t[j] = copysignf(s > 0.f ? __fdiv_rn(fabsf(x), s) : 0.f, x);
+      t[j] = sb != 0 ? copysignf(kv4::quotient(x, s, r), x) : copysignf(0.f, x);
     }
     code[i] = kv4::codes4(t[0], t[1], t[2], t[3]);
   }
@@ -100,21 +108,53 @@ __device__ __forceinline__ bool put_block(const uint4& a, const uint4& b, float 
 }
 
 // One CTA per token.  A thread has one place in a head (the two chunks of a rotated or copied
-// run of sixteen values), whose cosines and sines it holds, and takes every head of that
-// place in turn, four at a time so that their loads overlap.  The 4-bit cache's keys pass through
-// shared memory as bf16, because the sixteen values that share a scale are not those of one
-// thread's pairs.
-template <bool k4>
+// run of sixteen values), whose cosines and sines it holds, and takes every head of that place in
+// turn, kBatch at a time so that their loads overlap; the first ones are on their way before
+// position and slot are known.  The 4-bit cache's keys pass through shared memory as bf16,
+// because the sixteen values that share a scale are not those of one thread's pairs.
+template <bool k4, int kBatch>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
   extern __shared__ uint4 s_keys[];  // k4: the token's rotated keys
   const int t = blockIdx.x;
   const int per_head = a.hd / 16, lanes = kThreads / per_head;
   const int j = threadIdx.x % per_head, first = threadIdx.x / per_head;
   const int slot = __ldg(a.slots + t);
+  const int pos = a.rotary > 0 ? __ldg(a.positions + t) : 0;
+  // chunks of this thread's place in a head
   const bool turned = j < a.rotary / 16;
+  const bool split = turned && !a.interleaved;
+  const int ca = split ? j : 2 * j, cb = split ? j + a.rotary / 16 : 2 * j + 1;
+  const int nq = a.q != nullptr ? a.nh : 0;
+  const int heads = first < lanes ? nq + (k4 ? a.nkv : 2 * a.nkv) : 0;
+  const __nv_bfloat16* q = a.q + t * a.q_stride;
+  const __nv_bfloat16* k = a.k + t * a.k_stride;
+  const __nv_bfloat16* v = a.v + t * a.v_stride;
+  uint4 x[kBatch], y[kBatch];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i * lanes;
+      if (h >= heads) break;
+      const __nv_bfloat16* src = h < nq            ? q + static_cast<size_t>(h) * a.hd
+                                 : h < nq + a.nkv ? k + static_cast<size_t>(h - nq) * a.hd
+                                                  : v + static_cast<size_t>(h - nq - a.nkv) * a.hd;
+      const uint4* p = reinterpret_cast<const uint4*>(src);
+      x[i] = p[ca];
+      y[i] = p[cb];
+    }
+  };
+  load(first);
+  // k4: the block of sixteen values that this thread quantises first, of K (below `blocks`) or V
+  const int blocks = a.nkv * per_head;
+  uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
+  const int mine = static_cast<int>(threadIdx.x) - blocks;
+  if (k4 && mine >= 0 && mine < blocks) {
+    const uint4* p = reinterpret_cast<const uint4*>(v) + 2 * mine;
+    v0 = p[0];
+    v1 = p[1];
+  }
   float c[8], s[8];
   if (a.rotary > 0) {
-    const int pos = __ldg(a.positions + t);
     if (pos < 0 || pos >= a.max_position) {  // the token is left out
       if (threadIdx.x == 0) raise_error(a.err, RB_EBIT_POSITION);
       return;
@@ -132,55 +172,32 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
   }
   const bool keep = slot >= 0 && slot < a.num_slots;
   if (slot >= a.num_slots && threadIdx.x == 0) raise_error(a.err, RB_EBIT_SLOT);
-  // chunks of this thread's place in a head
-  const bool split = turned && !a.interleaved;
-  const int ca = split ? j : 2 * j, cb = split ? j + a.rotary / 16 : 2 * j + 1;
-  const int nq = a.q != nullptr ? a.nh : 0;
-  const int heads = nq + (keep ? (k4 ? a.nkv : 2 * a.nkv) : 0);
-  const __nv_bfloat16* q = a.q + t * a.q_stride;
-  const __nv_bfloat16* k = a.k + t * a.k_stride;
-  const __nv_bfloat16* v = a.v + t * a.v_stride;
   __nv_bfloat16* q_out = a.q_out + t * a.q_out_stride;
   const size_t cache_row = static_cast<size_t>(keep ? slot : 0) * a.nkv * a.hd;
   __nv_bfloat16* k_out = k4 ? reinterpret_cast<__nv_bfloat16*>(s_keys)
                             : static_cast<__nv_bfloat16*>(a.k_cache) + cache_row;
   __nv_bfloat16* v_out = static_cast<__nv_bfloat16*>(a.v_cache) + cache_row;
-  constexpr int kBatch = 4;
-  if (first < lanes) {
-    for (int h0 = first; h0 < heads; h0 += kBatch * lanes) {
-      uint4 x[kBatch], y[kBatch];
+  for (int h0 = first; h0 < heads; h0 += kBatch * lanes) {
+    if (h0 != first) load(h0);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int h = h0 + i * lanes;
-        if (h >= heads) break;
-        const __nv_bfloat16* src = h < nq            ? q + static_cast<size_t>(h) * a.hd
-                                   : h < nq + a.nkv ? k + static_cast<size_t>(h - nq) * a.hd
-                                                    : v + static_cast<size_t>(h - nq - a.nkv) * a.hd;
-        const uint4* p = reinterpret_cast<const uint4*>(src);
-        x[i] = p[ca];
-        y[i] = p[cb];
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i * lanes;
+      if (h >= heads || (h >= nq && !keep)) break;
+      __nv_bfloat16* dst;
+      if (h < nq + a.nkv) {
+        if (turned) turn16(x[i], y[i], c, s, a.interleaved != 0);
+        dst = h < nq ? q_out + static_cast<size_t>(h) * a.hd
+                     : k_out + static_cast<size_t>(h - nq) * a.hd;
+      } else {
+        dst = v_out + static_cast<size_t>(h - nq - a.nkv) * a.hd;
       }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int h = h0 + i * lanes;
-        if (h >= heads) break;
-        __nv_bfloat16* dst;
-        if (h < nq + a.nkv) {
-          if (turned) turn16(x[i], y[i], c, s, a.interleaved != 0);
-          dst = h < nq ? q_out + static_cast<size_t>(h) * a.hd
-                       : k_out + static_cast<size_t>(h - nq) * a.hd;
-        } else {
-          dst = v_out + static_cast<size_t>(h - nq - a.nkv) * a.hd;
-        }
-        reinterpret_cast<uint4*>(dst)[ca] = x[i];
-        reinterpret_cast<uint4*>(dst)[cb] = y[i];
-      }
+      reinterpret_cast<uint4*>(dst)[ca] = x[i];
+      reinterpret_cast<uint4*>(dst)[cb] = y[i];
     }
   }
   if constexpr (k4) {
     if (!keep) return;
     __syncthreads();
-    const int blocks = a.nkv * per_head;
     bool odd = false;
     for (int i = threadIdx.x; i < 2 * blocks; i += kThreads) {
       if (i < blocks) {
@@ -189,13 +206,30 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
                                 a.nkv, a.hd);
       } else {
         const int b = i - blocks;
-        const uint4* p = reinterpret_cast<const uint4*>(v) + 2 * b;
-        odd |= put_block<true>(p[0], p[1], a.v_scale, static_cast<uint8_t*>(a.v_cache), slot,
+        if (b != mine) {  // (not the one that is here already)
+          const uint4* p = reinterpret_cast<const uint4*>(v) + 2 * b;
+          v0 = p[0];
+          v1 = p[1];
+        }
+        odd |= put_block<true>(v0, v1, a.v_scale, static_cast<uint8_t*>(a.v_cache), slot,
                                b / per_head, b % per_head, a.nkv, a.hd);
       }
     }
     if (odd) raise_error(a.err, RB_EBIT_NOT_FINITE);
   }
+}
+
+template <bool k4>
+rb_status launch_append(const AppendArgs& a, size_t smem, cudaStream_t s) {
+  // heads that a thread takes: no more are loaded at a time, the fewer registers the more CTAs
+  const int lanes = kThreads / (a.hd / 16);
+  const int heads = (a.q != nullptr ? a.nh : 0) + (k4 ? a.nkv : 2 * a.nkv);
+  if (heads <= lanes) append_kernel<k4, 1><<<a.tokens, kThreads, smem, s>>>(a);
+  else if (heads <= 2 * lanes) append_kernel<k4, 2><<<a.tokens, kThreads, smem, s>>>(a);
+  else append_kernel<k4, 4><<<a.tokens, kThreads, smem, s>>>(a);
+  if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
+  note_launches(1);
+  return RB_OK;
 }
 
 // A thread per block of sixteen values of K or V: nine bytes in, thirty-two out.
@@ -334,11 +368,7 @@ extern "C" rb_status rb_kv_append(const rb_dims* dims, int32_t num_tokens_padded
                                     d_k, k_stride, d_v, v_stride, d_slot_mapping, d_q_out,
                                     q_out_stride, d_k_cache, d_v_cache, d_error_word, &a);
   if (st != RB_OK || num_tokens_padded == 0) return st;
-  append_kernel<false>
-      <<<num_tokens_padded, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
-  note_launches(1);
-  return RB_OK;
+  return launch_append<false>(a, 0, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" rb_status rb_kv4_append(const rb_dims* dims, int32_t num_tokens_padded,
@@ -357,15 +387,11 @@ extern "C" rb_status rb_kv4_append(const rb_dims* dims, int32_t num_tokens_padde
   if (st != RB_OK) return st;
   st = kv4_checks(*dims, k_scale, v_scale);
   if (st != RB_OK || num_tokens_padded == 0) return st;
-  a.k_scale = k_scale;
-  a.v_scale = v_scale;
+  a.k_scale = {k_scale, 1.f / k_scale};
+  a.v_scale = {v_scale, 1.f / v_scale};
   const size_t smem = static_cast<size_t>(a.nkv) * a.hd * 2;
   if (smem > 48 * 1024) return RB_ERR_UNSUPPORTED;
-  append_kernel<true>
-      <<<num_tokens_padded, kThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
-  if (last_launch_status() != RB_OK) return RB_ERR_CUDA;
-  note_launches(1);
-  return RB_OK;
+  return launch_append<true>(a, smem, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" rb_status rb_kv4_read(const rb_dims* dims, int32_t num_rows, const int32_t* d_slots,

@@ -7,9 +7,7 @@
 // Bound by HBM: a row is read once, held in registers between the sum of its squares and its
 // output, and written once.  A thread holds runs of eight values; a row is one warp's (up to 1024
 // values) or one CTA's.
-#include <cuda_fp16.h>
-
-#include "rb_internal.cuh"
+#include "kv4.cuh"
 
 namespace rb {
 namespace {
@@ -122,13 +120,6 @@ __device__ __forceinline__ float2 row_reduce(float sum, float top, float2* share
   return make_float2(sum, top);
 }
 
-// a / b, correctly rounded for ordinary values: a product with the rounded reciprocal and one
-// correction by its exact remainder (Markstein 1990), three instructions once r = 1 / b is there.
-__device__ __forceinline__ float quotient(float a, float b, float r) {
-  const float q = a * r;
-  return fmaf(fmaf(-q, b, a), r, q);
-}
-
 // The 8-bit codes need no norm: y / (max |y| / 448) is 448 z / max |z| with z = r weight, which is
 // exact in fp32 for 16-bit types.  So ties are ties, and one reduction gives sum and maximum.
 // A row is a CTA's: of kWarps warps, or (0) of as many as it has, kMost threads at most; with one warp a
@@ -233,7 +224,7 @@ __global__ void __launch_bounds__(kMost, kMost == 1024 ? 1 : 1536 / kMost)
       const bool ordinary = s > 0.f && top < INFINITY && r < INFINITY;
 #pragma unroll
       for (int k = 0; k < kRun; ++k)  // (0 where s is 0, but NaN stays NaN)
-        z[i][k] = ordinary ? quotient(z[i][k] * kMax8, top, r) : z[i][k] * inv * 0.f;
+        z[i][k] = ordinary ? kv4::quotient(z[i][k] * kMax8, top, r) : z[i][k] * inv * 0.f;
       const uint2 c = codes8(z[i]);
       if (out_wide && (run + 1) * kRun <= n) {
         *reinterpret_cast<uint2*>(out + run * kRun) = c;

@@ -1,74 +1,67 @@
 """The residual's addition and the root-mean-square norm of hidden states (``rb_add_rms_norm``)."""
 from __future__ import annotations
 
+import torch
+
 from . import _binding as rb
+from .kv4 import _device, _on, _stream, _wrong
 
-_KINDS = {}
+_KINDS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_E4M3 = 3
 
 
-def _kind(t) -> int:
-    import torch
+def _rows(name: str, t, rows: int, n: int, dtype, dev: int) -> int:
+    """The distance between rows of ``t`` [rows, n], whose values are adjacent."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != rows or shape[1] != n or t.dtype is not dtype or \
+            (stride[1] != 1 and n > 1) or t.get_device() != dev:
+        _wrong(name, t, f"[{rows}, {n}] {dtype}, the values of a row adjacent", dev)
+    return stride[0] if rows > 1 else n
 
-    if not _KINDS:
-        _KINDS.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
-    kind = _KINDS.get(t.dtype)
+
+def _norm(x, weight, eps, residual, residual_out, eight, group, out_dtype, out, scales, stream):
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, hidden]")
+    dtype = x.dtype
+    kind = _KINDS.get(dtype)
     if kind is None:
-        raise ValueError(f"x must be bf16, fp16 or fp32, got {t.dtype}")
-    return kind
-
-
-def _rows(name: str, t, like) -> int:
-    """The distance between rows of ``t``, shaped and typed as ``like``."""
-    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{name} must be {list(like.shape)} {like.dtype} on {like.device}, got "
-                         f"{list(t.shape)} {t.dtype} on {t.device}")
-    rows, n = t.shape
-    if n > 1 and t.stride(1) != 1:
-        raise ValueError(f"the values of a row of {name} must be adjacent")
-    return t.stride(0) if rows > 1 else n
-
-
-def _norm(x, weight, eps, residual, residual_out, out_kind, group, out_dtype, out, scales, stream):
-    import torch
-
-    if x.dim() != 2 or not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor [rows, hidden]")
-    kind = _kind(x)
+        raise ValueError(f"x must be bf16, fp16 or fp32, got {dtype}")
+    dev = _device("x", x)
     rows, n = x.shape
-    device = x.device
-    x_stride = _rows("x", x, x)
-    if weight.shape != (n,) or weight.dtype != x.dtype or weight.device != device or \
-            not weight.is_contiguous():
-        raise ValueError(f"weight must be [{n}] {x.dtype} on {device}")
-    on = rb._stream_on(device, stream)
-    if residual is None and residual_out is not None:
-        raise ValueError("residual_out without residual")
+    x_stride = _rows("x", x, rows, n, dtype, dev)
+    if weight.dtype is not dtype or weight.dim() != 1 or weight.shape[0] != n or \
+            not weight.is_contiguous() or weight.get_device() != dev:
+        _wrong("weight", weight, f"contiguous [{n}] {dtype}", dev)
+    on = _stream(dev, stream)
     res_at = after_at = None
     res_stride = after_stride = 0
     if residual is not None:
         if residual_out is None:
             residual_out = residual
-        res_stride = _rows("residual", residual, x)
-        after_stride = _rows("residual_out", residual_out, x)
+        res_stride = _rows("residual", residual, rows, n, dtype, dev)
+        after_stride = _rows("residual_out", residual_out, rows, n, dtype, dev)
         res_at, after_at = residual.data_ptr(), residual_out.data_ptr()
-    eight = out_kind == 3
-    width = (n // group if group and n % group == 0 else 1) if eight else 0
+    elif residual_out is not None:
+        raise ValueError("residual_out without residual")
+    width = n // group if group > 0 and n % group == 0 else 1
     if out is None or (eight and scales is None):
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+        with _on(stream):
             if out is None:
-                out = torch.empty((rows, n), dtype=out_dtype or x.dtype, device=device)
+                out = torch.empty((rows, n), dtype=out_dtype or dtype, device=x.device)
             if eight and scales is None:
-                scales = torch.empty((rows, width), dtype=torch.float32, device=device)
-    if out.shape != x.shape or out.dtype != (out_dtype or x.dtype) or out.device != device or \
-            not out.is_contiguous():
-        raise ValueError(f"out must be contiguous {[rows, n]} {out_dtype or x.dtype} on {device}")
-    if eight and (scales.shape != (rows, width) or scales.dtype != torch.float32 or
-                  scales.device != device or not scales.is_contiguous()):
-        raise ValueError(f"scales must be contiguous {[rows, width]} fp32 on {device}")
+                scales = torch.empty((rows, width), dtype=torch.float32, device=x.device)
+    _rows("out", out, rows, n, out_dtype or dtype, dev)
+    if not out.is_contiguous():
+        _wrong("out", out, "contiguous", dev)
+    scales_at = None
+    if eight:
+        _rows("scales", scales, rows, width, torch.float32, dev)
+        if not scales.is_contiguous():
+            _wrong("scales", scales, "contiguous", dev)
+        scales_at = scales.data_ptr()
     rb._check("rb_add_rms_norm", rb.lib.rb_add_rms_norm(
         rows, n, kind, x.data_ptr(), x_stride, res_at, res_stride, after_at, after_stride,
-        weight.data_ptr(), eps, 3 if eight else kind, group, out.data_ptr(),
-        scales.data_ptr() if eight else None, on))
+        weight.data_ptr(), eps, _E4M3 if eight else kind, group, out.data_ptr(), scales_at, on))
     return out, scales
 
 
@@ -77,7 +70,7 @@ def add_rms_norm(x, weight, eps: float = 1e-6, residual=None, residual_out=None,
     """r = x + residual, returned as r / sqrt(mean(r^2) + eps) * weight, row by row, in x's type
     (bf16, fp16 or fp32; [rows, hidden], rows any distance apart).  r goes to ``residual_out``
     (None: back into ``residual``); without a residual r is x."""
-    return _norm(x, weight, eps, residual, residual_out, None, 0, None, out, None, stream)[0]
+    return _norm(x, weight, eps, residual, residual_out, False, 0, None, out, None, stream)[0]
 
 
 def add_rms_norm_fp8(x, weight, eps: float = 1e-6, residual=None, residual_out=None,
@@ -85,7 +78,5 @@ def add_rms_norm_fp8(x, weight, eps: float = 1e-6, residual=None, residual_out=N
     """``add_rms_norm`` in 8 bits: (out, scales), out [rows, hidden] float8_e4m3fn whose product with
     its scale is the result; one scale a row (``group`` 0, scales [rows, 1]) or for every ``group``
     neighbouring values (16, 32, 64, 128 or 256; scales [rows, hidden / group])."""
-    import torch
-
-    return _norm(x, weight, eps, residual, residual_out, 3, group, torch.float8_e4m3fn, out,
+    return _norm(x, weight, eps, residual, residual_out, True, group, torch.float8_e4m3fn, out,
                  scales, stream)
