@@ -108,9 +108,9 @@ struct Turner {
     for (int i = 0; i < kPage / kTokens; ++i) {  // (rows 8 apart have the same swizzle)
       const uint4 c = *reinterpret_cast<const uint4*>(from + code + i * kTokens * (HD / 2));
       const uint8_t* sp = from + scale + i * kTokens * (kValues ? 1 : HD / 16);
-      const uint32_t s2 = kv4d::scales2(
-          kValues ? sp[0] | static_cast<uint32_t>(sp[kPage]) << 8
-                  : static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(sp)));
+      const uint32_t sb = kValues ? sp[0] | static_cast<uint32_t>(sp[kPage]) << 8
+                                  : static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(sp));
+      const uint32_t s2 = kv4d::scales2<0x4140>(sb);
       const uint32_t w[4] = {upper ? c.z : c.x, upper ? c.w : c.y, upper ? c.x : c.z,
                              upper ? c.y : c.w};
       const uint32_t m0 = __byte_perm(s2, 0, first), m1 = __byte_perm(s2, 0, second);
@@ -492,7 +492,7 @@ __device__ void softmax_kv4(const Kv4Args& g4, Kv4Shared& sh, uint32_t tmem, uin
     const bool partial = rows_used < C::kM || tok_base + a.tile_tokens > un.q;
     const bool releases = x == (un.n[1] > 0 ? 1 : 0);
     bool ok = true;
-    float scale = a.scale_log2;
+    float scale = a.scale_log2 * kv4d::kScaleUnit;
     if (n > 0) {  // this row of Q to fp16, in place
       if (!wait_all(&sh.q_full[x], uc_x & 1)) break;
       uint8_t* row = smem_ptr + K4::kQOffset + x * C::kQBytes + t * 128;
@@ -586,7 +586,7 @@ __device__ void softmax_kv4(const Kv4Args& g4, Kv4Shared& sh, uint32_t tmem, uin
       ++uc_x;
       tc_x += n;
       tc::fence_after_sync();
-      const float wa = l > 0.f ? g4.v_scale / l : l * 0.f;  // (NaN stays NaN)
+      const float wa = l > 0.f ? g4.v_scale * kv4d::kScaleUnit / l : l * 0.f;  // (NaN stays NaN)
       uint32_t pk[HD / 2];
 #pragma unroll
       for (int c = 0; c < HD / 32; ++c) {

@@ -64,38 +64,50 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
                             *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// Scale bytes 0 and 1 of `w` as a half2 (kv4::scale_value of each).
+// Scale bytes of `w` as a half2 (kv4::scale_value of each), times 2^-8: a byte's seven bits lie in a
+// half's fields as they are, the biases being 7 and 15.  A product with a code stays exact, down to
+// 2^-18 among fp16's subnormals.  kSelect names the bytes (byte_perm with 0: 0x4140 bytes 0 and
+// 1, 0x4040 byte 0 twice).
+constexpr float kScaleUnit = 256.f;
+template <int kSelect>
 __device__ __forceinline__ uint32_t scales2(uint32_t w) {
-  return hmul2((w & 0x7fu) << 7 | (w & 0x7f00u) << 15, 0x5c005c00u);  // times 256
+  return __byte_perm(w & 0x7f7f7f7fu, 0, kSelect) << 7;
 }
-__device__ __forceinline__ uint32_t low2(uint32_t w) { return __byte_perm(w, w, 0x1010); }
-__device__ __forceinline__ uint32_t high2(uint32_t w) { return __byte_perm(w, w, 0x3232); }
 
+// D = A B + C
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+                                        uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
+                                        float c2, float c3) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
-      " {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      " {%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// Geometry of a warp's ring: pages as they lie in the cache, but for the order of rows (and, in
-// rows of 64 bytes, of 16-byte chunks), which keeps the lanes' reads free of bank conflicts.
+// Geometry of a warp's ring: pages as they lie in the cache, but for the order of rows, which keeps the
+// lanes' reads free of bank conflicts and the places of a lane's copies a constant apart.
 //   K: the lanes' first rows, in order of g, then their second ones: lane's bytes at lane x hd / 8
-//   V: row 4t + i at t + 4i; chunk c of it at c ^ 2 for t >= 2 (hd 128)
+//   V: row 4t + i at row t % 2 + 2i of half t / 2, the halves 32 or 64 bytes apart
 template <int HD>
 struct Ring {
   static constexpr int kStages = 4;              // pages
-  static constexpr int kBytes = 9 * HD;          // K or V of a page
-  static constexpr int kStageBytes = 2 * kBytes;
-  static constexpr int kWarpBytes = kStages * kStageBytes;
   static constexpr int kRow = HD / 2;            // bytes of codes of a row
-  static constexpr int kCopies = (kBytes / 16 + 31) / 32;
+  static constexpr int kBytes = 9 * HD;          // K or V of a page in the cache
+  static constexpr int kVHalf = 8 * kRow + (HD == 128 ? 32 : 64);
+  static constexpr int kV = kBytes;              // V codes, K codes being at 0
+  static constexpr int kKScales = 16 * kRow, kVScales = kV + 2 * kVHalf;
+  static constexpr int kStageBytes = kVScales + HD;
+  static constexpr int kWarpBytes = kStages * kStageBytes;
+  static constexpr int kCopies = 16 * kRow / 512;  // of 16 bytes a lane: K (V) codes
+  static constexpr int kScaleLanes = HD / 16;      // lanes that copy the scales
 };
 
+template <int kTo, int kFrom>
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(kTo),
+               "n"(kFrom)
+               : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -103,52 +115,60 @@ __device__ __forceinline__ void copies_wait() {  // all but the last N groups ha
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Where chunk i of a page of K (V) goes in its stage.
-template <int HD, bool kValues>
-__device__ __forceinline__ int chunk_at(int i) {
-  constexpr int kPerRow = HD / 32;  // chunks of codes of a row
-  if (i >= 8 * HD / 16) return i * 16;  // scales stay where they are
-  const int r = i / kPerRow, c = i % kPerRow;
-  if (kValues) return ((r >> 2) + 4 * (r & 3)) * (HD / 2) + ((HD == 128 ? c ^ ((r >> 3) * 2) : c) << 4);
-  return (((r >> 2) * 2 + (r & 1)) + 8 * ((r >> 1) & 1)) * (HD / 2) + (c << 4);
+// Words of a ring at a shared-memory address and a constant distance.
+template <int kAt, int N>
+__device__ __forceinline__ void read_words(uint32_t (&r)[N], uint32_t at) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4 + %5];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at), "n"(kAt));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2 + %3];"
+                 : "=r"(r[0]), "=r"(r[1])
+                 : "r"(at), "n"(kAt));
+  else
+    asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(r[0]) : "r"(at), "n"(kAt));
+}
+template <int kAt, int kBytes>
+__device__ __forceinline__ uint32_t read_scales(uint32_t at) {
+  uint16_t v;
+  if constexpr (kBytes == 2)
+    asm volatile("ld.shared.u16 %0, [%1 + %2];" : "=h"(v) : "r"(at), "n"(kAt));
+  else
+    asm volatile("ld.shared.u8 %0, [%1 + %2];" : "=h"(v) : "r"(at), "n"(kAt));
+  return v;
 }
 
-template <int N>
-__device__ __forceinline__ void read_words(uint32_t (&r)[N], const uint8_t* p) {
-  if constexpr (N == 4) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    r[0] = w.x; r[1] = w.y; r[2] = w.z; r[3] = w.w;
-  } else if constexpr (N == 2) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    r[0] = w.x; r[1] = w.y;
-  } else {
-    r[0] = *reinterpret_cast<const uint32_t*>(p);
-  }
-}
-
-// S^T of the page whose K is at `k`: two chains of MMAs.
+// A lane's places in a stage: its K codes and scales, its V codes and scales.
 template <int HD>
-__device__ __forceinline__ void scores(const uint8_t* k, int lane, const uint32_t (&bq)[HD / 16][2],
-                                       float (&s)[4]) {
-  const int g = lane >> 2, t = lane & 3, key_g = 4 * (g >> 1) + (g & 1);
-  float s2[4] = {0.f, 0.f, 0.f, 0.f};
-  s[0] = s[1] = s[2] = s[3] = 0.f;
-  uint32_t c0[HD / 32], c1[HD / 32];
-  read_words(c0, k + lane * (HD / 8));
-  read_words(c1, k + 4 * HD + lane * (HD / 8));
-  const uint8_t* sp = k + 8 * HD + key_g * (HD / 16) + t * (HD / 64);
-  uint32_t sc0, sc1;
-  if constexpr (HD == 128) {
-    sc0 = scales2(*reinterpret_cast<const uint16_t*>(sp));
-    sc1 = scales2(*reinterpret_cast<const uint16_t*>(sp + 2 * (HD / 16)));
-  } else {
-    sc0 = scales2(*sp);
-    sc1 = scales2(*(sp + 2 * (HD / 16)));
+struct Places {
+  int k, k_scale, v, v_scale;
+  __device__ explicit Places(int lane) {
+    const int g = lane >> 2, t = lane & 3, key_g = 4 * (g >> 1) + (g & 1);
+    using R = Ring<HD>;
+    k = lane * (HD / 8);
+    k_scale = R::kKScales + key_g * (HD / 16) + t * (HD / 64);
+    v = R::kV + (t >> 1) * R::kVHalf + (t & 1) * R::kRow + g * (HD / 16);
+    v_scale = R::kVScales + g * (HD / 8) / 16 * 16 + 4 * t;
   }
+};
+
+// S^T of the page at `stage` (over kScaleUnit): two chains of MMAs.
+template <int HD>
+__device__ __forceinline__ void scores(uint32_t stage, const Places<HD>& at,
+                                       const uint32_t (&bq)[HD / 16][2], float (&s)[4]) {
+  uint32_t c0[HD / 32], c1[HD / 32];
+  read_words<0>(c0, stage + at.k);
+  read_words<8 * (HD / 2)>(c1, stage + at.k);
+  const uint32_t w0 = read_scales<0, HD / 64>(stage + at.k_scale);
+  const uint32_t w1 = read_scales<2 * (HD / 16), HD / 64>(stage + at.k_scale);
+  // (a lane's HD / 4 values are one block of 16 for HD 64, two for 128)
+  const uint32_t m00 = scales2<0x4040>(w0), m01 = HD == 128 ? scales2<0x4141>(w0) : 0u;
+  const uint32_t m10 = scales2<0x4040>(w1), m11 = HD == 128 ? scales2<0x4141>(w1) : 0u;
+  float s2[4];
 #pragma unroll
   for (int w = 0; w < HD / 32; ++w) {
-    // (a lane's HD / 4 values are one block of 16 for HD 64, two for 128)
-    const uint32_t m0 = w < 2 ? low2(sc0) : high2(sc0), m1 = w < 2 ? low2(sc1) : high2(sc1);
+    const uint32_t m0 = w < 2 ? m00 : m01, m1 = w < 2 ? m10 : m11;
     uint32_t x[4], y[4];
     kv4::values8(c0[w], x);
     kv4::values8(c1[w], y);
@@ -157,26 +177,30 @@ __device__ __forceinline__ void scores(const uint8_t* k, int lane, const uint32_
       x[i] = hmul2(x[i], m0);
       y[i] = hmul2(y[i], m1);
     }
-    mma_f16(s, x[0], y[0], x[1], y[1], bq[2 * w][0], bq[2 * w][1]);
-    mma_f16(s2, x[2], y[2], x[3], y[3], bq[2 * w + 1][0], bq[2 * w + 1][1]);
+    if (w == 0) {
+      mma_f16(s, x[0], y[0], x[1], y[1], bq[0][0], bq[0][1], 0.f, 0.f, 0.f, 0.f);
+      mma_f16(s2, x[2], y[2], x[3], y[3], bq[1][0], bq[1][1], 0.f, 0.f, 0.f, 0.f);
+    } else {
+      mma_f16(s, x[0], y[0], x[1], y[1], bq[2 * w][0], bq[2 * w][1], s[0], s[1], s[2], s[3]);
+      mma_f16(s2, x[2], y[2], x[3], y[3], bq[2 * w + 1][0], bq[2 * w + 1][1], s2[0], s2[1], s2[2],
+              s2[3]);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) s[i] += s2[i];
 }
 
-// O^T += V^T P^T of the page whose V is at `v`.
+// O^T += V^T P^T of the page at `stage` (V over kScaleUnit).
 template <int HD>
-__device__ __forceinline__ void add_values(const uint8_t* v, int lane, uint32_t pb0, uint32_t pb1,
-                                           float (&acc)[HD / 16][4]) {
-  const int g = lane >> 2, t = lane & 3;
-  const uint32_t sv = *reinterpret_cast<const uint32_t*>(
-      v + 8 * HD + (g * (HD / 8) / 16) * 16 + 4 * t);
-  const uint32_t s01 = scales2(sv), s23 = scales2(sv >> 16);
-  uint32_t c[4][HD / 64];
-  const int chunk = g * (HD / 16) / 16, in = g * (HD / 16) % 16;
-  const uint8_t* p = v + t * (HD / 2) + ((HD == 128 ? chunk ^ ((t >> 1) * 2) : chunk) << 4) + in;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) read_words(c[i], p + 4 * i * (HD / 2));
+__device__ __forceinline__ void add_values(uint32_t stage, const Places<HD>& at, uint32_t pb0,
+                                           uint32_t pb1, float (&acc)[HD / 16][4]) {
+  uint32_t sv[1], c[4][HD / 64];
+  read_words<0>(sv, stage + at.v_scale);
+  read_words<0>(c[0], stage + at.v);
+  read_words<2 * (HD / 2)>(c[1], stage + at.v);
+  read_words<4 * (HD / 2)>(c[2], stage + at.v);
+  read_words<6 * (HD / 2)>(c[3], stage + at.v);
+  const uint32_t s01 = scales2<0x4140>(sv[0]), s23 = scales2<0x4342>(sv[0]);
 #pragma unroll
   for (int w = 0; w < HD / 64; ++w) {
     // even and odd dims of a word, the first key of a pair in the low half of each byte
@@ -188,9 +212,11 @@ __device__ __forceinline__ void add_values(const uint8_t* v, int lane, uint32_t 
     kv4::values8(even(c[2][w], c[3][w]), e23);
     kv4::values8(odd(c[2][w], c[3][w]), o23);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      mma_f16(acc[4 * w + i], hmul2(e01[i], s01), hmul2(o01[i], s01), hmul2(e23[i], s23),
-              hmul2(o23[i], s23), pb0, pb1);
+    for (int i = 0; i < 4; ++i) {
+      float(&d)[4] = acc[4 * w + i];
+      mma_f16(d, hmul2(e01[i], s01), hmul2(o01[i], s01), hmul2(e23[i], s23), hmul2(o23[i], s23),
+              pb0, pb1, d[0], d[1], d[2], d[3]);
+    }
   }
 }
 
@@ -330,37 +356,44 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int w) {
     return x;
   };
   Window now = window(), next = window();
-  int pos = 0, to_copy = n, copy_slot = 0;
-  const uint32_t ring_at = smem_u32(ring);
-  const uint8_t* const k_src = g4.k + lane * 16;
-  const uint8_t* const v_src = g4.v + lane * 16;
-  const uint32_t page_stride = static_cast<uint32_t>(a.nkv) * kv4::page_bytes(HD);
-  int k_to[R::kCopies], v_to[R::kCopies];  // where this lane's chunks go in a stage
-#pragma unroll
-  for (int i = 0; i < R::kCopies; ++i) {
-    k_to[i] = chunk_at<HD, false>(lane + 32 * i);
-    v_to[i] = R::kBytes + chunk_at<HD, true>(lane + 32 * i);
-  }
+  int pos = 0, to_copy = n;
+  const uint32_t ring_at = smem_u32(ring), ring_end = ring_at + R::kWarpBytes;
+  uint32_t copy_to = ring_at;
+  const uint32_t page_stride = static_cast<uint32_t>(a.nkv) * R::kBytes;
+  const uint8_t *k_src, *v_src;  // this lane's chunks of page 0 of the window's head
+  auto sources = [&] {
+    k_src = g4.k + now.h * R::kBytes + lane * 16;
+    v_src = g4.v + now.h * R::kBytes + lane * 16;
+  };
+  sources();
+  // where this lane's first chunks of codes go in a stage (its second ones are rows 8 further on)
+  const int chunks = HD / 32, row = lane / chunks, in_row = lane % chunks * 16;
+  const int k_to = ((row >> 2) * 2 + (row & 1) + 8 * (row >> 1 & 1)) * R::kRow + in_row;
+  const int v_to = R::kV + (row >> 3) * R::kVHalf + ((row >> 2 & 1) + 2 * (row & 3)) * R::kRow + in_row;
   auto copy = [&]() {  // the next page; past the last one an empty group
     if (to_copy > 0) {
       --to_copy;
       if (pos == now.n) {
         now = next;
         pos = 0;
+        sources();
         next = window();
       }
       const uint32_t id = __shfl_sync(0xffffffffu, now.id, pos++);
-      const size_t off = static_cast<size_t>(id) * page_stride + now.h * kv4::page_bytes(HD);
-      const uint32_t to = ring_at + copy_slot * R::kStageBytes;
-      const uint8_t *ks = k_src + off, *vs = v_src + off;
-#pragma unroll
-      for (int c = 0; c < R::kCopies; ++c) {
-        if ((c + 1) * 32 <= R::kBytes / 16 || lane < R::kBytes / 16 - c * 32) {
-          copy16(to + k_to[c], ks + c * 512);
-          copy16(to + v_to[c], vs + c * 512);
-        }
+      const uint8_t* ks = k_src + static_cast<uint64_t>(id) * page_stride;
+      const uint8_t* vs = v_src + static_cast<uint64_t>(id) * page_stride;
+      copy16<0, 0>(copy_to + k_to, ks);
+      copy16<0, 0>(copy_to + v_to, vs);
+      if constexpr (R::kCopies == 2) {
+        copy16<4 * R::kRow, 512>(copy_to + k_to, ks);
+        copy16<R::kVHalf, 512>(copy_to + v_to, vs);
       }
-      copy_slot = copy_slot + 1 == R::kStages ? 0 : copy_slot + 1;
+      if (lane < R::kScaleLanes) {
+        copy16<R::kKScales, 16 * R::kRow>(copy_to + lane * 16, ks);
+        copy16<R::kVScales, 16 * R::kRow>(copy_to + lane * 16, vs);
+      }
+      copy_to += R::kStageBytes;
+      if (copy_to == ring_end) copy_to = ring_at;
     }
     copies_commit();
   };
@@ -368,7 +401,8 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int w) {
   for (int i = 0; i < R::kStages - 1; ++i) copy();
 
   const int key_g = 4 * (g >> 1) + (g & 1);  // key of the lane's first K row
-  int slot = 0;
+  const Places<HD> places(lane);
+  uint32_t stage = ring_at;
   for (int done = 0; done < n;) {  // segments: pages of one (request, kv head)
     const int r = at.r, h = at.h, first = at.page, pages = at.pages;
     const int seg = min(pages - first, n - done);
@@ -405,35 +439,40 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int w) {
     }
     // the lane's columns of S^T: their scales and their last visible key
     const int c0 = 2 * t, c1 = c0 + 1;
-    const float sc0 = __shfl_sync(0xffffffffu, up, 4 * c0) * a.scale_log2;
-    const float sc1 = __shfl_sync(0xffffffffu, up, 4 * c1) * a.scale_log2;
+    const float unit = a.scale_log2 * kScaleUnit;
+    const float sc0 = __shfl_sync(0xffffffffu, up, 4 * c0) * unit;
+    const float sc1 = __shfl_sync(0xffffffffu, up, 4 * c1) * unit;
     const int lim0 = c0 < cols ? c + c0 / a.group : c;
     const int lim1 = c1 < cols ? c + c1 / a.group : c;
+    // Exponents are taken against a reference m that moves only when a score exceeds it by more than
+    // kGrowth (log2 units), so that P stays below 2^(kPShift + kGrowth).  Kept beside it: the
+    // exponents' offset kPShift - m, and m + kGrowth in units of the raw products.
+    constexpr float kGrowth = 8.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float off0 = 0.f, off1 = 0.f, most0 = -INFINITY, most1 = -INFINITY;
     float acc[kKS][4];
 #pragma unroll
     for (int mt = 0; mt < kKS; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
+    // pages whose keys every column sees (the columns' last keys are c and more)
+    const int whole = min(first + seg, (c + 1) / kPage);
 #pragma unroll 1
     for (int page = first; page < first + seg; ++page) {
       copies_wait<R::kStages - 2>();
       __syncwarp();  // the page has landed for every lane, and every lane is done with the one before
       copy();
-      const uint8_t* stage = ring + slot * R::kStageBytes;
-      slot = slot + 1 == R::kStages ? 0 : slot + 1;
       float s[4];
-      scores<HD>(stage, lane, bq, s);
-      if (page * kPage + kPage - 1 > c) {  // (the columns' last keys are c and more)
+      scores<HD>(stage, places, bq, s);
+      if (page >= whole) {
         const int key = page * kPage + key_g;
         s[0] = key <= lim0 ? s[0] : -INFINITY;
         s[1] = key <= lim1 ? s[1] : -INFINITY;
         s[2] = key + 2 <= lim0 ? s[2] : -INFINITY;
         s[3] = key + 2 <= lim1 ? s[3] : -INFINITY;
       }
-      // exponents against a reference that moves only when a score exceeds it by more than
-      // kGrowth (log2 units), so that P stays below 2^(kPShift + kGrowth)
-      constexpr float kGrowth = 8.f;
-      float g0 = fmaxf(s[0], s[2]) * sc0, g1 = fmaxf(s[1], s[3]) * sc1;
-      if (__any_sync(0xffffffffu, g0 > m0 + kGrowth || g1 > m1 + kGrowth)) {
+      float g0 = fmaxf(s[0], s[2]), g1 = fmaxf(s[1], s[3]);
+      if (__any_sync(0xffffffffu, g0 > most0 || g1 > most1)) {
+        g0 *= sc0;
+        g1 *= sc1;
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
           g0 = fmaxf(g0, __shfl_xor_sync(0xffffffffu, g0, o));
@@ -450,15 +489,19 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int w) {
         }
         m0 = mn0;
         m1 = mn1;
+        off0 = m0 == -INFINITY ? 0.f : kPShift - m0;
+        off1 = m1 == -INFINITY ? 0.f : kPShift - m1;
+        most0 = (m0 + kGrowth) / sc0;
+        most1 = (m1 + kGrowth) / sc1;
       }
-      const float ms0 = m0 == -INFINITY ? 0.f : kPShift - m0;
-      const float ms1 = m1 == -INFINITY ? 0.f : kPShift - m1;
-      const float e0 = fast_exp2(fmaf(s[0], sc0, ms0)), e1 = fast_exp2(fmaf(s[1], sc1, ms1));
-      const float e2 = fast_exp2(fmaf(s[2], sc0, ms0)), e3 = fast_exp2(fmaf(s[3], sc1, ms1));
+      const float e0 = fast_exp2(fmaf(s[0], sc0, off0)), e1 = fast_exp2(fmaf(s[1], sc1, off1));
+      const float e2 = fast_exp2(fmaf(s[2], sc0, off0)), e3 = fast_exp2(fmaf(s[3], sc1, off1));
       l0 += e0 + e2;
       l1 += e1 + e3;
-      add_values<HD>(stage + R::kBytes, lane, movmatrix_trans(pack_f16x2(e0, e1)),
+      add_values<HD>(stage, places, movmatrix_trans(pack_f16x2(e0, e1)),
                      movmatrix_trans(pack_f16x2(e2, e3)), acc);
+      stage += R::kStageBytes;
+      if (stage == ring_end) stage = ring_at;
     }
 
 #pragma unroll
@@ -466,12 +509,13 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int w) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, o);
       l1 += __shfl_xor_sync(0xffffffffu, l1, o);
     }
+    const float v_unit = g4.v_scale * kScaleUnit;
     if (seg == pages) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int col = k == 0 ? c0 : c1;
         if (col >= cols) continue;
-        const float l = k == 0 ? l0 : l1, inv = l > 0.f ? g4.v_scale / l : l * 0.f;
+        const float l = k == 0 ? l0 : l1, inv = l > 0.f ? v_unit / l : l * 0.f;
         const int j = col / a.group, hh = col - j * a.group;
         uint4* o = reinterpret_cast<uint4*>(
             a.out + (static_cast<size_t>(t0 + j) * a.nh + h * a.group + hh) * HD + g * kPer);
@@ -490,8 +534,8 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int w) {
         float4* o = reinterpret_cast<float4*>(a.part_o + (piece * kMaxCols + col) * HD + g * kPer);
 #pragma unroll
         for (int v = 0; v < kPer / 4; ++v)
-          o[v] = make_float4(acc[2 * v][k] * g4.v_scale, acc[2 * v][k + 2] * g4.v_scale,
-                             acc[2 * v + 1][k] * g4.v_scale, acc[2 * v + 1][k + 2] * g4.v_scale);
+          o[v] = make_float4(acc[2 * v][k] * v_unit, acc[2 * v][k + 2] * v_unit,
+                             acc[2 * v + 1][k] * v_unit, acc[2 * v + 1][k + 2] * v_unit);
         if (g == 0)
           a.part_ml[piece * kMaxCols + col] = k == 0 ? make_float2(m0, l0) : make_float2(m1, l1);
       }

@@ -132,6 +132,16 @@ def test_queries_of_any_size(rb):
         b.check(b.run(rb, softmax_scale=scale), scale)
 
 
+@pytest.mark.parametrize("sb,size", [((0, 8), 300.0), ((0, 20), 60.0), ((120, 128), 0.002)])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_smallest_and_largest_scales(rb, hd, sb, size):
+    """Subnormal scales (2^-9 and up) and the largest ones (480), decodes and prompts."""
+    spec = wl.batch_from_lists([200, 77, 30], [1, 150, 2], num_q_heads=4, num_kv_heads=2,
+                               head_dim=hd, seed=9)
+    b = Batch(spec, 6, q_scale=size, sb=sb)
+    b.check(b.run(rb))
+
+
 def test_a_key_far_above_the_others_first_and_last(rb):
     """One key's score exceeds the others' by 2^5 to 2^20 in weight, at either end of a long
     sequence: the vanishing share of the many others is still theirs."""
