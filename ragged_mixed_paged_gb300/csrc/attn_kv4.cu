@@ -360,9 +360,9 @@ __device__ void mma_issuer4(const AttnArgs& a, Kv4Shared& sh, uint32_t tmem, uin
         const uint32_t ph_p = ph_s >> x & 1, ph_o = (ph_u >> x & 1) ^ 1;
         const bool ready = test(&sh.p_full[x], ph_p) & test(bar_v, ph_v) &
                            (!need_o || test(&sh.o_free[x], ph_o)) & (!next_s || test(bar_k, ph_k));
-        if (!ready && (!relaxed(&sh.p_full[x], ph_p) || !relaxed(bar_v, ph_v) ||
-                       (need_o && !relaxed(&sh.o_free[x], ph_o)) ||
-                       (next_s && !relaxed(bar_k, ph_k)))) {
+        // (P last: it comes last, and what is tested after it delays the MMAs)
+        if (!ready && (!relaxed(bar_v, ph_v) || (need_o && !relaxed(&sh.o_free[x], ph_o)) ||
+                       (next_s && !relaxed(bar_k, ph_k)) || !relaxed(&sh.p_full[x], ph_p))) {
           ok = false;
           break;
         }
