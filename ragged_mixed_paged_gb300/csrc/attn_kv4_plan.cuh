@@ -15,85 +15,79 @@ constexpr int kKv4MinPages = 4;
 
 // Validates the metadata, counts the decode requests' pages (a.dec_off: of one kv head, before each
 // request) and lists the prefill units longest first, divides the CTAs between the two, clears the
-// merge counters and writes the padding rows of the output as zeros.
+// merge counters and writes the padding rows of the output as zeros.  Requests are taken a thread
+// each, as many as there are threads at a time; of the prefill ones among them each is then a warp's,
+// whose lanes take its units (a request a lane, the fourteen of a small batch were one warp's: 9 us
+// instead of 7).
 __device__ __forceinline__ void kv4_plan_body(const AttnArgs& a, int head_dim, int warps_per_cta) {
-  __shared__ int s_longest, s_pre_max, s_bin[kTileBins];
+  constexpr int kMaxThreads = 1024;
+  __shared__ int s_longest, s_pre_max, s_pre_units, s_list, s_bin[kTileBins];
+  __shared__ int s_r[kMaxThreads], s_q[kMaxThreads], s_c[kMaxThreads];  // prefill requests
   __shared__ float s_pre_us;
-  const int tid = threadIdx.x, nthreads = blockDim.x, lane = tid & 31;
-  const int per = (a.R + nthreads - 1) / nthreads;  // the same for every thread
-  const int lo = min(tid * per, a.R), hi = min(lo + per, a.R);
+  const int tid = threadIdx.x, nthreads = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const ReqSrc src{a.qsl, a.seq_lens, nullptr};
-  // a thread's first requests are kept; the others are read again
-  constexpr int kCache = 2;
-  ReqInfo cache[kCache];
-#pragma unroll
-  for (int k = 0; k < kCache; ++k)
-    cache[k] = lo + k < hi ? req_info<false>(a, src, lo + k) : ReqInfo{false, 0, 0, 0};
-  auto get = [&](int k) {
-    return k == 0 ? cache[0] : k == 1 ? cache[1] : req_info<false>(a, src, lo + k);
-  };
   for (int i = tid; i < kTileBins; i += nthreads) s_bin[i] = 0;
   if (tid == 0) {
-    s_longest = s_pre_max = 0;
+    s_longest = s_pre_max = s_pre_units = s_list = 0;
     s_pre_us = 0.f;
   }
   int bits = tid == 0 && (a.qsl[0] != 0 || a.qsl[a.R] != a.N) ? RB_EBIT_ATTN_META : 0;
-  int pages = 0, pairs = 0, longest = 0;
-#pragma unroll 1
-  for (int k = 0; lo + k < hi; ++k) {
-    const ReqInfo x = get(k);
-    if (!x.ok) bits |= RB_EBIT_ATTN_META;
-    else if (is_decode_class(x.q, a.group)) {
-      pages += x.pages;
-      longest = max(longest, x.pages);
-    } else if (x.q > 0) {
-      pairs += prefill_pairs(x.q, a.tile_tokens);
+  __syncthreads();
+  auto is_prefill = [&](const ReqInfo& x) {
+    return x.ok && x.q > 0 && !is_decode_class(x.q, a.group);
+  };
+  auto put = [&](int r, const ReqInfo& x) {
+    if (!is_prefill(x)) return;
+    const int i = atomicAdd(&s_list, 1);
+    s_r[i] = r;
+    s_q[i] = x.q;
+    s_c[i] = x.L - x.q;
+  };
+  auto each_unit = [&](auto&& body) {  // body(r, key tiles, pair) of the listed requests
+    for (int i = warp; i < s_list; i += nthreads / 32) {
+      const int r = s_r[i], q = s_q[i], c = s_c[i], n = prefill_pairs(q, a.tile_tokens);
+      for (int p = lane; p < n; p += 32) body(r, pair_key_tiles(c, q, a.tile_tokens, p), p);
     }
-  }
-  int at, ex_pairs, total, total_pairs;
-  block_scan2(pages, pairs, &at, &ex_pairs, &total, &total_pairs);
+  };
+  int total = 0, longest = 0, most = 0, units = 0;
+  float us = 0.f;
 #pragma unroll 1
-  for (int k = 0; lo + k < hi; ++k) {
-    const ReqInfo x = get(k);
-    a.dec_off[lo + k] = at;
-    if (x.ok && is_decode_class(x.q, a.group)) at += x.pages;
-  }
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  if (lane == 0 && longest) atomicMax(&s_longest, longest);
-
-  if (total_pairs > 0) {  // a counting sort of the (request, pair) entries by key tiles
-    auto each_pair = [&](auto&& body) {  // body(r, key tiles, pair); a request's spread over a warp
-#pragma unroll 1
-      for (int k = 0; k < per; ++k) {
-        const ReqInfo x = lo + k < hi ? get(k) : ReqInfo{false, 0, 0, 0};
-        const int n = x.ok && x.q > 0 && !is_decode_class(x.q, a.group)
-                          ? prefill_pairs(x.q, a.tile_tokens) : 0;
-        for (unsigned m = __ballot_sync(0xffffffffu, n > 0); m; m &= m - 1) {
-          const int from = __ffs(m) - 1;
-          const int r = __shfl_sync(0xffffffffu, lo + k, from);
-          const int q = __shfl_sync(0xffffffffu, x.q, from);
-          const int c = __shfl_sync(0xffffffffu, x.L - x.q, from);
-          const int np = __shfl_sync(0xffffffffu, n, from);
-          for (int p = lane; p < np; p += 32) body(r, pair_key_tiles(c, q, a.tile_tokens, p), p);
-        }
-      }
-    };
-    float us = 0.f;
-    int most = 0;
-    each_pair([&](int, int n, int) {
+  for (int base = 0; base < a.R; base += nthreads) {
+    const int r = base + tid;
+    const ReqInfo x = r < a.R ? req_info<false>(a, src, r) : ReqInfo{true, 0, 0, 0};
+    if (!x.ok) bits |= RB_EBIT_ATTN_META;
+    const int pages = x.ok && is_decode_class(x.q, a.group) ? x.pages : 0;
+    longest = max(longest, pages);
+    put(r, x);
+    int at, none0, sum, none1;
+    block_scan2(pages, 0, &at, &none0, &sum, &none1);  // (with barriers: the list is whole)
+    if (r < a.R) a.dec_off[r] = total + at;
+    total += sum;
+    each_unit([&](int, int n, int) {
       atomicAdd(&s_bin[min(n, kTileBins - 1)], 1);
       us += kKv4UnitUs + kKv4TileUs * n;
       most = max(most, n);
+      ++units;
     });
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) us += __shfl_xor_sync(0xffffffffu, us, o);
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0 && most > 0) {
-      atomicAdd(&s_pre_us, us);
-      atomicMax(&s_pre_max, most);
-    }
     __syncthreads();
-    // bins in descending order: where each one's entries start in the list
+    if (base + nthreads < a.R && tid == 0) s_list = 0;
+    __syncthreads();
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  most = __reduce_max_sync(0xffffffffu, most);
+  units = __reduce_add_sync(0xffffffffu, units);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) us += __shfl_xor_sync(0xffffffffu, us, o);
+  if (lane == 0 && longest) atomicMax(&s_longest, longest);
+  if (lane == 0 && units) {
+    atomicMax(&s_pre_max, most);
+    atomicAdd(&s_pre_units, units);
+    atomicAdd(&s_pre_us, us);
+  }
+  __syncthreads();
+  const int total_pairs = s_pre_units;
+
+  if (total_pairs > 0) {  // a counting sort of the units by key tiles, longest first
     const int per_bin = (kTileBins + nthreads - 1) / nthreads;
     int count = 0, start, all, none0, none1;
     for (int i = 0; i < per_bin; ++i) {
@@ -109,9 +103,24 @@ __device__ __forceinline__ void kv4_plan_body(const AttnArgs& a, int head_dim, i
       start += c;
     }
     __syncthreads();
-    each_pair([&](int r, int n, int p) {
-      a.pre_list[atomicAdd(&s_bin[min(n, kTileBins - 1)], 1)] = r * 65536 + p;
-    });
+    auto list_units = [&] {
+      each_unit([&](int r, int n, int p) {
+        a.pre_list[atomicAdd(&s_bin[min(n, kTileBins - 1)], 1)] = r * 65536 + p;
+      });
+    };
+    if (a.R <= nthreads) {
+      list_units();
+    } else {  // the requests once more
+#pragma unroll 1
+      for (int base = 0; base < a.R; base += nthreads) {
+        __syncthreads();
+        if (tid == 0) s_list = 0;
+        __syncthreads();
+        if (base + tid < a.R) put(base + tid, req_info<false>(a, src, base + tid));
+        __syncthreads();
+        list_units();
+      }
+    }
   }
   __syncthreads();
   if (tid == 0) {

@@ -183,6 +183,16 @@ def test_rising_scores_move_the_reference(rb):
     b.check(b.run(rb))
 
 
+def test_more_requests_than_planner_threads(rb):
+    """1300 requests, most of one token, some of many and some of none."""
+    rng = np.random.default_rng(0)
+    new = np.where(rng.random(1300) < 0.1, rng.integers(3, 40, 1300), 1)
+    spec = wl.batch_from_lists(rng.integers(0, 60, 1300).tolist(), new.tolist(), num_q_heads=4,
+                               num_kv_heads=1, head_dim=64, seed=3)
+    b = Batch(spec)
+    b.check(b.run(rb))
+
+
 @pytest.mark.parametrize("ratio", [2, 4])
 @pytest.mark.parametrize("seed", range(4))
 def test_manager_blocks(rb, seed, ratio):
