@@ -91,7 +91,7 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 //   V: row 4t + i at row t % 2 + 2i of half t / 2, the halves 32 or 64 bytes apart
 template <int HD>
 struct Ring {
-  static constexpr int kStages = 4;              // pages
+  static constexpr int kStages = 6;              // pages; a step takes two
   static constexpr int kRow = HD / 2;            // bytes of codes of a row
   static constexpr int kBytes = 9 * HD;          // K or V of a page in the cache
   static constexpr int kVHalf = 8 * kRow + (HD == 128 ? 32 : 64);
@@ -397,8 +397,9 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int w) {
     }
     copies_commit();
   };
+  constexpr int kAhead = R::kStages - 2;  // pages copied beyond those that are done with
 #pragma unroll 1
-  for (int i = 0; i < R::kStages - 1; ++i) copy();
+  for (int i = 0; i < kAhead; ++i) copy();
 
   const int key_g = 4 * (g >> 1) + (g & 1);  // key of the lane's first K row
   const Places<HD> places(lane);
@@ -455,21 +456,31 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int w) {
     for (int mt = 0; mt < kKS; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
     // pages whose keys every column sees (the columns' last keys are c and more)
     const int whole = min(first + seg, (c + 1) / kPage);
+    // Two pages a step; the last one's second page may be missing: it is the first one again, unseen.
 #pragma unroll 1
-    for (int page = first; page < first + seg; ++page) {
-      copies_wait<R::kStages - 2>();
-      __syncwarp();  // the page has landed for every lane, and every lane is done with the one before
-      copy();
-      float s[4];
+    for (int page = first; page < first + seg; page += 2) {
+      copies_wait<kAhead - 2>();
+      __syncwarp();  // both have landed for every lane, and every lane is done with those before
+      uint32_t other = stage + R::kStageBytes;
+      if (other == ring_end) other = ring_at;
+      const bool both = page + 1 < first + seg;
+      if (!both) other = stage;
+      float s[4], u[4];
       scores<HD>(stage, places, bq, s);
-      if (page >= whole) {
+      scores<HD>(other, places, bq, u);
+      if (page + 1 >= whole) {
         const int key = page * kPage + key_g;
         s[0] = key <= lim0 ? s[0] : -INFINITY;
         s[1] = key <= lim1 ? s[1] : -INFINITY;
         s[2] = key + 2 <= lim0 ? s[2] : -INFINITY;
         s[3] = key + 2 <= lim1 ? s[3] : -INFINITY;
+        const int next = both ? key + kPage : 0x7ffffff0;
+        u[0] = next <= lim0 ? u[0] : -INFINITY;
+        u[1] = next <= lim1 ? u[1] : -INFINITY;
+        u[2] = next + 2 <= lim0 ? u[2] : -INFINITY;
+        u[3] = next + 2 <= lim1 ? u[3] : -INFINITY;
       }
-      float g0 = fmaxf(s[0], s[2]), g1 = fmaxf(s[1], s[3]);
+      float g0 = fmax3(fmaxf(s[0], s[2]), u[0], u[2]), g1 = fmax3(fmaxf(s[1], s[3]), u[1], u[3]);
       if (__any_sync(0xffffffffu, g0 > most0 || g1 > most1)) {
         g0 *= sc0;
         g1 *= sc1;
@@ -494,14 +505,24 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int w) {
         most0 = (m0 + kGrowth) / sc0;
         most1 = (m1 + kGrowth) / sc1;
       }
-      const float e0 = fast_exp2(fmaf(s[0], sc0, off0)), e1 = fast_exp2(fmaf(s[1], sc1, off1));
-      const float e2 = fast_exp2(fmaf(s[2], sc0, off0)), e3 = fast_exp2(fmaf(s[3], sc1, off1));
-      l0 += e0 + e2;
-      l1 += e1 + e3;
-      add_values<HD>(stage, places, movmatrix_trans(pack_f16x2(e0, e1)),
-                     movmatrix_trans(pack_f16x2(e2, e3)), acc);
-      stage += R::kStageBytes;
+      auto weights = [&](const float (&x)[4], uint32_t& b0, uint32_t& b1) {
+        const float e0 = fast_exp2(fmaf(x[0], sc0, off0)), e1 = fast_exp2(fmaf(x[1], sc1, off1));
+        const float e2 = fast_exp2(fmaf(x[2], sc0, off0)), e3 = fast_exp2(fmaf(x[3], sc1, off1));
+        l0 += e0 + e2;
+        l1 += e1 + e3;
+        b0 = movmatrix_trans(pack_f16x2(e0, e1));
+        b1 = movmatrix_trans(pack_f16x2(e2, e3));
+      };
+      uint32_t ps0, ps1, pu0, pu1;
+      weights(s, ps0, ps1);
+      weights(u, pu0, pu1);
+      add_values<HD>(stage, places, ps0, ps1, acc);
+      add_values<HD>(other, places, pu0, pu1, acc);
+      stage = other + R::kStageBytes;
       if (stage == ring_end) stage = ring_at;
+      __syncwarp();  // every lane is done with both
+      copy();
+      if (both) copy();
     }
 
 #pragma unroll
