@@ -7,8 +7,8 @@ namespace rb {
 namespace attn {
 
 // Finish-time model (this GPU, cold caches, heads of 128; fitted to whole-launch times): a CTA
-// decodes 12.5 pages of one kv head a microsecond, a prefill unit of n key tiles takes 6 + 2.7 n.
-constexpr float kKv4PagesPerUs = 12.5f, kKv4UnitUs = 6.f, kKv4TileUs = 2.7f;
+// decodes 14.5 pages of one kv head a microsecond, a prefill unit of n key tiles takes 6 + 2.4 n.
+constexpr float kKv4PagesPerUs = 14.5f, kKv4UnitUs = 6.f, kKv4TileUs = 2.4f;
 // Pages of a decode warp: at least kMinPages, and enough that a (request, kv head)'s pieces cost no
 // more to merge than its pages take (attn_plan.cuh's rule for splits).
 constexpr int kKv4MinPages = 4;
