@@ -802,7 +802,7 @@ rb_status rb_kv_append(const rb_dims* dims, int32_t num_tokens_padded,
  * 448), c = the code nearest to y / s (0 where s is 0), ties to the even one, quotients in fp32.
  * An infinity is held as the largest value, NaN as 0.
  * Errors: as rb_kv_append, RB_ERR_UNSUPPORTED for another block_size or head_dim and for nkv * hd
- * above 24576, RB_ERR_INVALID_ARG for a layer scale that is not positive and finite; device -> also
+ * above 24576, RB_ERR_INVALID_ARG for a layer scale outside [2^-100, 2^100]; device -> also
  * NOT_FINITE.
  */
 rb_status rb_kv4_append(const rb_dims* dims, int32_t num_tokens_padded,
@@ -827,8 +827,10 @@ rb_status rb_kv4_read(const rb_dims* dims, int32_t num_rows, const int32_t* d_sl
  * stands for (k_scale and v_scale included); they enter the products unrounded.
  * Arguments, layouts, workspace (rb_paged_attention_workspace_size), supported shapes and errors are
  * those of rb_paged_attention, with caches [num_blocks, nkv, 9 * hd] of bytes; RB_ERR_INVALID_ARG
- * also for a softmax_scale or layer scale that is not positive and finite.  What pages hold behind
- * a request's last token does not reach its rows.
+ * also for a softmax_scale that is not positive, a layer scale outside [2^-100, 2^100] and a product
+ * of softmax_scale and k_scale that fp32 does not hold; RB_ERR_CAPACITY also for more than 32768
+ * requests, 2^31 kernel pages in their block-table rows or num_tokens of 2^17 * floor(128 * nkv / nh)
+ * and more.  What pages hold behind a request's last token does not reach its rows.
  */
 rb_status rb_paged_attention_kv4(const rb_dims* dims, int32_t num_reqs, int32_t num_tokens,
                                  int32_t num_tokens_padded, const void* d_q,

@@ -763,9 +763,12 @@ extern "C" rb_status rb_paged_attention_kv4(
   if (st != RB_OK) return st;
   AttnArgs& a = su.a;
   const float scale = softmax_scale * k_scale * 1.4426950408889634f;
-  if (!(softmax_scale > 0.f) || !std::isfinite(k_scale) || !std::isfinite(v_scale) ||
-      !(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(scale) || !(scale > 0.f))
+  if (!(softmax_scale > 0.f) || !kv4::layer_scale_ok(k_scale) || !kv4::layer_scale_ok(v_scale) ||
+      !std::isfinite(scale * kv4d::kScaleUnit) || !(scale > 0.f))
     return RB_ERR_INVALID_ARG;
+  // the units' list holds 16 bits of request and 16 of tile pair, the decode stream 31 of pages
+  if (a.R > 32768 || a.N / (2 * a.tile_tokens) > 65535 || a.R * a.kp_cap > 0x7fffffffLL)
+    return RB_ERR_CAPACITY;
   a.scale_log2 = scale;
   if (a.N_pad > 0 &&
       !encode_q_tensor_map(&su.qmap, a.q, su.head_dim, a.nh, a.N_pad, a.group))

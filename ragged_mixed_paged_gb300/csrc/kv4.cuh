@@ -20,6 +20,10 @@ constexpr int kBlock = 16;  // values that share a scale
 
 __host__ __device__ constexpr int page_bytes(int hd) { return 9 * hd; }  // of one kv head
 
+// A layer's scale.  The range keeps it, its reciprocal and their products with what the kernels fold
+// into them (2^8, log2 e) ordinary fp32 numbers.
+inline bool layer_scale_ok(float s) { return s >= 0x1p-100f && s <= 0x1p100f; }
+
 // Byte offset of the codes of (slot, head, block of 16 values), 8 bytes, and of their scale.
 struct Place {
   size_t code, scale;

@@ -83,7 +83,8 @@ __device__ __forceinline__ bool put_block(const uint4& a, const uint4& b, const 
     const bool nan = y[i] != y[i];
     odd |= nan || fabsf(y[i]) > FLT_MAX;
     if (nan) y[i] = 0.f;
-    if (by.scale != 1.f) y[i] = kv4::quotient(y[i], by.scale, by.inverse);
+    if (by.scale != 1.f)  // (the quotient of -0 loses its sign, an infinite one is NaN)
+      y[i] = copysignf(kv4::quotient(y[i], by.scale, by.inverse), y[i]);
     if (!(fabsf(y[i]) <= FLT_MAX)) y[i] = copysignf(FLT_MAX, y[i]);
     top = fmaxf(top, fabsf(y[i]));
   }
@@ -346,9 +347,7 @@ rb_status kv4_checks(const rb_dims& d, float k_scale, float v_scale) {
   if (d.block_size != kv4::kPage || (d.head_dim != 64 && d.head_dim != 128))
     return RB_ERR_UNSUPPORTED;
   if (static_cast<long long>(d.num_blocks) * d.block_size > 0x7fffffffLL) return RB_ERR_CAPACITY;
-  if (!std::isfinite(k_scale) || !std::isfinite(v_scale) || !(k_scale > 0.f) || !(v_scale > 0.f))
-    return RB_ERR_INVALID_ARG;
-  return RB_OK;
+  return kv4::layer_scale_ok(k_scale) && kv4::layer_scale_ok(v_scale) ? RB_OK : RB_ERR_INVALID_ARG;
 }
 
 }  // namespace

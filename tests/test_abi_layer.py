@@ -77,6 +77,34 @@ def test_read_host_checks(lib):  # noqa: F811
         assert call(**{name: MISALIGNED}) == 1, name
 
 
+def test_attention_host_checks(lib):  # noqa: F811
+    def call(d=_dims(lib), reqs=2, tokens=3, padded=4, q=FAKE, kc=FAKE, vc=FAKE, table=FAKE,
+             loc=FAKE, lens=FAKE, scale=1.0, ks=1.0, vs=1.0, out=FAKE, ws=FAKE, size=1 << 40):
+        return lib.lib.rb_paged_attention_kv4(
+            None if d is None else ctypes.byref(d), reqs, tokens, padded, q, kc, vc, table, loc,
+            lens, scale, ks, vs, out, ws, size, None, None)
+
+    assert call(d=None) == 1 and call(reqs=-1) == 1 and call(tokens=-1) == 1 and call(padded=2) == 1
+    assert call(d=_dims(lib, block_size=32)) == 5 and call(d=_dims(lib, head_dim=96)) == 5
+    for name in ("q", "kc", "vc", "table", "loc", "lens", "out", "ws"):
+        assert call(**{name: None}) == 1, name
+    for name in ("q", "kc", "vc", "out", "ws"):
+        assert call(**{name: MISALIGNED}) == 1, name
+    assert call(size=256) == 2
+    for bad in (0.0, -1.0, float("inf"), float("nan"), 1e-31, 1e31):
+        assert call(ks=bad) == 1 and call(vs=bad) == 1, bad
+    for bad in (0.0, -1.0, float("inf"), float("nan")):
+        assert call(scale=bad) == 1, bad
+    assert call(scale=1e30, ks=1e7) == 1
+    many = _dims(lib, max_num_reqs=40000, max_blocks_per_req=4)
+    assert call(d=many, reqs=32769, tokens=32769, padded=32769) == 2
+    long = _dims(lib, max_num_reqs=2, max_blocks_per_req=1 << 30)
+    assert call(d=long) == 2
+    # a tile pair holds 2 * 128 / 16 tokens of a group of 16
+    wide = _dims(lib, num_q_heads=16, num_kv_heads=1)
+    assert call(d=wide, reqs=1, tokens=1 << 20, padded=1 << 20) == 2
+
+
 def test_norm_host_checks(lib):  # noqa: F811
     ODD = ctypes.c_void_p(0x100001)
 

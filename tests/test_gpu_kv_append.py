@@ -176,6 +176,49 @@ def test_extreme_values(rb, four):
         assert np.array_equal(sb[page, off], want[1])
 
 
+@pytest.mark.parametrize("k_scale,v_scale", [(0.25, 3.0), (2.0 ** -100, 2.0 ** 100), (1e-20, 7e19)])
+def test_extreme_values_over_a_layer_scale(rb, k_scale, v_scale):
+    """Infinities and quotients beyond fp32 keep their signs; NaN and 0 are 0."""
+    d = _dims(rb, 1, 1, 64)
+    c = Case(rb, d, 6, positions=1)
+    k = torch.zeros(6, 1, 64)
+    k[0, 0, 3], k[0, 0, 4], k[0, 0, 40] = float("inf"), -float("inf"), -float("inf")
+    k[1, 0, 17], k[1, 0, 18] = float("nan"), -float("nan")
+    k[2], k[3] = -3e38, 3e38
+    v = -k
+    k[4], v[4] = (torch.linspace(-7, 7, 64) * s for s in (k_scale, v_scale))
+    c.k, c.v = k.to(BF).cuda(), v.to(BF).cuda()
+    kc, vc = rb.kv4_cache(d)
+    rb.kv4_append(d, None, c.k, c.v, k_cache=kc, v_cache=vc, k_scale=k_scale, v_scale=v_scale,
+                  **c.args())
+    assert int(c.err.item()) == rb.EBIT_NOT_FINITE
+    for cache, x, scale, values in ((kc, c.k, k_scale, False), (vc, c.v, v_scale, True)):
+        code, sb = ref.unpack(cache.cpu().numpy(), 64, values)
+        page, off = c.slots // 16, c.slots % 16
+        want = ref.encode(_f(x), scale)
+        assert np.array_equal(sb[page, off], want[1])
+        # (a NaN's code is 0 of either sign)
+        nan = np.isnan(_f(x))
+        assert np.array_equal(code[page, off][~nan], want[0][~nan])
+        assert (code[page, off][nan] % 8 == 0).all()
+
+
+@pytest.mark.parametrize("bad", [0.0, -1.0, float("inf"), float("nan"), 1e-31, 1e31, 1e-39])
+def test_layer_scales_out_of_range(rb, bad):
+    d = _dims(rb, 1, 1, 64)
+    c = Case(rb, d, 4)
+    kc, vc = rb.kv4_cache(d)
+    a = c.args()
+    for scales in ((bad, 1.0), (1.0, bad)):
+        with pytest.raises(rb.RbError):
+            rb.kv4_append(d, None, c.k, c.v, k_cache=kc, v_cache=vc, k_scale=scales[0],
+                          v_scale=scales[1], **a)
+        with pytest.raises(rb.RbError):
+            rb.kv4_read(d, a["slot_mapping"], kc, vc, *scales)
+    torch.cuda.synchronize()
+    assert not kc.any() and not vc.any()
+
+
 @pytest.mark.parametrize("four", [False, True])
 def test_tokens_left_out(rb, four):
     """A position outside the table leaves its token out, a slot outside the pool its K and V."""
