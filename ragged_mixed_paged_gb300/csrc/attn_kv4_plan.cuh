@@ -23,13 +23,17 @@ __device__ __forceinline__ void kv4_plan_body(const AttnArgs& a, int head_dim, i
   constexpr int kMaxThreads = 1024;
   __shared__ int s_longest, s_pre_max, s_pre_units, s_list, s_bin[kTileBins];
   __shared__ int s_r[kMaxThreads], s_q[kMaxThreads], s_c[kMaxThreads];  // prefill requests
-  __shared__ float s_pre_us;
+  __shared__ unsigned s_pre_tiles;
   const int tid = threadIdx.x, nthreads = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const ReqSrc src{a.qsl, a.seq_lens, nullptr};
+  auto info = [&](int r) {  // (a length near 2^31, which rounding up to pages would overflow, is none)
+    if (a.seq_lens[r] > 0x7ffffff0) return ReqInfo{false, 0, 0, 0};
+    return req_info<false>(a, src, r);
+  };
   for (int i = tid; i < kTileBins; i += nthreads) s_bin[i] = 0;
   if (tid == 0) {
     s_longest = s_pre_max = s_pre_units = s_list = 0;
-    s_pre_us = 0.f;
+    s_pre_tiles = 0;
   }
   int bits = tid == 0 && (a.qsl[0] != 0 || a.qsl[a.R] != a.N) ? RB_EBIT_ATTN_META : 0;
   __syncthreads();
@@ -50,11 +54,11 @@ __device__ __forceinline__ void kv4_plan_body(const AttnArgs& a, int head_dim, i
     }
   };
   int total = 0, longest = 0, most = 0, units = 0;
-  float us = 0.f;
+  unsigned tiles = 0;  // (sums of integers: the plan does not depend on the atomics' order)
 #pragma unroll 1
   for (int base = 0; base < a.R; base += nthreads) {
     const int r = base + tid;
-    const ReqInfo x = r < a.R ? req_info<false>(a, src, r) : ReqInfo{true, 0, 0, 0};
+    const ReqInfo x = r < a.R ? info(r) : ReqInfo{true, 0, 0, 0};
     if (!x.ok) bits |= RB_EBIT_ATTN_META;
     const int pages = x.ok && is_decode_class(x.q, a.group) ? x.pages : 0;
     longest = max(longest, pages);
@@ -65,7 +69,7 @@ __device__ __forceinline__ void kv4_plan_body(const AttnArgs& a, int head_dim, i
     total += sum;
     each_unit([&](int, int n, int) {
       atomicAdd(&s_bin[min(n, kTileBins - 1)], 1);
-      us += kKv4UnitUs + kKv4TileUs * n;
+      tiles += n;
       most = max(most, n);
       ++units;
     });
@@ -76,16 +80,19 @@ __device__ __forceinline__ void kv4_plan_body(const AttnArgs& a, int head_dim, i
   longest = __reduce_max_sync(0xffffffffu, longest);
   most = __reduce_max_sync(0xffffffffu, most);
   units = __reduce_add_sync(0xffffffffu, units);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) us += __shfl_xor_sync(0xffffffffu, us, o);
+  tiles = __reduce_add_sync(0xffffffffu, tiles);
   if (lane == 0 && longest) atomicMax(&s_longest, longest);
   if (lane == 0 && units) {
     atomicMax(&s_pre_max, most);
     atomicAdd(&s_pre_units, units);
-    atomicAdd(&s_pre_us, us);
+    atomicAdd(&s_pre_tiles, tiles);
   }
   __syncthreads();
-  const int total_pairs = s_pre_units;
+  int total_pairs = s_pre_units;
+  if (total_pairs > max_prefill_pairs(a.R, a.N)) {  // rows that several requests claim: no list
+    total_pairs = 0;
+    bits |= RB_EBIT_ATTN_META;
+  }
 
   if (total_pairs > 0) {  // a counting sort of the units by key tiles, longest first
     const int per_bin = (kTileBins + nthreads - 1) / nthreads;
@@ -116,7 +123,7 @@ __device__ __forceinline__ void kv4_plan_body(const AttnArgs& a, int head_dim, i
         __syncthreads();
         if (tid == 0) s_list = 0;
         __syncthreads();
-        if (base + tid < a.R) put(base + tid, req_info<false>(a, src, base + tid));
+        if (base + tid < a.R) put(base + tid, info(base + tid));
         __syncthreads();
         list_units();
       }
@@ -132,7 +139,8 @@ __device__ __forceinline__ void kv4_plan_body(const AttnArgs& a, int head_dim, i
       // go on with prefill units, the shortest ones by then, so they are to be done with their own
       // after 3/4 of that.
       const float scale = static_cast<float>(head_dim) / 128.f;
-      const float dec = static_cast<float>(work) * scale / kKv4PagesPerUs, pre = s_pre_us * a.nkv;
+      const float dec = static_cast<float>(work) * scale / kKv4PagesPerUs;
+      const float pre = (kKv4UnitUs * total_pairs + kKv4TileUs * s_pre_tiles) * a.nkv;
       const float end = fmaxf((dec + pre) / ctas, kKv4UnitUs + kKv4TileUs * s_pre_max);
       decode_ctas = total_pairs == 0 ? ctas
                                      : min(ctas, static_cast<int>(dec / (0.75f * end)) + 1);

@@ -303,7 +303,7 @@ rb_status launch_norm(const NormArgs& a, cudaStream_t s) {
   const int runs = (a.hidden + kRun - 1) / kRun;
   const int warps = (runs + 63) / 64, rows = a.rows;
   if (a.wide) {
-    if (warps == 1) norm_kernel<T, 1, 128, 2, kOut, true><<<(rows + 3) / 4, 128, 0, s>>>(a);
+    if (warps == 1) norm_kernel<T, 1, 128, 2, kOut, true><<<(rows - 1) / 4 + 1, 128, 0, s>>>(a);
     else if (warps == 2) norm_kernel<T, 2, 64, 2, kOut, true><<<rows, 64, 0, s>>>(a);
     else if (warps == 4) norm_kernel<T, 4, 128, 2, kOut, true><<<rows, 128, 0, s>>>(a);
     else if (warps == 8) norm_kernel<T, 8, 256, 2, kOut, true><<<rows, 256, 0, s>>>(a);
@@ -312,7 +312,7 @@ rb_status launch_norm(const NormArgs& a, cudaStream_t s) {
     else if (warps <= 32) norm_kernel<T, 0, 1024, 2, kOut, true><<<rows, warps * 32, 0, s>>>(a);
     else norm_kernel<T, 0, 1024, 4, kOut, true><<<rows, (warps + 1) / 2 * 32, 0, s>>>(a);
   } else {
-    if (warps == 1) norm_kernel<T, 1, 128, 2, kOut, false><<<(rows + 3) / 4, 128, 0, s>>>(a);
+    if (warps == 1) norm_kernel<T, 1, 128, 2, kOut, false><<<(rows - 1) / 4 + 1, 128, 0, s>>>(a);
     else if (warps <= 16) norm_kernel<T, 0, 512, 2, kOut, false><<<rows, warps * 32, 0, s>>>(a);
     else if (warps <= 32) norm_kernel<T, 0, 1024, 2, kOut, false><<<rows, warps * 32, 0, s>>>(a);
     else norm_kernel<T, 0, 1024, 4, kOut, false><<<rows, (warps + 1) / 2 * 32, 0, s>>>(a);

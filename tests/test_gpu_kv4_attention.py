@@ -9,6 +9,8 @@ scores: hd roundings of a sum whose terms are together below S = max sum |q_i k_
 and ex2 (2^-22) less; twice (numerator and sum): 2^-10 w.  Weights below 2^-31 of a row's reference
 vanish: 2^-30 times keys times max |v| covers them.
 """
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
@@ -222,6 +224,27 @@ def test_invalid_pages_are_reported(rb):
         assert int(b.err.item()) & rb.EBIT_ATTN_META
 
 
+def test_rows_claimed_again_and_again_are_reported(rb):
+    """Every second request claims all rows, more of them than the list of tiles is made for; and a
+    length whose pages do not fit 32 bits."""
+    d = rb.Dims(16, 16, 1, 64, max_num_reqs=64, max_model_len=256, max_blocks_per_req=16,
+                num_blocks=20)
+    k, v = rb.kv4_cache(d)
+    q = torch.ones(256, 16, 64, dtype=BF, device="cuda")
+    table = torch.ones(64, 16, dtype=torch.int32, device="cuda")
+    loc = torch.tensor([0, 256] * 32 + [0], dtype=torch.int32, device="cuda")
+    lens = torch.full((64,), 256, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    rb.paged_attention_kv4(d, 64, 256, q, k, v, table, loc, lens, error_word=err)
+    assert int(err.item()) == rb.EBIT_ATTN_META
+    for new in (1, 40):
+        err.zero_()
+        loc = torch.tensor([0, new], dtype=torch.int32, device="cuda")
+        lens = torch.full((1,), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+        rb.paged_attention_kv4(d, 1, new, q[:new], k, v, table, loc, lens, error_word=err)
+        assert int(err.item()) == rb.EBIT_ATTN_META
+
+
 def test_empty_batches(rb):
     d = rb.Dims(16, 4, 2, 64, max_num_reqs=3, max_model_len=64, max_blocks_per_req=4, num_blocks=8)
     k, v = rb.kv4_cache(d)
@@ -277,6 +300,55 @@ def test_captured_with_a_workspace_of_its_own_and_replayed(rb):
         torch.cuda.synchronize()
         n.check(out)
         assert torch.equal(out, n.run(rb, stream=s))  # the same bits
+
+
+def test_pages_behind_32_bit_offsets_and_shared_ones(rb):
+    """Requests that share pages at the end of a cache whose byte offsets pass 2^31."""
+    spec = wl.batch_from_lists([300, 300, 40], [1, 90, 1], num_q_heads=16, num_kv_heads=8,
+                               head_dim=128, seed=4)
+    b = Batch(spec, 8)
+    d, shift, shared = b.d, 262144 - b.d.num_blocks, 17
+    b.keys[1][:shared * 16] = b.keys[0][:shared * 16]
+    b.values[1][:shared * 16] = b.values[0][:shared * 16]
+    table = np.where(spec.block_table >= 0, spec.block_table + shift, spec.block_table)
+    table[1, :shared] = table[0, :shared]
+    far = dataclasses.replace(d, num_blocks=262144)
+    a = list(b.args(table.astype(np.int32)))
+    caches = []
+    for c in a[4:6]:
+        big = torch.full((262144, *c.shape[1:]), 0x55, dtype=torch.uint8, device="cuda")
+        big[shift:] = c
+        caches.append(big)
+    out = rb.paged_attention_kv4(far, *a[1:4], *caches, *a[6:], error_word=b.err)
+    torch.cuda.synchronize()
+    assert int(b.err.item()) == 0
+    b.check(out)
+
+
+@pytest.mark.parametrize("c,q", [(250000, 1), (120000, 70), (65537, 2)])
+def test_long_sequences(rb, c, q):
+    spec = wl.batch_from_lists([c], [q], num_q_heads=2, num_kv_heads=1, head_dim=64, seed=1)
+    b = Batch(spec, 9, sb=(40, 48))
+    b.check(b.run(rb))
+
+
+def test_calls_on_two_streams_at_once(rb):
+    specs = [wl.random_batch(s, num_q_heads=8, num_kv_heads=2, head_dim=128, max_reqs=8, max_q=300,
+                             max_c=2000, decode_frac=0.5) for s in (1, 2)]
+    batches = [Batch(spec, i) for i, spec in enumerate(specs)]
+    want = [b.run(rb) for b in batches]
+    args = [b.args() for b in batches]
+    streams = [torch.cuda.Stream() for _ in batches]
+    got = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, b in enumerate(batches):
+            got[i].append(rb.paged_attention_kv4(*args[i], error_word=b.err, stream=streams[i]))
+    torch.cuda.synchronize()
+    for b, w, outs in zip(batches, want, got):
+        assert int(b.err.item()) == 0
+        b.check(w)
+        assert all(torch.equal(o, w) for o in outs)
 
 
 def test_it_is_the_attention_over_the_same_values(rb):
