@@ -792,8 +792,9 @@ rb_status rb_kv_append(const rb_dims* dims, int32_t num_tokens_padded,
  * fp32 number of a layer, which puts its values into the scales' range; 1 where they are of the
  * order of 0.01 to 1000).
  * Whole pages of such a cache are moved by rb_pages_copy and rb_pages_compact with dims whose
- * block_size is 1 and whose head_dim is 9 * hd / 2; after rb_pages_fork of another layer (its table,
- * with block_size 16) a partial page follows by rb_pages_copy, as it does for further layers.
+ * block_size is 1 and whose head_dim is 9 * hd / 2; after rb_pages_fork of a 16-bit layer (or a
+ * stand-in of one: 1 head of 8 values) a partial page follows by rb_pages_copy, as it does for
+ * further layers.
  */
 
 /*

@@ -155,7 +155,9 @@ def kv4_cache(dims: rb.Dims, device="cuda") -> tuple:
 
 def kv4_page_dims(dims: rb.Dims) -> rb.Dims:
     """``dims`` with which ``PagePool`` copies and compacts whole pages of a 4-bit cache (viewed as
-    ``kv4_pages``): a page is one token of 9 * head_dim / 2 values a head.  Not for ``fork``."""
+    ``kv4_pages``): a page is one token of 9 * head_dim / 2 values a head.  ``fork`` is for the pool of
+    a 16-bit layer, whose page table both follow, or, where every layer is in 4 bits, of a stand-in
+    of 16 bytes a token (1 head of 8 values); the 4-bit layers follow with ``copy``."""
     return rb.Dims(1, dims.num_q_heads, dims.num_kv_heads, 9 * dims.head_dim // 2,
                    dims.max_num_reqs, dims.max_model_len, dims.max_blocks_per_req,
                    dims.num_blocks, dims.null_block, dims.kernel_blocks_per_manager_block)
