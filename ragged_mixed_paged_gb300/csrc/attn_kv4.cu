@@ -676,6 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_alloc(&sh.tmem_base, C::kTmemCols);
     tc::tmem_relinquish();
   }
+  kv4_clear_padding(a, HD);  // (what ran before the planner is done)
   grid_wait();  // the planner's results
   if (tid == 0) sh.role_rank = atomicAdd(a.header + kHRoleNext, 1);
   tc::fence_before_sync();

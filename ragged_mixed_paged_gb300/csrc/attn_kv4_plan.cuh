@@ -13,9 +13,19 @@ constexpr float kKv4PagesPerUs = 14.5f, kKv4UnitUs = 6.f, kKv4TileUs = 2.4f;
 // more to merge than its pages take (attn_plan.cuh's rule for splits).
 constexpr int kKv4MinPages = 4;
 
+// Rows of padding tokens are written as zeros, by every CTA that calls this.
+__device__ __forceinline__ void kv4_clear_padding(const AttnArgs& a, int head_dim) {
+  const long long row16 = static_cast<long long>(a.nh) * head_dim * 2 / 16;
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
+  int4* out = reinterpret_cast<int4*>(a.out);
+  for (long long i = a.N * row16 + static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+       i < a.N_pad * row16; i += step)
+    out[i] = make_int4(0, 0, 0, 0);
+}
+
 // Validates the metadata, counts the decode requests' pages (a.dec_off: of one kv head, before each
-// request) and lists the prefill units longest first, divides the CTAs between the two, clears the
-// merge counters and writes the padding rows of the output as zeros.  Requests are taken a thread
+// request) and lists the prefill units longest first, divides the CTAs between the two and clears
+// the merge counters.  Requests are taken a thread
 // each, as many as there are threads at a time; of the prefill ones among them each is then a warp's,
 // whose lanes take its units (a request a lane, the fourteen of a small batch were one warp's: 9 us
 // instead of 7).
@@ -158,11 +168,7 @@ __device__ __forceinline__ void kv4_plan_body(const AttnArgs& a, int head_dim, i
     a.header[kHRoleNext] = 0;
   }
   for (int i = tid; i < a.R * a.nkv; i += nthreads) a.done[i] = 0;
-  // rows of padding tokens are written as zeros
-  const long long row16 = static_cast<long long>(a.nh) * head_dim * 2 / 16;
-  int4* out = reinterpret_cast<int4*>(a.out);
-  for (long long i = a.N * row16 + tid; i < a.N_pad * row16; i += nthreads)
-    out[i] = make_int4(0, 0, 0, 0);
+  if (a.R == 0) kv4_clear_padding(a, head_dim);  // (nothing else is launched)
   if (bits) raise_error(a.err, bits);
 }
 

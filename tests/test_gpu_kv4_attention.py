@@ -263,6 +263,23 @@ def test_empty_batches(rb):
     assert bool((out == 0).all())  # all values are 0
 
 
+@pytest.mark.parametrize("reqs", [0, 1, 3])
+@pytest.mark.parametrize("pad", [1, 700])
+def test_padding_rows_are_cleared(rb, reqs, pad):
+    new = [1, 40, 3][:reqs]
+    spec = wl.batch_from_lists([20, 5, 9][:reqs] or [0], new or [0], num_q_heads=6, num_kv_heads=2,
+                               head_dim=64, seed=1, num_tokens_padded=sum(new) + pad)
+    b = Batch(spec)
+    b.R = b.R if reqs else 0
+    out = torch.full_like(b.q, float("nan"))
+    args = list(b.args())
+    args[1] = b.R
+    rb.paged_attention_kv4(*args, out=out, error_word=b.err)
+    torch.cuda.synchronize()
+    assert int(b.err.item()) == 0
+    assert bool((out[sum(new):] == 0).all()) and bool(torch.isfinite(out).all())
+
+
 def test_not_finite_queries_stay_in_their_rows(rb):
     spec = wl.batch_from_lists([100, 60], [2, 90], num_q_heads=4, num_kv_heads=1, head_dim=64,
                                seed=1)
