@@ -55,7 +55,6 @@ struct Kv4Shared {
   TcUnit units[4];
   uint32_t tmem_base;
   int abort;
-  int role_rank;  // order in which the CTAs came: the first ones decode
 };
 
 __host__ __device__ constexpr uint32_t make_idesc_f16(int M, int N, bool b_mn_major) {
@@ -678,7 +677,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   kv4_clear_padding(a, HD);  // (what ran before the planner is done)
   grid_wait();  // the planner's results
-  if (tid == 0) sh.role_rank = atomicAdd(a.header + kHRoleNext, 1);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -687,9 +685,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The first CTAs take the decode requests' pages (the stream's warps spread over them); every CTA
   // then takes prefill units.
   const int decode_ctas = a.header[kHDecodeCtas];
-  if (sh.role_rank < decode_ctas) {
+  const int rank = static_cast<int>(blockIdx.x);
+  if (rank < decode_ctas) {
     decode_warp_kv4<HD>(g4, base_ptr + warp * kv4d::Ring<HD>::kWarpBytes,
-                        warp * decode_ctas + sh.role_rank);
+                        warp * decode_ctas + rank);
     fence_proxy_async_smem();  // the rings' ordinary accesses before the tiles' asynchronous ones
   }
   if (a.header[kHNumPrefillUnits] > 0) {

@@ -165,7 +165,6 @@ __device__ __forceinline__ void kv4_plan_body(const AttnArgs& a, int head_dim, i
     a.header[kHNumPrefillUnits] = total_pairs * a.nkv;
     a.header[kHPrefillNext] = 0;
     a.header[kHDecodeCtas] = decode_ctas;
-    a.header[kHRoleNext] = 0;
   }
   for (int i = tid; i < a.R * a.nkv; i += nthreads) a.done[i] = 0;
   if (a.R == 0) kv4_clear_padding(a, head_dim);  // (nothing else is launched)

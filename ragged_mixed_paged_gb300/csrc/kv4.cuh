@@ -62,9 +62,15 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 
 // a / b, correctly rounded for ordinary values: a product with the rounded reciprocal and one
 // correction by its exact remainder (Markstein 1990), three instructions once r = 1 / b is there.
+// The remainder is q b - a, so that the quotient of -0 is -0.
 __device__ __forceinline__ float quotient(float a, float b, float r) {
   const float q = a * r;
-  return fmaf(fmaf(-q, b, a), r, q);
+  return fmaf(-fmaf(q, b, -a), r, q);
+}
+__device__ __forceinline__ float2 quotient(float2 a, float b, float r) {
+  const float2 r2 = make_float2(r, r), q = __fmul2_rn(a, r2);
+  const float2 rest = __ffma2_rn(q, make_float2(b, b), make_float2(-a.x, -a.y));
+  return __ffma2_rn(rest, make_float2(-r, -r), q);
 }
 
 // The eight values of four bytes of codes as half2 (value 2i in the low half), exact.
