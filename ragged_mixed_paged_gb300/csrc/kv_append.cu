@@ -126,13 +126,14 @@ __device__ __forceinline__ bool put_block(const uint4& a, const uint4& b, const 
 // position and slot are known.  The 4-bit cache's keys pass through shared memory as bf16,
 // because the sixteen values that share a scale are not those of one thread's pairs.
 //
-// The 16-bit cache is HBM's (8192 tokens of 32 + 16 heads of 128: 0.85 of its copy rate).  The
-// 4-bit one has the codes' arithmetic as well, about 110 instructions a block, and the latency of a
-// CTA's steps: slot, table, keys, codes.  Eight CTAs an SM (64 registers, two heads at a time)
-// take 52 us for 8192 tokens of 32 + 16 heads, six with four heads at a time 58; a thread that
-// codes its own two halves of two blocks after a shuffle, without shared memory, 68.
+// The 16-bit cache is HBM's: 16384 tokens of 32 + 16 heads of 128, 403 MB, take 66 us (seven CTAs an
+// SM; six 70, five 77).  The 4-bit one has the codes' arithmetic as well, about 110 instructions a
+// block, and the latency of a CTA's steps: slot, table, keys, codes.  Eight CTAs an SM (64
+// registers, two heads at a time) take 52 us for 8192 tokens of 32 + 16 heads, six with four heads
+// at a time 58; a thread that codes its own two halves of two blocks after a shuffle, without shared
+// memory, 68.
 template <bool k4, int kBatch>
-__global__ void __launch_bounds__(kThreads, k4 ? 8 : 1) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, k4 ? 8 : 7) append_kernel(const AppendArgs a) {
   extern __shared__ uint4 s_keys[];  // k4: the token's rotated keys
   const int t = blockIdx.x;
   const int per_head = a.hd / 16, lanes = kThreads / per_head;
