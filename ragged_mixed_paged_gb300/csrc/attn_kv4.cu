@@ -83,17 +83,19 @@ struct Kv4Cfg {
 // token, four 16-byte stores each, of token `tok` and for heads of 128 of tok + 8.  A head of 128 has
 // its quarters in two blocks of the same banks: the upper two take their pieces in the order 2, 3,
 // 0, 1.  The places do not change, so they are worked out once.
-template <int HD, bool kValues>
+template <int HD>
 struct Turner {
   static constexpr int kParts = HD / 32, kTokens = 32 / kParts;
-  int code, scale, row, piece[4];  // bytes from the page; from the tile's row and in it
+  int code, scale, scale_run, scale_next, row, piece[4];  // bytes from the page; from the tile's row and in it
   uint32_t first, second;          // which of a run's two scales a piece takes (byte selectors)
   bool upper;
-  __device__ explicit Turner(int lane) {
+  __device__ Turner(int lane, bool values) {
     const int part = lane % kParts, tok = lane / kParts;
     upper = part >= 2;
     code = tok * (HD / 2) + part * 16;
-    scale = 8 * HD + (kValues ? 2 * part * kPage + tok : tok * (HD / 16) + 2 * part);
+    scale = 8 * HD + (values ? 2 * part * kPage + tok : tok * (HD / 16) + 2 * part);
+    scale_next = values ? kPage : 1;
+    scale_run = kTokens * (values ? 1 : HD / 16);
     row = (part >> 1) * (HD == 128 ? TcCfg<HD>::kHalfBytes : 0) + tok * 128;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -106,9 +108,8 @@ struct Turner {
 #pragma unroll
     for (int i = 0; i < kPage / kTokens; ++i) {  // (rows 8 apart have the same swizzle)
       const uint4 c = *reinterpret_cast<const uint4*>(from + code + i * kTokens * (HD / 2));
-      const uint8_t* sp = from + scale + i * kTokens * (kValues ? 1 : HD / 16);
-      const uint32_t sb = kValues ? sp[0] | static_cast<uint32_t>(sp[kPage]) << 8
-                                  : static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(sp));
+      const uint8_t* sp = from + scale + i * scale_run;
+      const uint32_t sb = sp[0] | static_cast<uint32_t>(sp[scale_next]) << 8;
       const uint32_t s2 = kv4d::scales2<0x4140>(sb);
       const uint32_t w[4] = {upper ? c.z : c.x, upper ? c.w : c.y, upper ? c.x : c.z,
                              upper ? c.y : c.w};
@@ -190,15 +191,15 @@ __device__ __forceinline__ void producer_raw(const Kv4Args& g4, Kv4Shared& sh, u
 }
 
 // A warp of the two that turn K (V): two pages of each half tile, into a ring of kStages tiles.
-template <int HD, bool kValues, int kStages>
-__device__ __forceinline__ void turn_tiles(const AttnArgs& a, Kv4Shared& sh, uint8_t* ring,
+template <int HD, int kStages>
+__device__ __forceinline__ void turn_tiles(const AttnArgs& a, Kv4Shared& sh, bool values, uint8_t* ring,
                                            const uint8_t* raw, uint64_t* full, uint64_t* empty) {
   using C = TcCfg<HD>;
   using K4 = Kv4Cfg<HD>;
   volatile int* abort = &sh.abort;
   constexpr int kBytes = 9 * HD, kHalf = C::kPagesPerTile / 2;
   const int lane = threadIdx.x & 31, page = (threadIdx.x >> 5 & 1) * (kHalf / 2);
-  const Turner<HD, kValues> turner(lane);
+  const Turner<HD> turner(lane, values);
   uint32_t it = 0, count = 0;
   auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {
     const bool done = tc_wait(bar, phase, abort, a);
@@ -215,12 +216,12 @@ __device__ __forceinline__ void turn_tiles(const AttnArgs& a, Kv4Shared& sh, uin
 #pragma unroll 1
     for (int i = 0; i < 2 * tiles; ++i, ++count) {
       const uint32_t tile = it + (i >> 1), st = tile % kStages, from = count % kRawSlots;
-      if (!wait(&sh.raw_full[kValues][from], (count / kRawSlots) & 1) ||
+      if (!wait(&sh.raw_full[values][from], (count / kRawSlots) & 1) ||
           ((i & 1) == 0 && !wait(&empty[st], ((tile / kStages) & 1) ^ 1))) {
         ok = false;
         break;
       }
-      const uint8_t* src = raw + (2 * from + kValues) * K4::kRawBytes;
+      const uint8_t* src = raw + (2 * from + values) * K4::kRawBytes;
 #pragma unroll 1
       for (int p = page; p < page + kHalf / 2; ++p)
         turner.page(src + p * kBytes,
@@ -228,7 +229,7 @@ __device__ __forceinline__ void turn_tiles(const AttnArgs& a, Kv4Shared& sh, uin
       if (i & 1) fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        tc::mbar_arrive(&sh.raw_empty[kValues][from]);
+        tc::mbar_arrive(&sh.raw_empty[values][from]);
         if (i & 1) tc::mbar_arrive(&full[st]);
       }
     }
@@ -704,12 +705,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         producer_q4<HD>(a, sh, base, &qmap);
       } else if (warp == 2) {
         producer_raw<HD>(g4, sh, base + K4::kRawOffset);
-      } else if (warp == kTurnWarp || warp == kTurnWarp + 1) {
-        turn_tiles<HD, false, K4::kStagesK>(a, sh, base_ptr, base_ptr + K4::kRawOffset, sh.k_full,
-                                            sh.k_empty);
-      } else if (warp > kTurnWarp) {
-        turn_tiles<HD, true, K4::kStagesV>(a, sh, base_ptr + K4::kVOffset,
-                                           base_ptr + K4::kRawOffset, sh.v_full, sh.v_empty);
+      } else if (warp >= kTurnWarp) {
+        const bool values = warp >= kTurnWarp + 2;
+        turn_tiles<HD, K4::kStagesK>(a, sh, values, base_ptr + (values ? K4::kVOffset : 0),
+                                     base_ptr + K4::kRawOffset, values ? sh.v_full : sh.k_full,
+                                     values ? sh.v_empty : sh.k_empty);
       }
       __syncwarp();
     } else {
