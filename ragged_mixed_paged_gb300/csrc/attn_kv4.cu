@@ -19,6 +19,14 @@
 // A tile is turned once for 256 query rows: 1/2 instruction a value and 4 bytes of shared
 // memory traffic, against 512 multiply-adds of the tensor core.
 // Values behind the sequence's end are finite whatever a page holds, so their zero weights suffice.
+//
+// What bounds a prefill unit: the chain of a side's steps.  A key tile takes 4400 cycles: softmax
+// 1850 (1024 of them ex2's rate for a row a thread), P V and the next S 1370 at the tensor core's
+// rate, the rest notices between the roles; the two sides in turn keep the tensor pipe at 0.53 of
+// its rate.  A prompt of 8192 tokens, 32 + 8 heads of 128: 536 us (1.02 PFLOP/s; 433 if nothing were
+// turned).  Measured against it: an issuer thread for each side 568; that, and steps of 64 keys with
+// S of the next one ahead, 592 (an MMA of 64 columns takes as long as one of 128, which reads as
+// much of A); two threads a row, all softmax warps on one side's tile at a time, 596 (ex2 bound).
 #include "attn_kv4_decode.cuh"
 #include "attn_kv4_plan.cuh"
 #include "attn_prefill_tc.cuh"
@@ -61,7 +69,8 @@ __host__ __device__ constexpr uint32_t make_idesc_f16(int M, int N, bool b_mn_ma
   return tc::make_idesc(M, N, b_mn_major) & ~((1u << 7) | (1u << 10));  // A and B fp16, not bf16
 }
 
-// The warps that turn tiles read the cache's bytes from rings of pages in shared memory.  Loops are kept rolled: straight-line code of several roles runs at the rate of
+// The warps that turn tiles read the cache's bytes from rings of pages in shared memory.  Loops are kept
+// rolled, and K and V share their code: straight-line code of several roles runs at the rate of
 // instruction fetch (a tile's half unrolled took 8000 cycles, ten times its instructions).
 template <int HD>
 struct Kv4Cfg {

@@ -7,10 +7,11 @@
 //   O^T[hd, 8 cols]     += V^T[hd, 16] . P^T[16, 8]
 // with mma.sync m16n8k16, fp16 in and fp32 accumulated.  Every value that the cache can hold is
 // exact in fp16 (two bits of a code times four of a scale, between 2^-10 and 2880), so K and V enter
-// the MMAs unrounded; Q is divided by a power of two per column, which keeps its 8 bits.
+// the MMAs unrounded (times 2^-8, kScaleUnit); Q is divided by a power of two per column, which keeps
+// its 8 bits.
 //
 // A page of one kv head is 9 hd contiguous bytes of K and as many of V.  A warp copies them to its
-// own ring in shared memory with 16-byte cp.async, kStages pages ahead, and each lane then reads the
+// own ring in shared memory with 16-byte cp.async, four pages ahead, and each lane then reads the
 // bytes that are its MMA operands.  The MMA does not mind which 16 values of head_dim (K) or
 // which dims and keys (V) a step takes, as long as both operands agree, so the order is chosen to
 // make a lane's bytes neighbours.  With g = lane / 4, t = lane % 4:
@@ -21,9 +22,13 @@
 //      shifts and masks for a word of eight: neighbouring codes then belong to neighbouring keys.
 // A lane so ends up with hd / 8 neighbouring values of two columns of the output.
 //
-// What bounds it: the codes' conversions.  A page costs 64 of them per lane (hd 128), two cycles
-// each on the pipe that also takes masks, shifts and comparisons, about 285 cycles a page of
-// 2304 bytes in all, where HBM delivers one to a quarter SM in 390.
+// Two pages a step: their chains of MMAs and exponentials overlap, and the tests of a step are made
+// once for both (256 decodes of 0.5 to 8 k 175 us with one, 167 with two).
+//
+// What bounds it: instruction issue.  A page costs about 340 instructions a warp (hd 128), 310 cycles
+// on the pipe of conversions, masks and shifts (64 conversions a lane, two cycles each); issue
+// slots are at 0.67, the pipe at 0.57, DRAM at 0.59 (decodes of one length, 256 of 4000 tokens: 5.2
+// TB/s, 0.77 of the copy rate).  A ring of 4, 5 or 6 pages makes no difference.
 #pragma once
 
 #include "attn_decode_warp.cuh"
