@@ -858,6 +858,7 @@ rb_status rb_paged_attention_kv4(const rb_dims* dims, int32_t num_reqs, int32_t 
  *   d_scales     [num_rows, hidden_size / group_size] fp32 ([num_rows, 1] for group_size 0)
  * Any alignment of whole elements; rows of 16-byte alignment are read and written 16 bytes at a
  * time.  hidden_size up to 32768; group_size 0, 16, 32, 64, 128 or 256, a divisor of hidden_size.
+ * Squares and their mean are fp32: where they overflow (values of 1e19) the row is 0.
  * A NaN makes its row NaN; an infinity becomes NaN (in 8 bits, with the values that share its scale)
  * and the rest of its row 0.
  * Errors: host -> RB_ERR_INVALID_ARG, RB_ERR_UNSUPPORTED.

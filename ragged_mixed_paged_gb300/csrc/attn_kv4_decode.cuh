@@ -27,8 +27,8 @@
 //
 // What bounds it: instruction issue.  A page costs about 340 instructions a warp (hd 128), 310 cycles
 // on the pipe of conversions, masks and shifts (64 conversions a lane, two cycles each); issue
-// slots are at 0.67, the pipe at 0.57, DRAM at 0.59 (decodes of one length, 256 of 4000 tokens: 5.2
-// TB/s, 0.77 of the copy rate).  A ring of 4, 5 or 6 pages makes no difference.
+// slots are at 0.65, the pipe at 0.55 (256 decodes of 4000 tokens: 5.2 TB/s, 0.77 of the copy rate).
+// A ring of 4, 5 or 6 pages makes no difference.
 #pragma once
 
 #include "attn_decode_warp.cuh"

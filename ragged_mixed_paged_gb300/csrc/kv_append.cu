@@ -128,10 +128,10 @@ __device__ __forceinline__ bool put_block(const uint4& a, const uint4& b, const 
 //
 // The 16-bit cache is HBM's: 16384 tokens of 32 + 16 heads of 128, 403 MB, take 66 us (seven CTAs an
 // SM; six 70, five 77).  The 4-bit one has the codes' arithmetic as well, about 110 instructions a
-// block, and the latency of a CTA's steps: slot, table, keys, codes.  Eight CTAs an SM (64
-// registers, two heads at a time) take 52 us for 8192 tokens of 32 + 16 heads, six with four heads
-// at a time 58; a thread that codes its own two halves of two blocks after a shuffle, without shared
-// memory, 68.
+// block, and the latency of a CTA's steps: slot, table, keys, codes (issue slots 0.63).  8192 tokens of
+// 32 + 16 heads, 177 MB, take 35 us alone.  With the read of their rows behind them they take 52 with
+// eight CTAs an SM (64 registers, two heads at a time), 58 with six and four heads at a time, and
+// 68 where a thread codes its own halves of two blocks after a shuffle, without shared memory.
 template <bool k4, int kBatch>
 __global__ void __launch_bounds__(kThreads, k4 ? 8 : 7) append_kernel(const AppendArgs a) {
   extern __shared__ uint4 s_keys[];  // k4: the token's rotated keys
