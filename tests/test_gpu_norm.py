@@ -150,3 +150,16 @@ def test_refusals(rb):
     with pytest.raises(ValueError):
         rb.add_rms_norm_fp8(x, w, group=128, scales=torch.empty(4, 1, device="cuda"))
     assert rb.add_rms_norm(x[:0], w).shape == (0, 256)
+
+
+def test_squares_beyond_fp32(rb):
+    """Rows whose squares overflow are 0, the others are as ever."""
+    x = torch.full((3, 256), 1e25, device="cuda")
+    x[1] = 2.0
+    w = torch.ones(256, device="cuda")
+    out = rb.add_rms_norm(x, w)
+    codes, scales = rb.add_rms_norm_fp8(x, w, group=64)
+    assert bool((out[[0, 2]] == 0).all()) and bool((codes.float()[[0, 2]] == 0).all())
+    assert bool((scales[[0, 2]] == 0).all()) and bool((codes[1].float() == 448).all())
+    # 4 + 1e-6 and its root within a few roundings of fp32
+    assert (out[1].double() - 2 / (4 + 1e-6) ** 0.5).abs().max().item() <= 8 * U
