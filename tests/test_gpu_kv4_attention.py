@@ -368,6 +368,21 @@ def test_calls_on_two_streams_at_once(rb):
         assert all(torch.equal(o, w) for o in outs)
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+def test_tiles_written_again_and_again(rb, hd):
+    """Prompts of many key tiles, whose two stages of K and V and whose Q are rewritten hundreds of
+    times a call: the right values, and the same bits every time."""
+    spec = wl.batch_from_lists([2900, 1500, 0], [700, 260, 900], num_q_heads=8, num_kv_heads=4,
+                               head_dim=hd, seed=6)
+    b = Batch(spec, 5)
+    args = b.args()
+    want = rb.paged_attention_kv4(*args, error_word=b.err)
+    b.check(want)
+    for _ in range(50):
+        assert torch.equal(rb.paged_attention_kv4(*args, error_word=b.err), want)
+    assert int(b.err.item()) == 0
+
+
 def test_it_is_the_attention_over_the_same_values(rb):
     """The 16-bit cache's attention over the rows that kv4_read gives."""
     spec = wl.random_batch(7, num_q_heads=8, num_kv_heads=2, head_dim=128, max_reqs=6, max_q=100,
