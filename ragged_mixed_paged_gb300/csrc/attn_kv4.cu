@@ -521,7 +521,7 @@ __device__ void softmax_kv4(const Kv4Args& g4, Kv4Shared& sh, uint32_t tmem, uin
       }
       float down, up;
       kv4d::power_of(top, &down, &up);
-      scale *= up;
+      scale = kv4d::score_scale(up, scale);
 #pragma unroll
       for (int i = 0; i < HD / 8; ++i) {
         uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};

@@ -31,6 +31,8 @@
 // A ring of 4, 5 or 6 pages makes no difference.
 #pragma once
 
+#include <cfloat>
+
 #include "attn_decode_warp.cuh"
 #include "kv4.cuh"
 
@@ -58,6 +60,14 @@ __device__ __forceinline__ void power_of(float top, float* down, float* up) {
   const bool odd = !(top < INFINITY);
   *down = odd ? 1.f : __uint_as_float((254u - e) << 23);
   *up = odd ? 1.f : __uint_as_float(e << 23);
+}
+
+// What turns a column's (row's) raw products into log2 units: 2^e times the call's factor, kept
+// above 0 and finite, so that neither a masked score (-inf) nor a raw score of 0 becomes NaN.  Raw
+// products are below 2^13: scores under the lower bound are 0 to within 2^-113.  They are multiples of
+// 2^-42 (of q's 2^-24 and the cache's 2^-18): above the upper one any two that differ are 2^58 apart.
+__device__ __forceinline__ float score_scale(float up, float unit) {
+  return fminf(fmaxf(up * unit, FLT_MIN), 0x1p100f);
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -446,8 +456,8 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int w) {
     // the lane's columns of S^T: their scales and their last visible key
     const int c0 = 2 * t, c1 = c0 + 1;
     const float unit = a.scale_log2 * kScaleUnit;
-    const float sc0 = __shfl_sync(0xffffffffu, up, 4 * c0) * unit;
-    const float sc1 = __shfl_sync(0xffffffffu, up, 4 * c1) * unit;
+    const float sc0 = score_scale(__shfl_sync(0xffffffffu, up, 4 * c0), unit);
+    const float sc1 = score_scale(__shfl_sync(0xffffffffu, up, 4 * c1), unit);
     const int lim0 = c0 < cols ? c + c0 / a.group : c;
     const int lim1 = c1 < cols ? c + c1 / a.group : c;
     // Exponents are taken against a reference m that moves only when a score exceeds it by more than

@@ -185,6 +185,34 @@ def test_rising_scores_move_the_reference(rb):
     b.check(b.run(rb))
 
 
+def _scaled_check(b, got, rows=None):
+    """As ``Batch.check``, in units of the values' layer scale."""
+    v = [x / b.v_scale for x in b.values]
+    out, weight = oracle_attention(to64(b.q), b.keys, v, b.qsl, b.lens)
+    g = got.double().cpu().numpy() / b.v_scale
+    top = max(np.abs(x).max() for x in v)
+    tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -11 + 2.0 ** -10) * weight + \
+        2.0 ** -30 * max(b.lens) * top
+    near = np.abs(g - out) <= tol
+    assert (near if rows is None else near[rows]).all()
+
+
+@pytest.mark.parametrize("k_scale", [2.0 ** -100, 2.0 ** -40, 1e-9])
+@pytest.mark.parametrize("nh,nkv,hd", [(4, 2, 64), (8, 1, 128), (6, 2, 128)])
+def test_rows_of_zeros_over_a_small_layer_scale(rb, k_scale, nh, nkv, hd):
+    """Their scores are 0 and the result is V's mean, whatever the scale; tiny rows are next to it.
+    Pages partly filled and odd counts of them, in one piece and in many; prompts."""
+    spec = wl.batch_from_lists([40, 5, 70, 1500, 0, 333], [1, 70, 2, 1, 130, 1], num_q_heads=nh,
+                               num_kv_heads=nkv, head_dim=hd, seed=5)
+    b = Batch(spec, 3, k_scale=k_scale)
+    b.q[::2] = 0
+    b.q[1::6] = (1e-38 * torch.randn(b.q[1::6].shape, device="cuda")).to(BF)
+    b.q[:, 0] = 0
+    _scaled_check(b, b.run(rb))
+    b.q.zero_()
+    _scaled_check(b, b.run(rb))
+
+
 def test_more_requests_than_planner_threads(rb):
     """1300 requests, most of one token, some of many and some of none."""
     rng = np.random.default_rng(0)
