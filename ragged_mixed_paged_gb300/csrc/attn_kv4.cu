@@ -411,27 +411,12 @@ __device__ __forceinline__ void store_weights(uint32_t at, const uint32_t (&p)[k
     tc::st16(at + 16 * c, *reinterpret_cast<const uint32_t(*)[16]>(p + 16 * c));
 }
 
-// A warp's rows take a new reference where their scores of columns [c0, c0 + kCols) exceed the old
-// one: O (if it holds anything), the sum and the row's P of the columns before move by a power of
-// two.  Out of line: rare, but for a row's first columns.
+// O (if it holds anything: S of this tile, issued after the tiles before, has landed) and P of the
+// tile's columns before c0, times alpha (in fp32: it may be below fp16's range).
 template <int HD>
-__device__ __noinline__ void move_reference(uint32_t col_s, uint32_t col_o, int c0, int seen,
-                                            float scale, bool has_o, float* m_ref, float* l) {
-  float top = -INFINITY;
-#pragma unroll 1
-  for (int c = 0; c < kCols; c += 16) {
-    uint32_t r[16];
-    tc::ld16(col_s + c0 + c, r);
-    tc::wait_ld();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float v = __uint_as_float(r[i]);
-      top = c0 + c + i < seen ? fmaxf(top, v) : top;
-    }
-  }
-  const float old = *m_ref, next = fmaxf(old, ceilf(top * scale));
-  const float alpha = next > old ? fast_exp2(old - next) : 1.f;
-  if (has_o) {  // O holds the tiles before: S of this one, issued after them, has landed
+__device__ __forceinline__ void rescale(uint32_t col_s, uint32_t col_o, int c0, bool has_o,
+                                        float alpha) {
+  if (has_o) {
 #pragma unroll 1
     for (int c = 0; c < HD; c += 16) {
       uint32_t r[16];
@@ -449,15 +434,81 @@ __device__ __noinline__ void move_reference(uint32_t col_s, uint32_t col_o, int 
     tc::ld16(col_s + c, r);
     tc::wait_ld();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {  // (fp32: alpha itself may be below fp16's range)
+    for (int i = 0; i < 16; ++i) {
       const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
       r[i] = kv4d::pack_f16x2(v.x * alpha, v.y * alpha);
     }
     tc::st16(col_s + c, r);
   }
+}
+
+// The two functions below are out of line.  They take a row's reference and sum by value and return
+// them: by address the loop that calls them keeps both in memory (a prompt of 8192 tokens 571 us
+// instead of 531).
+//
+// A warp's rows take a new reference where their scores of columns [c0, c0 + kCols) exceed the old
+// one: O, the sum and the row's P of the columns before move by a power of two.  Rare, but for a
+// row's first columns.
+template <int HD>
+__device__ __noinline__ float2 move_reference(uint32_t col_s, uint32_t col_o, int c0, int seen,
+                                              float scale, bool has_o, float old, float l) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < kCols; c += 16) {
+    uint32_t r[16];
+    tc::ld16(col_s + c0 + c, r);
+    tc::wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float v = __uint_as_float(r[i]);
+      top = c0 + c + i < seen ? fmaxf(top, v) : top;
+    }
+  }
+  const float next = fmaxf(old, ceilf(top * scale));
+  const float alpha = next > old ? fast_exp2(old - next) : 1.f;
+  rescale<HD>(col_s, col_o, c0, has_o, alpha);
   tc::wait_st();
-  *l *= alpha;
-  *m_ref = next;
+  return make_float2(next, l * alpha);
+}
+
+// Largest factor of the raw products (below 2^13) whose scores leave whole references exact in fp32.
+// (A row of 128 values of 16 at most has one of about 2^9, over k_scale 1.)
+constexpr float kNearScale = 0x1p11f;
+
+// P of a tile for a warp that has a row of a larger factor, whose scores may pass 2^24.  A reference is one of the raw products then, which is taken off
+// them before the factor, so that their differences keep their bits.
+template <int HD>
+__device__ __noinline__ float2 far_tile(uint32_t col_s, uint32_t col_o, int seen, float scale,
+                                        bool has_o, float ref, float l) {
+  constexpr float kGrowth = 8.f;  // P stays below 2^(kPShift + kGrowth)
+#pragma unroll 1
+  for (int c0 = 0; c0 < TcCfg<HD>::kN; c0 += kCols) {
+    float s[kCols], top = -INFINITY;
+    load_scores(col_s + c0, s);
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+      s[i] = c0 + i < seen ? s[i] : -INFINITY;
+      top = fmaxf(top, s[i]);
+    }
+    float alpha = 1.f;
+    if (top > -INFINITY && (ref == -INFINITY || (top - ref) * scale > kGrowth)) {
+      alpha = fast_exp2((ref - top) * scale);
+      ref = top;
+    }
+    l *= alpha;
+    if (__any_sync(0xffffffffu, alpha != 1.f)) rescale<HD>(col_s, col_o, c0, has_o, alpha);
+    const float base = ref == -INFINITY ? 0.f : ref;
+    uint32_t pk[kCols / 2];
+#pragma unroll
+    for (int i = 0; i < kCols / 2; ++i) {
+      const float p = fast_exp2(fmaf(s[2 * i] - base, scale, kPShift));
+      const float q = fast_exp2(fmaf(s[2 * i + 1] - base, scale, kPShift));
+      l += p + q;
+      pk[i] = kv4d::pack_f16x2(p, q);
+    }
+    store_weights(col_s + c0 / 2, pk);
+  }
+  return make_float2(ref, l);
 }
 
 // Softmax and epilogue of tile x (0 = A, 1 = B); thread t = row t of the tile = TMEM lane t.
@@ -535,7 +586,9 @@ __device__ void softmax_kv4(const Kv4Args& g4, Kv4Shared& sh, uint32_t tmem, uin
       fence_proxy_async_smem();
       arrive_warp(&sh.q_ready[x]);
     }
-    // running reference (log2 units, a whole number) and sum; a row without a query starts at 0
+    const bool far = __any_sync(0xffffffffu, valid && scale > kNearScale);
+    // running reference (log2 units, a whole number; if far, a raw product) and sum; a row without a
+    // query starts at 0
     float m_ref = valid ? -INFINITY : 0.f, l = 0.f;
     for (int j = 0; j < n; ++j) {
       const uint32_t tj = tc_x + j;
@@ -552,8 +605,13 @@ __device__ void softmax_kv4(const Kv4Args& g4, Kv4Shared& sh, uint32_t tmem, uin
       // keys of the tile that this row sees
       const int seen = masked ? lim + 1 - kv_base : C::kN;
       const float2 sc2 = make_float2(scale, scale);
+      if (far) {
+        const float2 next = far_tile<HD>(col_s, col_o, seen, scale, j > 0, m_ref, l);
+        m_ref = next.x;
+        l = next.y;
+      }
 #pragma unroll 1
-      for (int c0 = 0; c0 < C::kN; c0 += kCols) {
+      for (int c0 = far ? C::kN : 0; c0 < C::kN; c0 += kCols) {
         float s[kCols];
         load_scores(col_s + c0, s);
         if (masked) {
@@ -578,7 +636,9 @@ __device__ void softmax_kv4(const Kv4Args& g4, Kv4Shared& sh, uint32_t tmem, uin
         float sum = exponents();
         // the row's first columns, and any that exceed the reference by too much
         if (__any_sync(0xffffffffu, !(sum <= kSumLimit) || m_ref == -INFINITY)) {
-          move_reference<HD>(col_s, col_o, c0, seen, scale, j > 0, &m_ref, &l);
+          const float2 next = move_reference<HD>(col_s, col_o, c0, seen, scale, j > 0, m_ref, l);
+          m_ref = next.x;
+          l = next.y;
           sum = exponents();
         }
         l += sum;

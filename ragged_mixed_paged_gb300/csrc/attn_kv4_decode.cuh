@@ -31,8 +31,6 @@
 // A ring of 4, 5 or 6 pages makes no difference.
 #pragma once
 
-#include <cfloat>
-
 #include "attn_decode_warp.cuh"
 #include "kv4.cuh"
 
@@ -64,11 +62,13 @@ __device__ __forceinline__ void power_of(float top, float* down, float* up) {
 
 // What turns a column's (row's) raw products into log2 units: 2^e times the call's factor, kept
 // above 0 and finite, so that neither a masked score (-inf) nor a raw score of 0 becomes NaN.  Raw
-// products are below 2^13: scores under the lower bound are 0 to within 2^-113.  They are multiples of
+// products are below 2^13: scores under the lower bound are 0 to within 2^-87.  They are multiples of
 // 2^-42 (of q's 2^-24 and the cache's 2^-18): above the upper one any two that differ are 2^58 apart.
+// kNoReference is the offset of a column that has no reference yet: it puts any product far above one.
 __device__ __forceinline__ float score_scale(float up, float unit) {
-  return fminf(fmaxf(up * unit, FLT_MIN), 0x1p100f);
+  return fminf(fmaxf(up * unit, 0x1p-100f), 0x1p100f);
 }
+constexpr float kNoReference = 0x1p120f;
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
@@ -460,12 +460,14 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int w) {
     const float sc1 = score_scale(__shfl_sync(0xffffffffu, up, 4 * c1), unit);
     const int lim0 = c0 < cols ? c + c0 / a.group : c;
     const int lim1 = c1 < cols ? c + c1 / a.group : c;
-    // Exponents are taken against a reference m that moves only when a score exceeds it by more than
-    // kGrowth (log2 units), so that P stays below 2^(kPShift + kGrowth).  Kept beside it: the
-    // exponents' offset kPShift - m, and m + kGrowth in units of the raw products.
+    // Exponents are taken against a reference, one of the raw products, that moves only when one
+    // exceeds it by more than kGrowth (log2 units), so that P stays below 2^(kPShift + kGrowth).  It
+    // is taken off the raw products, so that their differences keep their bits however large the scores
+    // are; an offset in log2 units gives infinite weights from scores of 2^23 on.  (256 decodes 170 us,
+    // 167 with such an offset; the raw difference only for segments with a large factor is no faster.)
     constexpr float kGrowth = 8.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    float off0 = 0.f, off1 = 0.f, most0 = -INFINITY, most1 = -INFINITY;
+    const float2 sc = make_float2(sc0, sc1);
+    float2 off = make_float2(kNoReference, kNoReference), l = make_float2(0.f, 0.f);  // (-reference)
     float acc[kKS][4];
 #pragma unroll
     for (int mt = 0; mt < kKS; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
@@ -496,35 +498,29 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int w) {
         u[3] = next + 2 <= lim1 ? u[3] : -INFINITY;
       }
       float g0 = fmax3(fmaxf(s[0], s[2]), u[0], u[2]), g1 = fmax3(fmaxf(s[1], s[3]), u[1], u[3]);
-      if (__any_sync(0xffffffffu, g0 > most0 || g1 > most1)) {
-        g0 *= sc0;
-        g1 *= sc1;
+      const float2 above = __fmul2_rn(__fadd2_rn(make_float2(g0, g1), off), sc);
+      if (__any_sync(0xffffffffu, above.x > kGrowth || above.y > kGrowth)) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
           g0 = fmaxf(g0, __shfl_xor_sync(0xffffffffu, g0, o));
           g1 = fmaxf(g1, __shfl_xor_sync(0xffffffffu, g1, o));
         }
-        const float mn0 = fmaxf(m0, g0), mn1 = fmaxf(m1, g1);
-        const float al0 = fast_exp2(m0 - (mn0 == -INFINITY ? 0.f : mn0));
-        const float al1 = fast_exp2(m1 - (mn1 == -INFINITY ? 0.f : mn1));
-        l0 *= al0;
-        l1 *= al1;
+        const float2 old = off;
+        off = make_float2(fminf(old.x, -g0), fminf(old.y, -g1));
+        const float al0 = fast_exp2((off.x - old.x) * sc0), al1 = fast_exp2((off.y - old.y) * sc1);
+        l = __fmul2_rn(l, make_float2(al0, al1));
 #pragma unroll
         for (int mt = 0; mt < kKS; ++mt) {
           acc[mt][0] *= al0; acc[mt][1] *= al1; acc[mt][2] *= al0; acc[mt][3] *= al1;
         }
-        m0 = mn0;
-        m1 = mn1;
-        off0 = m0 == -INFINITY ? 0.f : kPShift - m0;
-        off1 = m1 == -INFINITY ? 0.f : kPShift - m1;
-        most0 = (m0 + kGrowth) / sc0;
-        most1 = (m1 + kGrowth) / sc1;
       }
       auto weights = [&](const float (&x)[4], uint32_t& b0, uint32_t& b1) {
-        const float e0 = fast_exp2(fmaf(x[0], sc0, off0)), e1 = fast_exp2(fmaf(x[1], sc1, off1));
-        const float e2 = fast_exp2(fmaf(x[2], sc0, off0)), e3 = fast_exp2(fmaf(x[3], sc1, off1));
-        l0 += e0 + e2;
-        l1 += e1 + e3;
+        const float2 shift = make_float2(kPShift, kPShift);
+        const float2 lo = __ffma2_rn(__fadd2_rn(make_float2(x[0], x[1]), off), sc, shift);
+        const float2 hi = __ffma2_rn(__fadd2_rn(make_float2(x[2], x[3]), off), sc, shift);
+        const float e0 = fast_exp2(lo.x), e1 = fast_exp2(lo.y);
+        const float e2 = fast_exp2(hi.x), e3 = fast_exp2(hi.y);
+        l = __fadd2_rn(l, __fadd2_rn(make_float2(e0, e1), make_float2(e2, e3)));
         b0 = movmatrix_trans(pack_f16x2(e0, e1));
         b1 = movmatrix_trans(pack_f16x2(e2, e3));
       };
@@ -540,6 +536,7 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int w) {
       if (both) copy();
     }
 
+    float l0 = l.x, l1 = l.y;
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, o);
@@ -573,7 +570,9 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int w) {
           o[v] = make_float4(acc[2 * v][k] * v_unit, acc[2 * v][k + 2] * v_unit,
                              acc[2 * v + 1][k] * v_unit, acc[2 * v + 1][k + 2] * v_unit);
         if (g == 0)
-          a.part_ml[piece * kMaxCols + col] = k == 0 ? make_float2(m0, l0) : make_float2(m1, l1);
+          a.part_ml[piece * kMaxCols + col] =
+              k == 0 ? make_float2(l0 == 0.f ? -INFINITY : -off.x * sc0, l0)
+                     : make_float2(l1 == 0.f ? -INFINITY : -off.y * sc1, l1);
       }
       // the last piece of this (request, kv head) to finish merges all of them
       const long long begin = static_cast<long long>(a.dec_off[r]) * a.nkv +

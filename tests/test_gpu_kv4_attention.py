@@ -213,6 +213,72 @@ def test_rows_of_zeros_over_a_small_layer_scale(rb, k_scale, nh, nkv, hd):
     _scaled_check(b, b.run(rb))
 
 
+@pytest.mark.parametrize("q_size,k_scale", [(1e5, 1.0), (3e7, 1.0), (1e12, 1.0), (1e30, 1.0),
+                                            (1.0, 1e30), (1e30, 2.0 ** 100), (1e35, 2.0 ** 100)])
+@pytest.mark.parametrize("nh,nkv,hd", [(4, 2, 64), (8, 1, 128)])
+def test_scores_of_any_size(rb, q_size, k_scale, nh, nkv, hd):
+    """Scores from 1e6 to 1e66: a row is the value of its largest score, exactly, and rows of zeros
+    among them are V's mean.  Sums of fp32 (hd roundings of terms together below S: 2^-24 hd S) tell the
+    two largest scores of a row apart in the rows that are compared."""
+    spec = wl.batch_from_lists([40, 5, 70, 1500, 0, 333], [1, 70, 2, 1, 130, 1], num_q_heads=nh,
+                               num_kv_heads=nkv, head_dim=hd, seed=5)
+    b = Batch(spec, 3, k_scale=k_scale, v_scale=4.0)
+    b.q = (q_size * torch.randn(b.q.shape, generator=torch.Generator(device="cuda").manual_seed(2),
+                                device="cuda")).to(BF)
+    b.q[3::7] = 0
+    got = b.run(rb)
+    assert bool(torch.isfinite(got).all())
+    rows = np.zeros(b.q.shape[:2], bool)
+    q = to64(b.q)
+    for i in range(b.R):
+        for t in range(b.qsl[i], b.qsl[i + 1]):
+            n = b.lens[i] - (b.qsl[i + 1] - 1 - t)
+            for h in range(nh):
+                k = b.keys[i][:n, h // (nh // nkv)]
+                s = np.sort(k @ q[t, h]) * hd ** -0.5
+                size = (np.abs(k) @ np.abs(q[t, h])).max() * hd ** -0.5
+                gap = s[-1] - s[-2] if n > 1 else np.inf
+                rows[t, h] = size == 0 or gap > max(100.0, 2.0 ** -22 * hd * size)
+    assert rows[:b.N].mean() > 0.9
+    _scaled_check(b, got, rows)
+
+
+def test_equal_scores_of_any_size(rb):
+    """Keys that are all the same have the same weight, however large their scores are."""
+    spec = wl.batch_from_lists([40, 70, 1500, 0], [1, 2, 1, 200], num_q_heads=4, num_kv_heads=2,
+                               head_dim=64, seed=5)
+    for size, k_scale in ((1e6, 1.0), (3e8, 1.0), (1e30, 1.0), (1e30, 2.0 ** 100)):
+        for sign in (1, -1):
+            b = Batch(spec, 3, k_scale=k_scale)
+            code, s = (x.copy() for x in ref.unpack(b.k, 64, False))
+            code[:], s[:] = 5, 57
+            b.k = ref.pack(code, s, False)
+            for k in b.keys:
+                k[:] = 3 * 1.125 * k_scale
+            b.q = torch.full_like(b.q, sign * size)
+            b.q[::5] = 0
+            _scaled_check(b, b.run(rb))
+
+
+def test_rising_scores_beyond_24_bits(rb):
+    """Scores that climb from 1e2 past 1e9 and fall again: a row is the value of the largest one."""
+    spec = wl.batch_from_lists([1500, 900], [1, 600], num_q_heads=4, num_kv_heads=2, head_dim=128,
+                               seed=2)
+    for top in (1e4, 1e6, 1e9):
+        for sign in (1.0, -1.0):
+            b = Batch(spec, 4, sb=(40, 48))
+            code, s = (x.copy() for x in ref.unpack(b.k, 128, False))
+            for i in range(2):
+                p = np.arange(b.lens[i])
+                page, off = spec.block_table[i, p // 16], p % 16
+                code[page, off] = 2
+                s[page, off] = (8 + 8 * (p // 16 * 7 % 12) + p % 8)[:, None, None]
+                b.keys[i][:] = ref.decode(code[page, off], s[page, off])
+            b.k = ref.pack(code, s, False)
+            b.q = torch.full_like(b.q, sign * top / 128)
+            _scaled_check(b, b.run(rb))
+
+
 def test_more_requests_than_planner_threads(rb):
     """1300 requests, most of one token, some of many and some of none."""
     rng = np.random.default_rng(0)
