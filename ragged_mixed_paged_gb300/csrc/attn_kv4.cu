@@ -475,8 +475,9 @@ __device__ __noinline__ float2 move_reference(uint32_t col_s, uint32_t col_o, in
 // (A row of 128 values of 16 at most has one of about 2^9, over k_scale 1.)
 constexpr float kNearScale = 0x1p11f;
 
-// P of a tile for a warp that has a row of a larger factor, whose scores may pass 2^24.  A reference is one of the raw products then, which is taken off
-// them before the factor, so that their differences keep their bits.
+// P of a tile for a warp that has a row of a larger factor, whose scores may pass 2^24.  A reference is
+// one of the raw products then, which is taken off them before the factor, so that their differences
+// keep their bits.
 template <int HD>
 __device__ __noinline__ float2 far_tile(uint32_t col_s, uint32_t col_o, int seen, float scale,
                                         bool has_o, float ref, float l) {

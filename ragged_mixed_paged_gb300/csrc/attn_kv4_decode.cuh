@@ -239,10 +239,12 @@ __device__ __forceinline__ void add_values(uint32_t stage, const Places<HD>& at,
 
 // Log-sum-exp merge of the pieces of one (request, kv head) by one warp, kLanes lanes per column,
 // each lane owning that part of head_dim.  Piece 0 is the last one of its warp, the others are the
-// first of theirs.  Partials of other SMs are read through L2, 16 loads in flight.
+// first of theirs.  Partials of other SMs are read through L2, 16 loads in flight.  They are sums of
+// weights of up to 2^(kPShift + 8) over V without its scale `v_unit`, which would take them out of
+// fp32's range before the division.
 template <int HD, int kLanes>
 __device__ __forceinline__ void merge_pieces(const AttnArgs& a, int w0, int n, int h, int t0,
-                                             int cols) {
+                                             int cols, float v_unit) {
   constexpr int kPer = HD / kLanes, kVec = kPer / 4, kBatch = 16 / kVec;
   const int lane = threadIdx.x & 31;
   const int col = lane / kLanes, part = lane % kLanes;
@@ -287,7 +289,7 @@ __device__ __forceinline__ void merge_pieces(const AttnArgs& a, int w0, int n, i
   }
   if (!active) return;
   const int j = col / a.group, hh = col - j * a.group;
-  const float inv = sum > 0.f ? 1.f / sum : sum * 0.f;  // (NaN stays NaN)
+  const float inv = sum > 0.f ? v_unit / sum : sum * 0.f;  // (NaN stays NaN)
   uint2* dst = reinterpret_cast<uint2*>(
       a.out + (static_cast<size_t>(t0 + j) * a.nh + h * a.group + hh) * HD + part * kPer);
 #pragma unroll
@@ -567,8 +569,8 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int w) {
         float4* o = reinterpret_cast<float4*>(a.part_o + (piece * kMaxCols + col) * HD + g * kPer);
 #pragma unroll
         for (int v = 0; v < kPer / 4; ++v)
-          o[v] = make_float4(acc[2 * v][k] * v_unit, acc[2 * v][k + 2] * v_unit,
-                             acc[2 * v + 1][k] * v_unit, acc[2 * v + 1][k + 2] * v_unit);
+          o[v] = make_float4(acc[2 * v][k], acc[2 * v][k + 2], acc[2 * v + 1][k],
+                             acc[2 * v + 1][k + 2]);
         if (g == 0)
           a.part_ml[piece * kMaxCols + col] =
               k == 0 ? make_float2(l0 == 0.f ? -INFINITY : -off.x * sc0, l0)
@@ -585,8 +587,8 @@ __device__ void decode_warp_kv4(const Kv4Args& g4, uint8_t* ring, int w) {
       prev = __shfl_sync(0xffffffffu, prev, 0);
       if (prev == pieces - 1) {
         __threadfence();
-        if (cols <= 4) merge_pieces<HD, 8>(a, w0, pieces, h, t0, cols);
-        else merge_pieces<HD, 4>(a, w0, pieces, h, t0, cols);
+        if (cols <= 4) merge_pieces<HD, 8>(a, w0, pieces, h, t0, cols, v_unit);
+        else merge_pieces<HD, 4>(a, w0, pieces, h, t0, cols, v_unit);
       }
     }
   }

@@ -279,6 +279,21 @@ def test_rising_scores_beyond_24_bits(rb):
             _scaled_check(b, b.run(rb))
 
 
+@pytest.mark.parametrize("c", [3000, 250000])
+@pytest.mark.parametrize("v_scale", [2.0 ** 100, 2.0 ** -100])
+def test_values_of_the_largest_size_in_many_pieces(rb, c, v_scale):
+    """V's largest value everywhere and a layer scale at the end of its range: the sums of a piece do
+    not fit fp32 with the scale in them, the result does and is exact."""
+    spec = wl.batch_from_lists([c, 700], [1, 40], num_q_heads=2, num_kv_heads=1, head_dim=64, seed=1)
+    b = Batch(spec, 9, sb=(40, 48), v_scale=v_scale)
+    code, s = (x.copy() for x in ref.unpack(b.v, 64, True))
+    code[:], s[:] = 7, 126
+    b.v = ref.pack(code, s, True)
+    b.q.zero_()
+    got = b.run(rb).double().cpu().numpy()
+    assert (got == 6 * 448 * v_scale).all()
+
+
 def test_more_requests_than_planner_threads(rb):
     """1300 requests, most of one token, some of many and some of none."""
     rng = np.random.default_rng(0)
