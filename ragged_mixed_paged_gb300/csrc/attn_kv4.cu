@@ -448,7 +448,8 @@ __device__ __forceinline__ void rescale(uint32_t col_s, uint32_t col_o, int c0, 
 //
 // A warp's rows take a new reference where their scores of columns [c0, c0 + kCols) exceed the old
 // one: O, the sum and the row's P of the columns before move by a power of two.  Rare, but for a
-// row's first columns.
+// row's first columns.  (All rows at once: each by itself comes here far more often, and a prompt of
+// 8192 tokens takes 606 us instead of 530.)
 template <int HD>
 __device__ __noinline__ float2 move_reference(uint32_t col_s, uint32_t col_o, int c0, int seen,
                                               float scale, bool has_o, float old, float l) {
@@ -658,7 +659,7 @@ __device__ void softmax_kv4(const Kv4Args& g4, Kv4Shared& sh, uint32_t tmem, uin
       ++uc_x;
       tc_x += n;
       tc::fence_after_sync();
-      const float wa = l > 0.f ? g4.v_scale * kv4d::kScaleUnit / l : l * 0.f;  // (NaN stays NaN)
+      const float wa = g4.v_scale * kv4d::kScaleUnit / l;  // (nothing but -inf: 0 / 0)
       uint32_t pk[HD / 2];
 #pragma unroll
       for (int c = 0; c < HD / 32; ++c) {

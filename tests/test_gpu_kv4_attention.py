@@ -404,6 +404,28 @@ def test_not_finite_queries_stay_in_their_rows(rb):
     assert torch.equal(got[~bad], want[~bad])
 
 
+def test_a_row_of_nothing_but_minus_infinity_is_nan(rb):
+    """As softmax of such a row is: its weights are 0 / 0.  The other rows are right."""
+    spec = wl.batch_from_lists([100, 1500, 60], [2, 1, 90], num_q_heads=4, num_kv_heads=1,
+                               head_dim=64, seed=1)
+    b = Batch(spec)
+    code, s = (x.copy() for x in ref.unpack(b.k, 64, False))
+    for i in range(b.R):
+        p = np.arange(b.lens[i])
+        page, off = spec.block_table[i, p // 16], p % 16
+        code[page, off, :, 5] = 3
+        b.keys[i][:] = ref.decode(code[page, off], s[page, off])
+    b.k = ref.pack(code, s, False)
+    rows = np.ones(b.q.shape[:2], bool)
+    for t, h in ((1, 2), (2, 0), (50, 0), (70, 3)):
+        b.q[t, h, 5] = -float("inf")
+        rows[t, h] = False
+    got = b.run(rb)
+    assert bool(torch.isnan(got[torch.from_numpy(~rows).cuda()]).all())
+    with np.errstate(invalid="ignore"):
+        _scaled_check(b, got, rows)
+
+
 def test_captured_with_a_workspace_of_its_own_and_replayed(rb):
     spec = wl.batch_from_lists([300, 60, 9], [1, 90, 1], num_q_heads=8, num_kv_heads=2,
                                head_dim=128, seed=1)
