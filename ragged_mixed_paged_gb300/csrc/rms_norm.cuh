@@ -17,8 +17,6 @@
 
 #include <cuda_fp16.h>
 
-#include <cfloat>
-
 #include "rb_internal.cuh"
 
 namespace rb {
@@ -272,8 +270,14 @@ __global__ void __launch_bounds__(kMost,
       }
       if (!p.any()) continue;
       const float s = top * inv * (1.f / kMax8);
+      float most = top;
+      if (most < 0x1p-100f) {  // (448 / most would pass fp32's range)
+        most *= 0x1p100f;
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) z[i][k] *= 0x1p100f;
+      }
       // codes are 0 where s is, and NaN where s or the value is
-      const float by = s > 0.f && top < INFINITY ? fminf(kMax8 / top, FLT_MAX) : s * 0.f;
+      const float by = s > 0.f && most < INFINITY ? kMax8 / most : s * 0.f;
 #pragma unroll
       for (int k = 0; k < kRun; ++k) z[i][k] *= by;
       const uint2 c = codes8(z[i]);

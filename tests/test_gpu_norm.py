@@ -163,3 +163,19 @@ def test_squares_beyond_fp32(rb):
     assert bool((scales[[0, 2]] == 0).all()) and bool((codes[1].float() == 448).all())
     # 4 + 1e-6 and its root within a few roundings of fp32
     assert (out[1].double() - 2 / (4 + 1e-6) ** 0.5).abs().max().item() <= 8 * U
+
+
+@pytest.mark.parametrize("dtype,group", [("fp32", 0), ("fp32", 64), ("bf16", 0), ("bf16", 128)])
+@pytest.mark.parametrize("gap,offset", [(0, 0), (3, 1)])
+def test_vanishing_rows_in_eight_bits(rb, dtype, group, gap, offset):
+    """Rows and groups of 1e-37 to 1e-33 among ordinary ones: the scale is theirs (an ordinary number of
+    fp32), and the codes fill their range.  Weighted values below 2^-126 are off by 2^-150, which
+    is less than 2^-24 of rows of 1e-37."""
+    x, _, w = _inputs(12, 512, dtype, gap, offset, residual=False)
+    x[:6] *= torch.logspace(-37, -33, 6, device="cuda")[:, None].to(x.dtype)
+    x[7, 128:256] = 0
+    codes, scales = rb.add_rms_norm_fp8(x, w, 1e-6, group=group)
+    assert bool((scales[:6] > 2.0 ** -126).all())
+    _check8(ref.rms_norm(x.double().cpu().numpy(), w.double().cpu().numpy(), 1e-6), codes, scales,
+            group)
+    assert bool((codes[:6].float().abs().amax(1) == 448).all())
