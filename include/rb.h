@@ -101,7 +101,8 @@ typedef enum rb_status {
 #define RB_EBIT_TOKEN_ID 0x8000     /* rb_token_logprobs: token id below -1 or >= vocab_size */
 #define RB_EBIT_LOGITS 0x10000      /* rb_token_logprobs: a row holds NaN or +inf */
 #define RB_EBIT_POSITION 0x20000    /* rb_kv_append, rb_kv4_append: position outside the table */
-#define RB_EBIT_NOT_FINITE 0x40000  /* rb_kv4_append: an appended key or value is NaN or infinite */
+#define RB_EBIT_NOT_FINITE 0x40000  /* rb_kv4_append: an appended key or value is NaN or infinite
+                                       (not on the null page, which takes the padding tokens) */
 
 /* Static sizes of the persistent batch and of one layer's paged KV pool. */
 typedef struct rb_dims {

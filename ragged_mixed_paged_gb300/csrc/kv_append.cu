@@ -27,7 +27,7 @@ struct AppendArgs {
   void *k_cache, *v_cache;
   int32_t* err;
   long long num_slots;
-  int tokens, nh, nkv, hd, rotary, max_position, interleaved;
+  int tokens, nh, nkv, hd, rotary, max_position, interleaved, null_block;
   LayerScale k_scale, v_scale;
 };
 
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, k4 ? 8 : 7) append_kernel(const Appe
                                b / per_head, b % per_head, a.nkv, a.hd);
       }
     }
-    if (odd) raise_error(a.err, RB_EBIT_NOT_FINITE);
+    if (odd && slot / kv4::kPage != a.null_block) raise_error(a.err, RB_EBIT_NOT_FINITE);
   }
 }
 
@@ -358,6 +358,7 @@ rb_status append_setup(const rb_dims* dims, int32_t num_tokens_padded, const rb_
   a.nh = d.num_q_heads;
   a.nkv = d.num_kv_heads;
   a.hd = d.head_dim;
+  a.null_block = d.null_block;
   return RB_OK;
 }
 

@@ -219,6 +219,22 @@ def test_layer_scales_out_of_range(rb, bad):
     assert not kc.any() and not vc.any()
 
 
+def test_padding_tokens_that_are_not_finite_are_not_reported(rb):
+    """Tokens on the reserved page pad a batch: what they hold is no error.  Elsewhere it is."""
+    for null in (0, 3):
+        d = _dims(rb, 2, 1, 64, null_block=null)
+        c = Case(rb, d, 6)
+        c.slots = np.array([17, 40, 16 * null, 16 * null, 16 * null + 5, -1], np.int32)
+        for t in (c.k, c.v):
+            t[2], t[3, 0, 5], t[4], t[5] = float("nan"), float("inf"), float("nan"), float("nan")
+        kc, vc = rb.kv4_cache(d)
+        rb.kv4_append(d, None, c.k, c.v, k_cache=kc, v_cache=vc, **c.args())
+        assert int(c.err.item()) == 0
+        c.v[1, 0, 63] = float("nan")
+        rb.kv4_append(d, None, c.k, c.v, k_cache=kc, v_cache=vc, **c.args())
+        assert int(c.err.item()) == rb.EBIT_NOT_FINITE
+
+
 @pytest.mark.parametrize("four", [False, True])
 def test_tokens_left_out(rb, four):
     """A position outside the table leaves its token out, a slot outside the pool its K and V."""
