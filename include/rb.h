@@ -830,7 +830,7 @@ rb_status rb_kv4_read(const rb_dims* dims, int32_t num_rows, const int32_t* d_sl
  * Arguments, layouts, workspace (rb_paged_attention_workspace_size), supported shapes and errors are
  * those of rb_paged_attention, with caches [num_blocks, nkv, 9 * hd] of bytes; RB_ERR_INVALID_ARG
  * also for a softmax_scale that is not positive, a layer scale outside [2^-100, 2^100] and a product
- * of softmax_scale and k_scale that fp32 does not hold; RB_ERR_CAPACITY also for more than 32768
+ * of softmax_scale and k_scale that is no ordinary fp32 number; RB_ERR_CAPACITY also for more than 32768
  * requests, 2^31 kernel pages in their block-table rows or num_tokens of 2^17 * floor(128 * nkv / nh)
  * and more.  What pages hold behind a request's last token does not reach its rows.
  */

@@ -27,6 +27,8 @@
 // turned).  Measured against it: an issuer thread for each side 568; that, and steps of 64 keys with
 // S of the next one ahead, 592 (an MMA of 64 columns takes as long as one of 128, which reads as
 // much of A); two threads a row, all softmax warps on one side's tile at a time, 596 (ex2 bound).
+#include <cfloat>
+
 #include "attn_kv4_decode.cuh"
 #include "attn_kv4_plan.cuh"
 #include "attn_prefill_tc.cuh"
@@ -837,8 +839,8 @@ extern "C" rb_status rb_paged_attention_kv4(
   AttnArgs& a = su.a;
   const float scale = softmax_scale * k_scale * 1.4426950408889634f;
   if (!(softmax_scale > 0.f) || !kv4::layer_scale_ok(k_scale) || !kv4::layer_scale_ok(v_scale) ||
-      !std::isfinite(scale * kv4d::kScaleUnit) || !(scale > 0.f))
-    return RB_ERR_INVALID_ARG;
+      !std::isfinite(scale * kv4d::kScaleUnit) || !(softmax_scale * k_scale >= FLT_MIN))
+    return RB_ERR_INVALID_ARG;  // (a subnormal product has lost bits)
   // the units' list holds 16 bits of request and 16 of tile pair, the decode stream 31 of pages
   if (a.R > 32768 || a.N / (2 * a.tile_tokens) > 65535 || a.R * a.kp_cap > 0x7fffffffLL)
     return RB_ERR_CAPACITY;

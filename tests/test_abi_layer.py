@@ -105,6 +105,15 @@ def test_attention_host_checks(lib):  # noqa: F811
     assert call(d=wide, reqs=1, tokens=1 << 20, padded=1 << 20) == 2
 
 
+def test_attention_refuses_a_product_of_scales_that_loses_bits(lib):  # noqa: F811
+    def call(scale, ks):
+        return lib.lib.rb_paged_attention_kv4(
+            ctypes.byref(_dims(lib)), 2, 3, 4, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, scale, ks, 1.0,
+            FAKE, FAKE, 1 << 40, None, None)
+
+    assert call(1e-9, 1e-30) == 1 and call(1e-20, 1e-30) == 1  # subnormal, 0
+
+
 def test_norm_host_checks(lib):  # noqa: F811
     ODD = ctypes.c_void_p(0x100001)
 
