@@ -354,6 +354,27 @@ def test_rows_claimed_again_and_again_are_reported(rb):
         assert int(err.item()) == rb.EBIT_ATTN_META
 
 
+def test_no_list_of_rows_claimed_again_and_again(rb):
+    """32 requests that claim all 256 rows are 512 pairs of tiles, the list holds 81: nothing is
+    written behind it, and no row of the output."""
+    d = rb.Dims(16, 16, 1, 64, max_num_reqs=64, max_model_len=256, max_blocks_per_req=16,
+                num_blocks=20)
+    k, v = rb.kv4_cache(d)
+    q = torch.ones(256, 16, 64, dtype=BF, device="cuda")
+    table = torch.ones(64, 16, dtype=torch.int32, device="cuda")
+    loc = torch.tensor([0, 256] * 32 + [0], dtype=torch.int32, device="cuda")
+    lens = torch.full((64,), 256, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 7.0)
+    ws = torch.full((rb.workspace_size(d, 64, 256),), 0x5a, dtype=torch.uint8, device="cuda")
+    rb.paged_attention_kv4(d, 64, 256, q, k, v, table, loc, lens, out=out, workspace=ws,
+                           error_word=err)
+    assert int(err.item()) == rb.EBIT_ATTN_META
+    # header, two lists of offsets (65 words each), 64 counters, the list itself, in 256-byte pieces
+    start = 256 + 2 * 512 + 256 + 512
+    assert bool((ws[start:] == 0x5a).all()) and bool((out == 7).all())
+
+
 def test_empty_batches(rb):
     d = rb.Dims(16, 4, 2, 64, max_num_reqs=3, max_model_len=64, max_blocks_per_req=4, num_blocks=8)
     k, v = rb.kv4_cache(d)
