@@ -805,7 +805,7 @@ rb_status rb_kv_append(const rb_dims* dims, int32_t num_tokens_padded,
  * An infinity is held as the largest value, NaN as 0.
  * Errors: as rb_kv_append, RB_ERR_UNSUPPORTED for another block_size or head_dim and for nkv * hd
  * above 24576, RB_ERR_INVALID_ARG for a layer scale outside [2^-100, 2^100]; device -> also
- * NOT_FINITE.
+ * NOT_FINITE (not for tokens on the null page).
  */
 rb_status rb_kv4_append(const rb_dims* dims, int32_t num_tokens_padded,
                         const rb_rotation* rotation, const int32_t* d_positions, const void* d_q,
@@ -832,7 +832,8 @@ rb_status rb_kv4_read(const rb_dims* dims, int32_t num_rows, const int32_t* d_sl
  * also for a softmax_scale that is not positive, a layer scale outside [2^-100, 2^100] and a product
  * of softmax_scale and k_scale that is no ordinary fp32 number; RB_ERR_CAPACITY also for more than 32768
  * requests, 2^31 kernel pages in their block-table rows or num_tokens of 2^17 * floor(128 * nkv / nh)
- * and more.  What pages hold behind a request's last token does not reach its rows.
+ * and more.  What pages hold behind a request's last token does not reach its rows.  A row of q with
+ * NaN or an infinity is NaN; scores of any size are taken with the bits that fp32 has for them.
  */
 rb_status rb_paged_attention_kv4(const rb_dims* dims, int32_t num_reqs, int32_t num_tokens,
                                  int32_t num_tokens_padded, const void* d_q,
@@ -848,7 +849,9 @@ rb_status rb_paged_attention_kv4(const rb_dims* dims, int32_t num_reqs, int32_t 
  *   y = r / sqrt(mean(r^2) + eps) * weight            (fp32)
  * written as y in the rows' type (out_dtype = dtype, d_scales NULL) or in 8 bits (out_dtype
  * RB_E4M3): s = max |y| / 448 over the row (group_size 0) or over each group_size neighbouring
- * values, out = the e4m3 number nearest to y / s (0 where s is 0).
+ * values, out = y / s in e4m3 (0 where s is 0), taken as z (448 / max |z|) with z = r weight: z, the
+ * quotient and the product each rounded to fp32, then to the nearest number, ties to even.  Within those
+ * roundings of a tie it may be the neighbour of the number nearest to y / s.
  *
  *   d_x, d_residual, d_residual_out  [num_rows, hidden_size] of dtype (RB_BF16, RB_FP16, RB_FP32),
  *                rows *_stride values apart (at least hidden_size); residual and residual_out
@@ -859,9 +862,12 @@ rb_status rb_paged_attention_kv4(const rb_dims* dims, int32_t num_reqs, int32_t 
  *   d_scales     [num_rows, hidden_size / group_size] fp32 ([num_rows, 1] for group_size 0)
  * Any alignment of whole elements; rows of 16-byte alignment are read and written 16 bytes at a
  * time.  hidden_size up to 32768; group_size 0, 16, 32, 64, 128 or 256, a divisor of hidden_size.
- * Squares and their mean are fp32: where they overflow (values of 1e19) the row is 0.
+ * Squares and their mean are fp32: where they overflow (values of 1e19) the row is 0; where they
+ * fall below its ordinary numbers (values of 1e-19 and less) and eps does not cover them, y loses bits
+ * and in the end is infinite or NaN.  In 8 bits z is an fp32 number too: where it overflows, the values
+ * of its scale are NaN, below 1e-38 it loses bits, and so does s.
  * A NaN makes its row NaN; an infinity becomes NaN (in 8 bits, with the values that share its scale)
- * and the rest of its row 0.
+ * and the rest of its row 0.  A NaN of the weight is one in its column alone, and left out of s.
  * Errors: host -> RB_ERR_INVALID_ARG, RB_ERR_UNSUPPORTED.
  */
 rb_status rb_add_rms_norm(int32_t num_rows, int32_t hidden_size, int32_t dtype, const void* d_x,

@@ -23,8 +23,8 @@
 // What bounds a prefill unit: the chain of a side's steps.  A key tile takes 4400 cycles: softmax
 // 1850 (1024 of them ex2's rate for a row a thread), P V and the next S 1370 at the tensor core's
 // rate, the rest notices between the roles; the two sides in turn keep the tensor pipe at 0.53 of
-// its rate.  A prompt of 8192 tokens, 32 + 8 heads of 128: 536 us (1.02 PFLOP/s; 433 if nothing were
-// turned).  Measured against it: an issuer thread for each side 568; that, and steps of 64 keys with
+// its rate.  A prompt of 8192 tokens, 32 + 8 heads of 128: 530 us (1.04 PFLOP/s).  Measured when it took
+// 536: 433 if nothing were turned; an issuer thread for each side 568; that, and steps of 64 keys with
 // S of the next one ahead, 592 (an MMA of 64 columns takes as long as one of 128, which reads as
 // much of A); two threads a row, all softmax warps on one side's tile at a time, 596 (ex2 bound).
 #include <cfloat>
@@ -306,7 +306,7 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t phase) {
 // threads make them visible to the tensor core (a proxy fence) and then arrive: the issuer's waits for
 // them acquire, so that its MMAs come after those stores.  P and O are in tensor memory, whose
 // accesses tcgen05.fence::after_thread_sync orders behind a relaxed wait.  (A prompt of 8192 tokens:
-// 536 us, 538 with P tested first, 542 with relaxed tests and one acquiring fence a step.)
+// 536 us then, 538 with P tested first, 542 with relaxed tests and one acquiring fence a step.)
 template <int HD>
 __device__ void mma_issuer4(const AttnArgs& a, Kv4Shared& sh, uint32_t tmem, uint32_t smem_base) {
   using C = TcCfg<HD>;

@@ -23,11 +23,14 @@
 // A lane so ends up with hd / 8 neighbouring values of two columns of the output.
 //
 // Two pages a step: their chains of MMAs and exponentials overlap, and the tests of a step are made
-// once for both (256 decodes of 0.5 to 8 k 175 us with one, 167 with two).
+// once for both (256 decodes of 0.5 to 8 k 175 us with one, 171 with two, when that was the change).
+// Where a segment (the pages of one head that a warp has) is odd, its last step takes one page twice,
+// the second time unseen.
 //
 // What bounds it: instruction issue.  A page costs about 340 instructions a warp (hd 128), 310 cycles
 // on the pipe of conversions, masks and shifts (64 conversions a lane, two cycles each); issue
-// slots are at 0.65, the pipe at 0.55 (256 decodes of 4000 tokens: 5.2 TB/s, 0.77 of the copy rate).
+// slots are at 0.63, the pipe at 0.54 (256 decodes of 4000 tokens: 224 us, 5.3 TB/s, 0.78 of the copy
+// rate).  All 128 registers are taken; 44 bytes are spilled for heads of 128.
 // A ring of 4, 5 or 6 pages makes no difference.
 #pragma once
 

@@ -7,12 +7,15 @@ namespace rb {
 namespace attn {
 
 // Finish-time model (this GPU, cold caches, heads of 128; fitted to whole-launch times): a CTA
-// decodes 14.5 pages of one kv head a microsecond, a prefill unit of n key tiles takes 6 + 2.4 n.
+// decodes 14.5 pages of one kv head a microsecond (twice as many of heads of 64), a prefill unit of n
+// key tiles takes 6 + 2.4 n, whatever its heads and whether it has one side or two.  It divides the CTAs,
+// so that what it is off by costs time alone.
 constexpr float kKv4PagesPerUs = 14.5f, kKv4UnitUs = 6.f, kKv4TileUs = 2.4f;
 // Pages of a decode warp: at least kMinPages (64 decodes of 100 to 500 tokens: 25 us, 29 with 4), and
 // enough that a (request, kv head)'s pieces cost no more to merge than its pages take
-// (attn_plan.cuh's rule for splits); an even number, because a step takes two (24 decodes of 4000
-// tokens, 20 pages a warp instead of 19.7: 58 -> 46 us).
+// (attn_plan.cuh's rule for splits); an even number, because a step takes two.  It sets the count of
+// warps, over which the stream is cut in equal parts: they are even where it divides (24 decodes of
+// 4000 tokens, 20 pages a warp instead of 19.7: 58 -> 46 us), near it elsewhere.
 constexpr int kKv4MinPages = 6;
 
 // Rows of padding tokens are written as zeros, by every CTA that calls this.
@@ -149,8 +152,8 @@ __device__ __forceinline__ void kv4_plan_body(const AttnArgs& a, int head_dim, i
     if (work > 0) {
       // Both kinds together take (their SM time) / ctas, or the longest unit.  The decode CTAs then
       // go on with prefill units, the shortest ones by then, so they are to be done with their own
-      // after 3/4 of that (flat: 1/2 to 19/20 give the large mix 425 to 431 us, other mixes 166 to
-      // 176 and 869 to 884).
+      // after 3/4 of that (flat: 1/2 to 19/20 gave the large mix, now 411 us, 425 to 431 when it was
+      // fitted, other mixes 166 to 176 and 869 to 884).
       const float scale = static_cast<float>(head_dim) / 128.f;
       const float dec = static_cast<float>(work) * scale / kKv4PagesPerUs;
       const float pre = (kKv4UnitUs * total_pairs + kKv4TileUs * s_pre_tiles) * a.nkv;

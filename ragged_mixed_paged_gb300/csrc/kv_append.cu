@@ -129,7 +129,7 @@ __device__ __forceinline__ bool put_block(const uint4& a, const uint4& b, const 
 // The 16-bit cache is HBM's: 16384 tokens of 32 + 16 heads of 128, 403 MB, take 66 us (seven CTAs an
 // SM; six 70, five 77).  The 4-bit one has the codes' arithmetic as well, about 110 instructions a
 // block, and the latency of a CTA's steps: slot, table, keys, codes (issue slots 0.63).  8192 tokens of
-// 32 + 16 heads, 177 MB, take 35 us alone.  With the read of their rows behind them they take 52 with
+// 32 + 16 heads, 177 MB, take 38 us alone.  With the read of their rows behind them they take 51 with
 // eight CTAs an SM (64 registers, two heads at a time), 58 with six and four heads at a time, and
 // 68 where a thread codes its own halves of two blocks after a shuffle, without shared memory.
 template <bool k4, int kBatch>
@@ -252,7 +252,9 @@ rb_status launch_append(const AppendArgs& a, size_t smem, cudaStream_t s) {
   return RB_OK;
 }
 
-// A thread per block of sixteen values of K or V: nine bytes in, thirty-two out.
+// A thread per block of sixteen values of K and of V: nine bytes in, thirty-two out, in two stores
+// that each fill half of their sectors.  8192 rows of 8 heads of 128, 43 MB, take 17 us cold (floor
+// 6.3): three dependent loads (slot, codes, scale) and two divisions a block, and those stores.
 template <bool kValues>
 __device__ __forceinline__ void read_block(const uint8_t* cache, int slot, int head, int block,
                                            int nkv, int hd, float scale, uint4* dst) {

@@ -299,9 +299,16 @@ __global__ void __launch_bounds__(kMost,
 }
 
 // Two runs a thread, in whole warps, up to a CTA of 1024 (four beyond).  For rows of whole aligned
-// runs a count of warps that is a power of two is compiled in (8192 x 4096 bf16 into 8 bits: 44 us
-// against 49); four runs on half the threads take 54 there, persistent CTAs that load the next row
-// ahead 65.
+// runs a count of warps that is a power of two is compiled in (8192 x 4096 bf16 into 8 bits, cold: 36 us
+// against 38).  Four runs on half the threads are equal there, and 2047 x 5120 fp16 in groups takes
+// 21.6 instead of 19.6; persistent CTAs that load the next row ahead took 65 where this took 44.
+// Rows that are not whole aligned runs go one value at a time: 8192 x 4096 bf16, rows 4157 apart,
+// 71 us instead of 40, into 8 bits 75 instead of 36.
+//
+// Four runs are held in the 64 registers that a CTA of 1024 leaves: above 16384 values fp32 rows spill
+// 112 to 292 bytes a thread (1024 x 32768 fp32 124 us, 0.64 of the copy rate; bf16, 16 at most, 0.75).
+// Unaligned fp16 and bf16 rows of up to 8192 values spill 4 to 52 bytes in the 40 registers of their
+// three CTAs an SM.
 template <class T, int kOut>
 rb_status launch_norm(const NormArgs& a, cudaStream_t s) {
   const int runs = (a.hidden + kRun - 1) / kRun;

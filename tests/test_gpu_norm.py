@@ -152,6 +152,21 @@ def test_refusals(rb):
     assert rb.add_rms_norm(x[:0], w).shape == (0, 256)
 
 
+@pytest.mark.parametrize("group", [0, 64])
+def test_a_weight_that_is_nan_stays_in_its_column(rb, group):
+    x, _, w = _inputs(5, 256, "bf16", residual=False)
+    w[70] = float("nan")
+    rest = torch.arange(256, device="cuda") != 70
+    out = rb.add_rms_norm(x, w)
+    codes, scales = rb.add_rms_norm_fp8(x, w, group=group)
+    assert bool(torch.isnan(out[:, 70]).all()) and bool(torch.isnan(codes.float()[:, 70]).all())
+    assert not bool(torch.isnan(out[:, rest]).any()) and bool(torch.isfinite(scales).all())
+    w[70] = 0
+    want, want_scales = rb.add_rms_norm_fp8(x, w, group=group)
+    assert torch.equal(codes.float()[:, rest], want.float()[:, rest])
+    assert torch.equal(scales, want_scales)
+
+
 def test_squares_beyond_fp32(rb):
     """Rows whose squares overflow are 0, the others are as ever."""
     x = torch.full((3, 256), 1e25, device="cuda")
