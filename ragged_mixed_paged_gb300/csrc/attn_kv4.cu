@@ -427,7 +427,8 @@ __device__ __forceinline__ void store_weights(uint32_t at, const uint32_t (&p)[k
 }
 
 // O (if it holds anything: S of this tile, issued after the tiles before, has landed) and P of the
-// tile's columns before c0, times alpha (in fp32: it may be below fp16's range).
+// tile's columns before c0, times alpha (in fp32: it may be below fp16's range).  The stores have
+// landed when it returns: it may be called again for the same tile.
 template <int HD>
 __device__ __forceinline__ void rescale(uint32_t col_s, uint32_t col_o, int c0, bool has_o,
                                         float alpha) {
@@ -455,6 +456,7 @@ __device__ __forceinline__ void rescale(uint32_t col_s, uint32_t col_o, int c0, 
     }
     tc::st16(col_s + c, r);
   }
+  tc::wait_st();
 }
 
 // The two functions below are out of line.  They take a row's reference and sum by value and return
@@ -483,7 +485,6 @@ __device__ __noinline__ float2 move_reference(uint32_t col_s, uint32_t col_o, in
   const float next = fmaxf(old, ceilf(top * scale));
   const float alpha = next > old ? fast_exp2(old - next) : 1.f;
   rescale<HD>(col_s, col_o, c0, has_o, alpha);
-  tc::wait_st();
   return make_float2(next, l * alpha);
 }
 

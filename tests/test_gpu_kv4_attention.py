@@ -294,6 +294,29 @@ def test_values_of_the_largest_size_in_many_pieces(rb, c, v_scale):
     assert (got == 6 * 448 * v_scale).all()
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("top", [3e4, 1e7, 1e12])
+def test_references_that_move_in_every_part_of_a_tile(rb, hd, top):
+    """Scores that rise every few keys by far more than a reference bears: O and P of a tile's earlier
+    columns are moved several times a tile, and a row is the mean of its last keys."""
+    spec = wl.batch_from_lists([1500, 900], [1, 600], num_q_heads=4, num_kv_heads=2, head_dim=hd,
+                               seed=2)
+    b = Batch(spec, 4, sb=(40, 48))
+    code, s = (x.copy() for x in ref.unpack(b.k, hd, False))
+    for i in range(2):
+        p = np.arange(b.lens[i])
+        page, off = spec.block_table[i, p // 16], p % 16
+        code[page, off] = 2
+        s[page, off] = (p * 80 // b.lens[i] + 8)[:, None, None]
+        b.keys[i][:] = ref.decode(code[page, off], s[page, off])
+    b.k = ref.pack(code, s, False)
+    b.q = torch.full_like(b.q, top / hd)
+    want = b.run(rb)
+    _scaled_check(b, want)
+    for _ in range(10):
+        assert torch.equal(b.run(rb), want)
+
+
 def test_more_requests_than_planner_threads(rb):
     """1300 requests, most of one token, some of many and some of none."""
     rng = np.random.default_rng(0)
