@@ -63,11 +63,11 @@ FLUSH_BYTES = 512 << 20
 # its planner's code, comments left out): a figure is reported only while the code is the code
 # it was measured on.
 KNOWN_TRAFFIC = {
-    (2, "243f94e4ec9aae15"): 78989568 + 3869184,
-    (3, "243f94e4ec9aae15"): 4545406720 + 26100736,
+    (2, "7f23da8dca2f316c"): 79012352 + 3830272,
+    (3, "7f23da8dca2f316c"): 4545521152 + 25990144,
     # the stream: mean over the launches of stream steps 5..99 (the default timed steps)
-    (4, "243f94e4ec9aae15"): 9543039138 + 80848678,
-    (5, "243f94e4ec9aae15"): 6940740608 + 114152448,
+    (4, "7f23da8dca2f316c"): 9559010336 + 80872909,
+    (5, "7f23da8dca2f316c"): 7199145472 + 114155008,
 }
 
 WORKLOAD_NAMES = {1: "pages' worked example A/B/C", 2: "pages' padding example",

@@ -289,19 +289,6 @@ __device__ void producer_q4(const AttnArgs& a, Kv4Shared& sh, uint32_t smem_base
   __syncwarp();
 }
 
-// Non-blocking test of a phase, acquiring (mbar_test_relaxed is the other one).
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t phase) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(phase)
-      : "memory");
-  return ok != 0;
-}
-
 // The MMA issuer (one thread).  Q, K and V are written to shared memory by ordinary stores, whose
 // threads make them visible to the tensor core (a proxy fence) and then arrive: the issuer's waits for
 // them acquire, so that its MMAs come after those stores.  P and O are in tensor memory, whose

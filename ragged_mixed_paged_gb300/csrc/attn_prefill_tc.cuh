@@ -463,13 +463,18 @@ __device__ void mma_issuer(const AttnArgs& a, TcShared<kScored>& sh, uint32_t tm
   // tcgen05.fence::after_thread_sync before the MMAs that read it, so the waits are relaxed: an
   // acquiring try_wait behind queued MMAs left the tensor pipe idle ~140 cycles per wait on this
   // GPU, a relaxed one costs nothing.  The unit descriptor is plain shared memory written by the
-  // producer warp: its barrier keeps the acquiring wait.
+  // producer warp: its barrier keeps the acquiring wait.  So does P's of a scored launch, whose
+  // softmax warps write to the tile's V as well (attn_scored_tc.cu).
   auto wait = [&](uint64_t* bar, uint32_t phase) { return tc_wait<true>(bar, phase, abort, a); };
+  auto wait_p = [&](uint64_t* bar, uint32_t phase) { return tc_wait<!kScored>(bar, phase, abort, a); };
   // A wait whose result decides a branch costs the issuing thread a few hundred cycles even when
   // the phase is long complete; so every barrier of one step is first tested at once (the tests
   // issue back to back, one branch on their conjunction) and only a step that finds one not yet
   // complete takes the bounded waits one by one.
   auto test = [](uint64_t* bar, uint32_t phase) { return mbar_test_relaxed(bar, phase); };
+  auto test_p = [](uint64_t* bar, uint32_t phase) {
+    return kScored ? mbar_test(bar, phase) : mbar_test_relaxed(bar, phase);
+  };
   // Shared-memory descriptors are built once: a k-step moves the start address by 32 bytes
   // within a 128-byte swizzle atom, a 64-dim half by a half tile, a stage or a Q tile by whole
   // tiles.  All of these only add to the address field in the descriptor's low word (which no
@@ -534,9 +539,9 @@ __device__ void mma_issuer(const AttnArgs& a, TcShared<kScored>& sh, uint32_t tm
                        ph_o = (ucount[x] - 1) & 1, ph_k = ((kt + 1) / C::kStagesK) & 1;
         uint64_t* bar_v = &sh.v_full[kt % C::kStagesV];
         uint64_t* bar_k = &sh.k_full[(kt + 1) % C::kStagesK];
-        const bool ready = test(&sh.p_full[x], ph_p) & (!need_v || test(bar_v, ph_v)) &
+        const bool ready = test_p(&sh.p_full[x], ph_p) & (!need_v || test(bar_v, ph_v)) &
                            (!need_o || test(&sh.o_free[x], ph_o)) & (!need_k || test(bar_k, ph_k));
-        if (!ready && (!wait(&sh.p_full[x], ph_p) || (need_v && !wait(bar_v, ph_v)) ||
+        if (!ready && (!wait_p(&sh.p_full[x], ph_p) || (need_v && !wait(bar_v, ph_v)) ||
                        (need_o && !wait(&sh.o_free[x], ph_o)) || (need_k && !wait(bar_k, ph_k)))) {
           ok = false;
           break;

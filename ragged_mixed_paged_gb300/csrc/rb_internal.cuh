@@ -157,7 +157,19 @@ __device__ __forceinline__ void st_global_v8(void* p, uint32_t r0, uint32_t r1, 
                : "memory");
 }
 
-// Non-blocking test of a phase, relaxed (see mbar_try_wait_relaxed).  Several of these issued
+// Non-blocking test of a phase.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t phase) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(phase)
+      : "memory");
+  return ok != 0;
+}
+// The same, relaxed (see mbar_try_wait_relaxed).  Several of these issued
 // back to back, their results combined before one branch, overlap their latencies.
 __device__ __forceinline__ bool mbar_test_relaxed(uint64_t* bar, uint32_t phase) {
   uint32_t ok;

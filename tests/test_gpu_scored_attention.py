@@ -362,6 +362,25 @@ def test_infinities_and_nan_stay_with_the_rows_that_see_them(rb, nh, nkv, hd, ki
         assert bool(finite.any())
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+def test_tiles_whose_values_are_taken_out_again_and_again(rb, hd):
+    """Windows with infinities in V of every tile, which the softmax warps take out of the staged
+    tiles before the MMAs read them: the rows that see none are finite, and every run's bits agree."""
+    spec = wl.batch_from_lists([1200, 0], [500, 900], num_q_heads=8, num_kv_heads=2, head_dim=hd,
+                               seed=hd)
+    tens = wl.make_tensors(spec, device="cuda")
+    for v in [*tens.hist_v, tens.v]:
+        v[50::97, :, 3] = float("inf")
+    wl.place_history(spec, tens.hist_v, tens.v_cache)
+    rules = dict(key_start=_positions(spec) - 40)
+    want, args, r, _ = _check(rb, spec, tens=tens, **rules)
+    finite = torch.isfinite(want.float()).flatten(1).all(1)
+    assert bool(finite.any()) and not bool(finite.all())
+    for _ in range(30):
+        got = rb.paged_attention_scored(*args, r)
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
 def test_a_step_without_requests_writes_padding_only(rb):
     spec = wl.batch_from_lists([5], [3], num_q_heads=4, num_kv_heads=2, head_dim=128, seed=1)
     tens, _ = _setup(rb, spec)
